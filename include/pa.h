@@ -53,13 +53,18 @@ typedef enum pa_status {
   PA_ERR_TIMEOUT = 7         /* a bounded device wait gave up (see pa_get_device_error) */
 } pa_status;
 
-typedef enum pa_dtype { PA_BF16 = 0, PA_FP32 = 1 } pa_dtype;
+typedef enum pa_dtype {
+  PA_BF16 = 0,
+  PA_FP32 = 1,
+  PA_FP4 = 2 /* a 4-bit pool: only for the pa_*_fp4 calls and the block copies */
+} pa_dtype;
 
 /* Bits of the device error word. */
 #define PA_DEVERR_SLOT 0x1u        /* reshape_and_cache: slot >= num_blocks * block_size */
 #define PA_DEVERR_BLOCK_ID 0x2u    /* decode / copy_blocks: block id outside [0, num_blocks) */
 #define PA_DEVERR_SEQ_LEN 0x4u     /* decode: seq_len > max_seq_len or > table capacity */
 #define PA_DEVERR_TIMEOUT 0x8u     /* a pipeline wait exceeded its limit (about 2 s by default) */
+#define PA_DEVERR_BLOCKS 0x10u     /* extend_tables: the free list holds fewer blocks than needed */
 
 /* partition_size of pa_decode: the stage-balanced split (see pa_decode). */
 #define PA_PARTITION_BALANCED (-2)
@@ -71,7 +76,7 @@ typedef struct pa_cache_desc {
   int32_t num_kv_heads;  /* KV heads, >= 1 */
   int32_t head_size;     /* elements per head: 64, 128 or 256 */
   int32_t dtype;         /* pa_dtype */
-} pa_cache_desc;
+} pa_cache_desc;             /* PA_FP4: block_size a power of two in [8, 256] */
 
 /* ---------------------------------------------------------------------------
  * Cache write.  Each new token's key and value go to the physical slot that
@@ -380,6 +385,135 @@ pa_status pa_decode_no_alloc(void* out, const void* query, const void* cache,
                              int32_t max_blocks_per_seq, const int32_t* seq_lens,
                              int32_t num_seqs, int32_t num_heads, float scale,
                              int32_t max_seq_len, int32_t partition_size, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit pool (pa_cache_desc.dtype = PA_FP4).  The pages store 16-bit
+ * caches and size the pool by its bytes (studying-code.tistory.com/16: the
+ * cache of one token of OPT-13B takes 800 KB); a 4-bit pool holds 3.6 times
+ * the tokens in the same memory and is read in as much less time.
+ *
+ * A key or value is held as an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4 or 6, and a
+ * sign bit); 16 consecutive elements of one token's head share an e4m3 scale,
+ * and the pool's keys and its values each have a tensor scale, a power of two
+ * in [2^-32, 2^32] that the caller passes with every call:
+ *     x = code * scale * tensor_scale,
+ * which is exact in bf16 and fp32.  The buffer is
+ *     uint8 cache[num_blocks][num_kv_heads][block_size / 8][9 * head_size],
+ * 16-byte aligned; its last axis is a tile of eight tokens (D = head_size):
+ *     [8 tokens][D / 2]       key codes, the even element in the low nibble
+ *     [D / 16][8 tokens][8]   value codes, by groups of 16 elements
+ *     [8 tokens][D / 16]      key scales
+ *     [D / 16][8 tokens]      value scales
+ * so that a block's keys and values of one head are one contiguous range.
+ * Slots, block tables and the host pool are those of the other pools;
+ * pa_copy_blocks and pa_swap_blocks take 4-bit pools as well.
+ * head_size is 64, 128 or 256 (else PA_ERR_UNSUPPORTED).  `dtype` of a call is
+ * the element type (PA_BF16 or PA_FP32) of its keys, values, queries and
+ * outputs; arithmetic is fp32 or exact.
+ *
+ * pa_reshape_and_cache_fp4 writes new tokens: per group of 16,
+ *     scale = e4m3(max |x| / 6 / tensor_scale), at most 448,
+ *     code  = e2m1(x / (scale * tensor_scale)),
+ * both the nearest number, ties to even, magnitudes past 6 to 6 (decided on
+ * the exact quotients).  A group whose scale rounds to zero becomes zero; a
+ * group with a NaN becomes NaN; an infinity becomes the largest number.
+ *   key, value    device, [num_tokens] rows of [num_kv_heads][head_size]
+ *                 elements, key_stride / value_stride elements apart (the
+ *                 rows of a fused projection's output, say); pointers and
+ *                 strides are multiples of 16 bytes.
+ *   slot_mapping  as in pa_reshape_and_cache: negative slots are padding, a
+ *                 slot past the pool is skipped and records PA_DEVERR_SLOT.
+ *
+ * pa_gather_cache_fp4 reads tokens back: key / value [num_tokens]
+ * [num_kv_heads][head_size], contiguous, 16-byte aligned, receive the numbers
+ * that the slots hold (a prompt chunk's attention over its cached prefix
+ * needs them).  Rows of negative slots are left as they were, and so are rows
+ * of slots past the pool, which record PA_DEVERR_SLOT.  A slot may repeat.
+ * num_tokens == 0 is a no-op for both.
+ * ------------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_fp4(void* cache, const pa_cache_desc* desc, const void* key,
+                                   const void* value, int32_t dtype, int64_t key_stride,
+                                   int64_t value_stride, const int64_t* slot_mapping,
+                                   int32_t num_tokens, float key_scale, float value_scale,
+                                   void* stream);
+pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void* cache,
+                              const pa_cache_desc* desc, const int64_t* slot_mapping,
+                              int32_t num_tokens, float key_scale, float value_scale,
+                              void* stream);
+
+/* Decode attention over a 4-bit pool: pa_decode's operation on the numbers
+ * that the pool holds.
+ *   out    device, [num_seqs][num_heads][head_size] of `dtype`, contiguous.
+ *   query  device, [num_seqs] rows of [num_heads][head_size] of `dtype`,
+ *          query_stride elements apart; pointer and stride are multiples of
+ *          16 bytes, and so is `out`.
+ * Tables, lengths, scale and their errors are pa_decode's: a length of 0
+ * gives zero rows, a length past the table's row records PA_DEVERR_SEQ_LEN and
+ * leaves its rows undefined, an id outside the pool records
+ * PA_DEVERR_BLOCK_ID and its tokens count as zero keys and values.  What the
+ * pool holds past a sequence's end (NaN scales among it) is never used.
+ * Groups of num_heads / num_kv_heads <= 16.  No bound on the lengths is
+ * needed: the launch depends on the shapes alone, so that a captured call
+ * serves sequences as they grow.  Weights of the values enter their product
+ * rounded to fp16 for bf16 outputs (relative 2^-11; a bf16 output has 2^-8), in
+ * two fp16 parts for fp32 outputs; queries likewise (bf16 queries are exact).
+ *   workspace  device scratch of pa_decode_fp4_workspace_size bytes, 256-byte
+ *              aligned, zeroed once at allocation; every call leaves its
+ *              counters zero.  Calls that overlap on the GPU need separate
+ *              workspaces. */
+pa_status pa_decode_fp4_workspace_size(const pa_cache_desc* desc, int32_t num_heads,
+                                       size_t* bytes);
+pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t query_stride,
+                        const void* cache, const pa_cache_desc* desc, float key_scale,
+                        float value_scale, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                        int32_t num_heads, float scale, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Block tables, slot map and positions on the device, from request lengths
+ * (tech.blogsailing.com/?p=100, section 2; itan.pw page, section
+ * "ブロック割当のロジック"): the step's bookkeeping without the host, so that a
+ * captured step advances by itself.  Request r (a row of the tables) holds
+ * seq_lens[r] tokens in its first ceil(seq_lens[r] / block_size) entries and
+ * gets new_tokens[r] >= 0 more.  The blocks that it then lacks come from the
+ * front of a ring of free blocks, requests in order, each request's in the
+ * order of its tokens (the order in which pa_pool_append_tokens hands blocks
+ * of unshared sequences out); token i of request r goes to
+ *     position p = seq_lens[r] + i,
+ *     slot block_tables[r][p / block_size] * block_size + p % block_size.
+ *   block_tables   device int32 [num_seqs][max_blocks_per_seq], in/out: new
+ *                  entries are written, the others stay.
+ *   seq_lens       device int32 [num_seqs]; new_tokens device int32 [num_seqs].
+ *   free_blocks    device int32 [free_capacity], the ring; free_state device
+ *                  int32 [2]: the place of its front, and how many blocks it
+ *                  holds.  Both NULL (free_capacity 0): every block is in the
+ *                  tables already, as a host pool filled them.
+ *   seq_lens_out, free_state_out   the state after the step; each may be its
+ *                  input (in place), or other memory.
+ *   slot_mapping   device int64 [max_tokens]: the tokens' slots, request after
+ *                  request, then -1 up to max_tokens (padding, which the cache
+ *                  writes skip).
+ *   positions      device int32 [max_tokens] or NULL: the tokens' positions,
+ *                  then -1.
+ *   token_starts   device int32 [num_seqs + 1] or NULL: the first token of
+ *                  every request, and their number at the end.
+ * All or nothing: a negative length or count, more tokens than max_tokens or a
+ * request past its row record PA_DEVERR_SEQ_LEN, too few free blocks record
+ * PA_DEVERR_BLOCKS, and the step then changes nothing: lengths and ring state
+ * are passed on as they were, slots and positions are all -1, starts all 0.
+ * A block id outside [0, num_blocks) records PA_DEVERR_BLOCK_ID and gives its
+ * tokens slot -1.  num_seqs is at most PA_MAX_TABLE_REQUESTS, max_tokens at
+ * most 2^30 (else PA_ERR_INVALID_ARG); with num_seqs == 0 the slots are all
+ * -1.  Buffers that are not the same must not overlap. */
+#define PA_MAX_TABLE_REQUESTS 8192
+pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
+                           int32_t block_size, int32_t num_blocks, const int32_t* free_blocks,
+                           int32_t free_capacity, const int32_t* free_state,
+                           int32_t* seq_lens_out, int32_t* free_state_out, int64_t* slot_mapping,
+                           int32_t* positions, int32_t* token_starts, int32_t max_tokens,
+                           void* stream);
 
 /* ---------------------------------------------------------------------------
  * Slot mapping from block tables (host).  slots[i] is the physical slot of

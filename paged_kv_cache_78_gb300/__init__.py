@@ -7,7 +7,10 @@ memory and streams.  If libpa.so is missing this module raises on import:
 there is no fallback path.
 
 Cache layout (one layer): a contiguous tensor [2, num_blocks, block_size,
-num_kv_heads, head_size] of bf16 or fp32, index 0 = keys, 1 = values.
+num_kv_heads, head_size] of bf16 or fp32, index 0 = keys, 1 = values; or a
+4-bit pool, a contiguous uint8 tensor [num_blocks, num_kv_heads,
+block_size / 8, 9 * head_size] (alloc_fp4_cache) for the pa_*_fp4 calls and
+the block copies.
 """
 from __future__ import annotations
 
@@ -29,6 +32,7 @@ PA_ERR_DEVICE_CHECK = 6
 PA_ERR_TIMEOUT = 7
 PA_BF16 = 0
 PA_FP32 = 1
+PA_FP4 = 2
 PA_KERNEL_AUTO = 0
 PA_KERNEL_SIMT = 1
 PA_KERNEL_TENSOR = 2
@@ -36,6 +40,7 @@ PA_DEVERR_SLOT = 0x1
 PA_DEVERR_BLOCK_ID = 0x2
 PA_DEVERR_SEQ_LEN = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_BLOCKS = 0x10
 PA_PARTITION_BALANCED = -2
 
 # Every function include/pa.h declares.
@@ -51,7 +56,8 @@ EXPORTS = (
     "pa_swap_blocks", "pa_pool_set_cpu_blocks", "pa_pool_swap_out", "pa_pool_swap_in",
     "pa_pool_is_swapped", "pa_pool_num_free_cpu", "pa_decode_append", "pa_copy_bytes",
     "pa_set_decode_wait_limit", "pa_decode_shared_plan", "pa_decode_shared_workspace_size",
-    "pa_decode_shared",
+    "pa_decode_shared", "pa_reshape_and_cache_fp4", "pa_gather_cache_fp4", "pa_decode_fp4",
+    "pa_decode_fp4_workspace_size", "pa_extend_tables",
 )
 
 
@@ -117,6 +123,13 @@ def _load() -> ctypes.CDLL:
                                             p_sz],
         "pa_decode_shared": [vp, vp, vp, desc, vp, i32, vp, i32, i32, f32, i32, vp,
                              ctypes.POINTER(SharedPlanInfo), vp, vp, vp, sz, vp],
+        "pa_reshape_and_cache_fp4": [vp, desc, vp, vp, i32, i64, i64, vp, i32, f32, f32, vp],
+        "pa_gather_cache_fp4": [vp, vp, i32, vp, desc, vp, i32, f32, f32, vp],
+        "pa_decode_fp4_workspace_size": [desc, i32, p_sz],
+        "pa_decode_fp4": [vp, vp, i32, i64, vp, desc, f32, f32, vp, i32, vp, i32, i32, f32, vp, sz,
+                          vp],
+        "pa_extend_tables": [vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32,
+                             vp],
         "pa_pool_add_seq_tokens": [vp, vp, i64, p_i64, p_i64],
         "pa_pool_append_token_id": [vp, i64, i32, p_i64, vp],
         "pa_pool_is_cached": [vp, i32, p_i32],
@@ -186,6 +199,32 @@ def cache_desc(cache: torch.Tensor) -> CacheDesc:
     return CacheDesc(nb, bs, hkv, d, _dtype_code(cache))
 
 
+def fp4_cache_desc(cache: torch.Tensor) -> CacheDesc:
+    """Descriptor of a 4-bit pool [num_blocks, num_kv_heads, block_size / 8, 9 * head_size]."""
+    if cache.dtype != torch.uint8:
+        raise TypeError("a 4-bit cache must be uint8, got %s" % cache.dtype)
+    if cache.dim() != 4 or cache.shape[3] % 9:
+        raise ValueError("a 4-bit cache must be [num_blocks, num_kv_heads, block_size / 8, "
+                         "9 * head_size]")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    nb, hkv, tiles, size = cache.shape
+    return CacheDesc(nb, 8 * tiles, hkv, size // 9, PA_FP4)
+
+
+def alloc_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
+                    device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit pool (every key and value zero)."""
+    if block_size < 8 or block_size % 8:
+        raise ValueError("a 4-bit cache's block_size is a power of two in [8, 256]")
+    return torch.zeros((num_blocks, num_kv_heads, block_size // 8, 9 * head_size),
+                       dtype=torch.uint8, device=device)
+
+
+def _pool_desc(cache: torch.Tensor) -> CacheDesc:
+    return fp4_cache_desc(cache) if cache.dtype == torch.uint8 else cache_desc(cache)
+
+
 def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -228,7 +267,7 @@ def pa_reshape_and_cache(cache: torch.Tensor, key: torch.Tensor, value: torch.Te
 
 def pa_copy_blocks(cache: torch.Tensor, pairs: torch.Tensor, stream=None) -> None:
     """Copy block pairs[i, 0] to block pairs[i, 1] (keys and values)."""
-    desc = cache_desc(cache)
+    desc = _pool_desc(cache)
     n = pairs.shape[0] if pairs.numel() else 0
     if n and (pairs.dim() != 2 or pairs.shape[1] != 2):
         raise ValueError("pairs must be [num_pairs, 2]")
@@ -266,7 +305,7 @@ def pa_swap_blocks(dst_cache: torch.Tensor, src_cache: torch.Tensor, pairs: torc
     n = pairs.shape[0] if pairs.numel() else 0
     if n and (pairs.dim() != 2 or pairs.shape[1] != 2):
         raise ValueError("pairs must be [num_pairs, 2]")
-    dd, sd = cache_desc(dst_cache), cache_desc(src_cache)
+    dd, sd = _pool_desc(dst_cache), _pool_desc(src_cache)
     _check(lib.pa_swap_blocks(_dev_or_pinned_ptr(dst_cache, "dst_cache"), ctypes.byref(dd),
                               _dev_or_pinned_ptr(src_cache, "src_cache"), ctypes.byref(sd),
                               _dev_or_pinned_ptr(pairs, "pairs", torch.int64) if n else None, n,
@@ -460,6 +499,166 @@ def pa_decode_shared(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor
                                 s, hq, float(scale), int(max_seq_len),
                                 _dev_ptr(plan_dev, "plan", torch.int32), ctypes.byref(plan.info),
                                 kn, vn, ws_ptr, ws_bytes, _stream(stream)), "pa_decode_shared")
+
+
+# ---------------------------------------------------------------------------
+# 4-bit pool and device-side tables
+# ---------------------------------------------------------------------------
+
+def _on_current_device(cache: torch.Tensor, *others: torch.Tensor) -> None:
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError("cache must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are on device %d, which is not the current one" % dev)
+    for t in others:
+        if t.get_device() != dev:
+            raise ValueError("every tensor must be on the cache's device")
+
+
+def _rows(t: torch.Tensor, name: str, heads: int, head_size: int):
+    """Address and row stride (elements) of [n, heads, head_size] rows, which
+    may lie apart (a slice of a fused projection's output)."""
+    n, h, d = t.shape
+    if h != heads or d != head_size:
+        raise ValueError("%s must be [n, %d, %d], got %s" % (name, heads, head_size, tuple(t.shape)))
+    row, inner, one = t.stride()
+    if (one != 1 and d > 1) or (inner != d and h > 1):
+        raise ValueError("%s: each row's heads must be contiguous" % name)
+    return t.data_ptr(), (row if n > 1 else heads * head_size)
+
+
+def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                             slot_mapping: torch.Tensor, key_scale: float = 1.0,
+                             value_scale: float = 1.0, stream=None) -> None:
+    """pa_reshape_and_cache into a 4-bit pool: key/value [n, num_kv_heads,
+    head_size] (bf16 or fp32, rows may lie apart) are rounded to 4-bit codes
+    with a scale per 16 elements; key_scale / value_scale are the pool's
+    tensor scales (powers of two)."""
+    desc = fp4_cache_desc(cache)
+    n = key.shape[0]
+    if key.shape != value.shape or key.dim() != 3:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
+    if key.dtype != value.dtype:
+        raise TypeError("key and value must have the same dtype")
+    if slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    _on_current_device(cache, key, value, slot_mapping)
+    kp, ks = _rows(key, "key", desc.num_kv_heads, desc.head_size)
+    vp, vs = _rows(value, "value", desc.num_kv_heads, desc.head_size)
+    _check(lib.pa_reshape_and_cache_fp4(cache.data_ptr(), ctypes.byref(desc), kp, vp,
+                                        _dtype_code(key), ks, vs,
+                                        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
+                                        key_scale, value_scale, _stream(stream)),
+           "pa_reshape_and_cache_fp4")
+
+
+def pa_gather_cache_fp4(key: torch.Tensor, value: torch.Tensor, cache: torch.Tensor,
+                        slot_mapping: torch.Tensor, key_scale: float = 1.0,
+                        value_scale: float = 1.0, stream=None) -> None:
+    """Read tokens back from a 4-bit pool: key/value [n, num_kv_heads,
+    head_size] (bf16 or fp32, contiguous) receive what the slots hold; rows of
+    negative slots stay as they were."""
+    desc = fp4_cache_desc(cache)
+    n = key.shape[0]
+    if key.shape != value.shape or tuple(key.shape[1:]) != (desc.num_kv_heads, desc.head_size):
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
+    if key.dtype != value.dtype:
+        raise TypeError("key and value must have the same dtype")
+    if slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    _on_current_device(cache, key, value, slot_mapping)
+    _check(lib.pa_gather_cache_fp4(_dev_ptr(key, "key"), _dev_ptr(value, "value"),
+                                   _dtype_code(key), cache.data_ptr(), ctypes.byref(desc),
+                                   _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
+                                   key_scale, value_scale, _stream(stream)),
+           "pa_gather_cache_fp4")
+
+
+def pa_decode_fp4_workspace_size(cache_or_desc, num_heads: int) -> int:
+    """Workspace bytes of pa_decode_fp4, whatever the batch (alloc_workspace)."""
+    desc = (cache_or_desc if isinstance(cache_or_desc, CacheDesc)
+            else fp4_cache_desc(cache_or_desc))
+    out = ctypes.c_size_t()
+    _check(lib.pa_decode_fp4_workspace_size(ctypes.byref(desc), num_heads, ctypes.byref(out)),
+           "pa_decode_fp4_workspace_size")
+    return out.value
+
+
+def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
+                  block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                  workspace: torch.Tensor, key_scale: float = 1.0, value_scale: float = 1.0,
+                  stream=None) -> None:
+    """pa_decode over a 4-bit pool; query (rows may lie apart) and out are
+    bf16 or fp32.  The launch depends on the shapes alone, so that a captured
+    call serves sequences as they grow."""
+    desc = fp4_cache_desc(cache)
+    s, hq, d = query.shape
+    if out.shape != query.shape or d != desc.head_size:
+        raise ValueError("query/out must be [num_seqs, num_heads, head_size]")
+    if query.dtype != out.dtype:
+        raise TypeError("query and out must have the same dtype")
+    if block_tables.dim() != 2 or block_tables.shape[0] != s or seq_lens.shape != (s,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
+    _on_current_device(cache, out, query, block_tables, seq_lens, workspace)
+    qp, qs = _rows(query, "query", hq, d)
+    _check(lib.pa_decode_fp4(_dev_ptr(out, "out"), qp, _dtype_code(query), qs, cache.data_ptr(),
+                             ctypes.byref(desc), key_scale, value_scale,
+                             _dev_ptr(block_tables, "block_tables", torch.int32),
+                             block_tables.shape[1], _dev_ptr(seq_lens, "seq_lens", torch.int32), s,
+                             hq, scale, _dev_ptr(workspace, "workspace"), workspace.nbytes,
+                             _stream(stream)), "pa_decode_fp4")
+
+
+def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     new_tokens: torch.Tensor, block_size: int, num_blocks: int,
+                     slot_mapping: torch.Tensor, positions: torch.Tensor | None = None,
+                     token_starts: torch.Tensor | None = None,
+                     seq_lens_out: torch.Tensor | None = None,
+                     free_blocks: torch.Tensor | None = None,
+                     free_state: torch.Tensor | None = None,
+                     free_state_out: torch.Tensor | None = None, stream=None) -> None:
+    """Append new_tokens[r] tokens to every request on the device: block
+    tables extended from the ring of free blocks (free_blocks, free_state =
+    [front, blocks left]; without them the tables hold every block already),
+    slots and positions of the new tokens, -1 behind them, lengths and ring
+    state advanced (in place unless *_out are given)."""
+    n = seq_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or new_tokens.shape != (n,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens and new_tokens "
+                         "[num_seqs]")
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [max_tokens]")
+    if positions is not None and positions.shape != slot_mapping.shape:
+        raise ValueError("positions must be [max_tokens]")
+    if token_starts is not None and token_starts.shape != (n + 1,):
+        raise ValueError("token_starts must be [num_seqs + 1]")
+    if (free_blocks is None) != (free_state is None):
+        raise ValueError("free_blocks and free_state go together")
+    if free_state_out is not None and free_state is None:
+        raise ValueError("free_state_out needs free_state")
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    free_state_out = free_state if free_state_out is None else free_state_out
+    if seq_lens_out.shape != (n,):
+        raise ValueError("seq_lens_out must be [num_seqs]")
+    if free_state is not None and (free_state.shape != (2,) or free_state_out.shape != (2,) or
+                                   free_blocks.dim() != 1):
+        raise ValueError("free_blocks must be [capacity], free_state [2]")
+    given = [t for t in (seq_lens, new_tokens, slot_mapping, positions, token_starts, seq_lens_out,
+                         free_blocks, free_state, free_state_out) if t is not None]
+    _on_current_device(block_tables, *given)
+
+    def ptr(t, name, dtype=torch.int32):
+        return None if t is None else _dev_ptr(t, name, dtype)
+
+    _check(lib.pa_extend_tables(
+        ptr(block_tables, "block_tables"), block_tables.shape[1], ptr(seq_lens, "seq_lens"),
+        ptr(new_tokens, "new_tokens"), n, block_size, num_blocks, ptr(free_blocks, "free_blocks"),
+        0 if free_blocks is None else free_blocks.shape[0], ptr(free_state, "free_state"),
+        ptr(seq_lens_out, "seq_lens_out"), ptr(free_state_out, "free_state_out"),
+        ptr(slot_mapping, "slot_mapping", torch.int64), ptr(positions, "positions"),
+        ptr(token_starts, "token_starts"), slot_mapping.shape[0], _stream(stream)),
+        "pa_extend_tables")
 
 
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20

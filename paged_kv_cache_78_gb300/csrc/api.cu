@@ -64,6 +64,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 pa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
+}  // namespace
+
+namespace pa {
+
 // Device-side state of the current device: the error word's address and the SM count.
 pa_status device_state(unsigned int** err, int* num_sms) {
   int dev = 0;
@@ -82,6 +86,12 @@ pa_status device_state(unsigned int** err, int* num_sms) {
   if (num_sms) *num_sms = g_num_sms[dev];
   return PA_OK;
 }
+
+}  // namespace pa
+
+namespace {
+
+using pa::device_state;
 
 pa_status encode_fn(EncodeTiledFn* fn) {
   std::lock_guard<std::mutex> lock(g_mutex);
@@ -105,6 +115,30 @@ pa_status check_desc(const pa_cache_desc* d) {
   if (d->dtype != PA_BF16 && d->dtype != PA_FP32) return PA_ERR_INVALID_ARG;
   if ((d->head_size * elem_bytes(d->dtype)) % 16 != 0) return PA_ERR_INVALID_ARG;
   return PA_OK;
+}
+
+// The copies also take 4-bit pools (PA_FP4).
+pa_status check_pool_desc(const pa_cache_desc* d) {
+  return d && d->dtype == PA_FP4 ? pa::check_fp4_desc(d) : check_desc(d);
+}
+
+// Half a block: one plane's rows of a bf16 or fp32 block, or half the bytes
+// of a 4-bit block (whose tiles hold keys and values together).
+pa::BlockGeometry block_geometry(const pa_cache_desc* d) {
+  pa::BlockGeometry g;
+  if (d->dtype == PA_FP4) {
+    g.bytes = pa::fp4_block_bytes(d) / 2;
+    g.stride = 2 * g.bytes;
+  } else {
+    g.bytes = (int64_t)d->block_size * d->num_kv_heads * d->head_size * elem_bytes(d->dtype);
+    g.stride = g.bytes;
+  }
+  return g;
+}
+
+// Distance between a block's halves.
+int64_t half_stride(const pa_cache_desc* d, const pa::BlockGeometry& g) {
+  return d->dtype == PA_FP4 ? g.bytes : d->num_blocks * g.bytes;
 }
 
 bool head_size_supported(int d) { return d == 64 || d == 128 || d == 256; }
@@ -390,17 +424,17 @@ pa_status pa_reshape_and_cache(void* cache, const pa_cache_desc* desc, const voi
 
 pa_status pa_copy_blocks(void* cache, const pa_cache_desc* desc, const int64_t* pairs,
                          int32_t num_pairs, void* stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_pool_desc(desc);
   if (st != PA_OK) return st;
   if (num_pairs < 0 || num_pairs > kMaxCopyPairs) return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (!cache || !pairs || !aligned(cache, 16) || !aligned(pairs, 8)) return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = device_state(&err, nullptr)) != PA_OK) return st;
-  const int64_t block_bytes = (int64_t)desc->block_size * desc->num_kv_heads * desc->head_size *
-                              elem_bytes(desc->dtype);
+  const pa::BlockGeometry g = block_geometry(desc);
+  const int64_t half = half_stride(desc, g);
   return cuda_status(pa::launch_copy_blocks(cache, cache, pairs, num_pairs, desc->num_blocks,
-                                            desc->num_blocks, block_bytes, err,
+                                            desc->num_blocks, g, half, half, err,
                                             static_cast<cudaStream_t>(stream)));
 }
 
@@ -427,9 +461,9 @@ static pa_status kernel_address(const void* p, const void** out) {
 pa_status pa_swap_blocks(void* dst_cache, const pa_cache_desc* dst_desc, const void* src_cache,
                          const pa_cache_desc* src_desc, const int64_t* pairs, int32_t num_pairs,
                          void* stream) {
-  pa_status st = check_desc(dst_desc);
+  pa_status st = check_pool_desc(dst_desc);
   if (st != PA_OK) return st;
-  if ((st = check_desc(src_desc)) != PA_OK) return st;
+  if ((st = check_pool_desc(src_desc)) != PA_OK) return st;
   if (dst_desc->block_size != src_desc->block_size ||
       dst_desc->num_kv_heads != src_desc->num_kv_heads ||
       dst_desc->head_size != src_desc->head_size || dst_desc->dtype != src_desc->dtype)
@@ -447,12 +481,12 @@ pa_status pa_swap_blocks(void* dst_cache, const pa_cache_desc* dst_desc, const v
   if ((st = kernel_address(pairs, &pr)) != PA_OK) return st;
   unsigned int* err = nullptr;
   if ((st = device_state(&err, nullptr)) != PA_OK) return st;
-  const int64_t block_bytes = (int64_t)dst_desc->block_size * dst_desc->num_kv_heads *
-                              dst_desc->head_size * elem_bytes(dst_desc->dtype);
+  const pa::BlockGeometry g = block_geometry(dst_desc);
   return cuda_status(pa::launch_copy_blocks(const_cast<void*>(d), s,
                                             static_cast<const int64_t*>(pr), num_pairs,
-                                            dst_desc->num_blocks, src_desc->num_blocks,
-                                            block_bytes, err, static_cast<cudaStream_t>(stream)));
+                                            dst_desc->num_blocks, src_desc->num_blocks, g,
+                                            half_stride(dst_desc, g), half_stride(src_desc, g),
+                                            err, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_copy_bytes(void* dst, const void* src, size_t bytes, void* stream) {

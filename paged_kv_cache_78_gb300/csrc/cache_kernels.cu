@@ -42,7 +42,7 @@ __global__ void reshape_and_cache_kernel(uint8_t* __restrict__ cache,
   stg_v4(dst, ldg_nc_v4(src));
 }
 
-// One CTA per (pair, K or V, slice of the block): block src of the source
+// One CTA per (pair, half of a block, slice of the half): block src of the source
 // pool -> block dst of the destination pool, copied whole.  Copy-on-write
 // copies within one pool (studying-code.tistory.com/16, section "생성 단계에서의
 // Copy-on-Write": the writer of a shared block copies its content to a new
@@ -51,8 +51,8 @@ __global__ void reshape_and_cache_kernel(uint8_t* __restrict__ cache,
 __global__ void copy_blocks_kernel(uint8_t* __restrict__ dst_cache,
                                    const uint8_t* __restrict__ src_cache,
                                    const int64_t* __restrict__ pairs, int64_t dst_blocks,
-                                   int64_t src_blocks, int64_t block_bytes, int64_t dst_plane,
-                                   int64_t src_plane, unsigned int* err) {
+                                   int64_t src_blocks, int64_t block_bytes, int64_t block_stride,
+                                   int64_t dst_plane, int64_t src_plane, unsigned int* err) {
   grid_dependents_launch();
   grid_dependency_wait();
   const int pair = blockIdx.x >> 1;
@@ -63,8 +63,8 @@ __global__ void copy_blocks_kernel(uint8_t* __restrict__ dst_cache,
     if (kv == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(err, PA_DEVERR_BLOCK_ID);
     return;
   }
-  const uint8_t* s = src_cache + kv * src_plane + src * block_bytes;
-  uint8_t* d = dst_cache + kv * dst_plane + dst * block_bytes;
+  const uint8_t* s = src_cache + kv * src_plane + src * block_stride;
+  uint8_t* d = dst_cache + kv * dst_plane + dst * block_stride;
   const int64_t n16 = block_bytes / 16;
   const int64_t step = (int64_t)gridDim.y * blockDim.x;
   int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
@@ -135,8 +135,10 @@ cudaError_t launch_reshape_and_cache(void* cache, const void* key, const void* v
 
 cudaError_t launch_copy_blocks(void* dst_cache, const void* src_cache, const int64_t* pairs,
                                int num_pairs, int64_t dst_blocks, int64_t src_blocks,
-                               int64_t block_bytes, unsigned int* err, cudaStream_t stream) {
+                               BlockGeometry geometry, int64_t dst_half, int64_t src_half,
+                               unsigned int* err, cudaStream_t stream) {
   const int block = 256;
+  int64_t block_bytes = geometry.bytes, block_stride = geometry.stride;
   const int64_t per_cta = (int64_t)block * 16 * 8;  // about 8 vectors per thread
   int slices = (int)((block_bytes + per_cta - 1) / per_cta);
   if (slices < 1) slices = 1;
@@ -144,9 +146,8 @@ cudaError_t launch_copy_blocks(void* dst_cache, const void* src_cache, const int
   dim3 grid((unsigned)num_pairs * 2u, (unsigned)slices);
   uint8_t* d = static_cast<uint8_t*>(dst_cache);
   const uint8_t* s = static_cast<const uint8_t*>(src_cache);
-  int64_t dst_plane = dst_blocks * block_bytes, src_plane = src_blocks * block_bytes;
-  void* args[] = {&d, &s, &pairs, &dst_blocks, &src_blocks, &block_bytes, &dst_plane, &src_plane,
-                  &err};
+  void* args[] = {&d, &s, &pairs, &dst_blocks, &src_blocks, &block_bytes, &block_stride, &dst_half,
+                  &src_half, &err};
   return launch_overlapped((const void*)copy_blocks_kernel, grid, dim3(block), 0, stream, args);
 }
 

@@ -1,0 +1,597 @@
+"""The 4-bit pool on the GPU against the binary64 oracle: quantising write and
+read-back (exact), block copies (exact), decode attention (within a bound
+derived from the roundings), the device-side tables (exact), and the three as
+a decode step, captured and replayed."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_78_gb300 as pa
+from fp4_util import TORCH, Batch, assert_decode, host, rounded
+from oracle import fp4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word():
+    pa.pa_get_device_error()
+    yield
+
+
+def dev(a):
+    return (a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))).cuda()
+
+
+def same(a, b):
+    return np.array_equal(np.asarray(a, dtype=np.float64), b, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------
+# write and read-back
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("head,hkv,block,n", [(64, 1, 8, 1), (64, 3, 16, 77), (128, 8, 16, 130),
+                                              (128, 2, 256, 300), (256, 5, 32, 41)])
+def test_write_and_gather(dtype, head, hkv, block, n):
+    rng = np.random.default_rng(head + n)
+    nb = -(-n // block) + 3
+    cache = rng.integers(0, 256, (nb, hkv, block // 8, 9 * head), dtype=np.uint8)
+    slots = rng.permutation(nb * block)[:n].astype(np.int64)
+    k = rounded(4 * rng.standard_normal((n, hkv, head)) * np.exp(rng.standard_normal((n, hkv, 1))), dtype)
+    v = rounded(0.1 * rng.standard_normal((n, hkv, head)), dtype)
+    d = dev(cache)
+    pa.pa_reshape_and_cache_fp4(d, dev(k), dev(v), dev(slots), 2.0, 0.125)
+    want = cache.copy()
+    fp4.write(want, host(k), host(v), slots, 2.0, 0.125)
+    got = d.cpu().numpy()
+    every = np.arange(nb * block)
+    for a, b in zip(fp4.read(got, every, 2.0, 0.125), fp4.read(want, every, 2.0, 0.125)):
+        assert same(a, b)
+    # the read-back gives the very numbers, slots repeated
+    again = np.concatenate([slots, slots[:3]])
+    ko = torch.empty((len(again), hkv, head), dtype=TORCH[dtype], device="cuda")
+    vo = torch.empty_like(ko)
+    pa.pa_gather_cache_fp4(ko, vo, d, dev(again), 2.0, 0.125)
+    rk, rv = fp4.read(want, again, 2.0, 0.125)
+    assert same(host(ko), rk) and same(host(vo), rv)
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_write_rounds_on_the_exact_quotients(dtype):
+    # Every border of e2m1 times scales of every mantissa, the number itself
+    # and its neighbours in the type; each group's maximum fixes its scale.
+    rows = []
+    for m in range(8, 16):
+        for e in (-6, 0, 5):
+            s = m / 8 * 2.0 ** e
+            b = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * s
+            t = torch.from_numpy(b.astype(np.float32)).to(TORCH[dtype])
+            up = torch.nextafter(t, torch.full_like(t, float("inf")))
+            down = torch.nextafter(t, torch.zeros_like(t))
+            for x in (t, up, down):
+                x = host(x)
+                rows.append(np.concatenate([[6 * s], x, -x, [0.0]]))
+    x = np.zeros((len(rows), 1, 64))
+    x[:, 0, :16] = rows
+    x[:, 0, 16:32] = np.array(rows)[:, ::-1]
+    key, value = rounded(x, dtype), rounded(-x, dtype)
+    cache = torch.zeros((-(-len(rows) // 8), 1, 1, 9 * 64), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(len(rows), device="cuda")
+    pa.pa_reshape_and_cache_fp4(cache, dev(key), dev(value), slots)
+    gk, gv = fp4.read(cache.cpu().numpy(), np.arange(len(rows)))
+    assert same(gk, fp4.dequantise(*fp4.quantise(host(key))))
+    assert same(gv, fp4.dequantise(*fp4.quantise(host(value))))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_write_special_values(dtype):
+    rng = np.random.default_rng(7)
+    x = rng.standard_normal((6, 2, 64))
+    x[0, 0, 3] = np.nan
+    x[1, 1, 17] = np.inf
+    x[2, 0, 40] = -np.inf
+    x[2, 0, 41] = np.nan
+    x[3] = 0.0
+    x[4] = 1e-30 * rng.standard_normal((2, 64))     # below the smallest scale
+    x[5] = 3e38 * np.sign(rng.standard_normal((2, 64)))
+    t = rounded(x, dtype)
+    cache = torch.randint(0, 256, (1, 2, 1, 9 * 64), dtype=torch.uint8, device="cuda")
+    pa.pa_reshape_and_cache_fp4(cache, dev(t), dev(t), torch.arange(6, device="cuda"))
+    want = fp4.dequantise(*fp4.quantise(host(t)))
+    for got in fp4.read(cache.cpu().numpy(), np.arange(6)):
+        assert same(got, want)
+    ko = torch.empty((6, 2, 64), dtype=TORCH[dtype], device="cuda")
+    vo = torch.empty_like(ko)
+    pa.pa_gather_cache_fp4(ko, vo, cache, torch.arange(6, device="cuda"))
+    assert same(host(ko), want) and same(host(vo), want)
+
+
+def test_padding_and_slots_outside_the_pool():
+    rng = np.random.default_rng(8)
+    cache = rng.integers(0, 256, (3, 2, 2, 9 * 64), dtype=np.uint8)
+    k = rounded(rng.standard_normal((5, 2, 64)), "bf16")
+    slots = np.array([5, -1, 48, 47, 1 << 40], dtype=np.int64)
+    d = dev(cache)
+    pa.pa_reshape_and_cache_fp4(d, dev(k), dev(k), dev(slots))
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SLOT
+    want = cache.copy()
+    fp4.write(want, host(k), host(k), slots)
+    others = np.setdiff1d(np.arange(48), [5, 47])
+    for a, b in zip(fp4.read(d.cpu().numpy(), others), fp4.read(cache, others)):
+        assert same(a, b)
+    ko = torch.full((5, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    vo = torch.full_like(ko, 8.0)
+    pa.pa_gather_cache_fp4(ko, vo, d, dev(slots))
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SLOT
+    rk, rv = fp4.read(want, slots[[0, 3]])
+    assert same(host(ko)[[0, 3]], rk) and same(host(vo)[[0, 3]], rv)
+    assert (host(ko)[[1, 2, 4]] == 9).all() and (host(vo)[[1, 2, 4]] == 8).all()
+
+
+def test_write_takes_rows_of_a_fused_projection():
+    rng = np.random.default_rng(9)
+    qkv = dev(rounded(rng.standard_normal((37, 6 * 64)), "bf16"))
+    k, v = qkv[:, 2 * 64:4 * 64].unflatten(1, (2, 64)), qkv[:, 4 * 64:].unflatten(1, (2, 64))
+    slots = torch.arange(37, device="cuda")
+    a, b = (pa.alloc_fp4_cache(5, 8, 2, 64) for _ in range(2))
+    pa.pa_reshape_and_cache_fp4(a, k, v, slots)
+    pa.pa_reshape_and_cache_fp4(b, k.contiguous(), v.contiguous(), slots)
+    assert torch.equal(a, b) and a.any()
+    with pytest.raises(ValueError):
+        pa.pa_reshape_and_cache_fp4(a, k.transpose(1, 2).contiguous().transpose(1, 2), v, slots)
+    with pytest.raises(pa.PAError):  # rows that start off a 16-byte boundary
+        pa.pa_reshape_and_cache_fp4(a, qkv[:, 1:129].unflatten(1, (2, 64)), v, slots)
+
+
+def test_no_tokens():
+    c = pa.alloc_fp4_cache(2, 8, 2, 64)
+    k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    s = torch.empty(0, dtype=torch.int64, device="cuda")
+    pa.pa_reshape_and_cache_fp4(c, k, k, s)
+    pa.pa_gather_cache_fp4(k, k, c, s)
+
+
+@pytest.mark.parametrize("head,hkv,block", [(64, 1, 8), (128, 3, 16), (256, 2, 64)])
+def test_block_copies(head, hkv, block):
+    rng = np.random.default_rng(head)
+    a = rng.integers(0, 256, (9, hkv, block // 8, 9 * head), dtype=np.uint8)
+    d = dev(a)
+    pairs = torch.tensor([[0, 7], [3, 1], [8, 2]], device="cuda")
+    pa.pa_copy_blocks(d, pairs)
+    want = a.copy()
+    want[[7, 1, 2]] = a[[0, 3, 8]]
+    assert np.array_equal(d.cpu().numpy(), want)
+    cpu = torch.zeros((4, hkv, block // 8, 9 * head), dtype=torch.uint8).pin_memory()
+    pa.pa_swap_blocks(cpu, d, torch.tensor([[7, 3], [4, 0]], device="cuda"))
+    torch.cuda.synchronize()
+    assert np.array_equal(cpu.numpy()[[3, 0]], want[[7, 4]]) and not cpu[1:3].any()
+    pa.pa_swap_blocks(d, cpu, torch.tensor([[3, 5]], device="cuda"))
+    want[5] = want[7]
+    assert np.array_equal(d.cpu().numpy(), want)
+    pa.pa_copy_blocks(d, torch.tensor([[0, 9]], device="cuda"))
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_BLOCK_ID
+    assert np.array_equal(d.cpu().numpy(), want)
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+
+class Run:
+    """A batch on the device and its decode."""
+
+    def __init__(self, batch, workspace=None):
+        b = self.batch = batch
+        self.cache, self.query = dev(b.cache), dev(b.query)
+        self.tables, self.lens = dev(b.tables), dev(b.lens)
+        self.out = torch.full_like(self.query, 77.0)
+        self.ws = workspace
+        if workspace is None:
+            self.ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(self.cache, b.query.shape[1]),
+                                         "cuda")
+
+    def __call__(self, stream=None):
+        b = self.batch
+        pa.pa_decode_fp4(self.out, self.query, self.cache, self.tables, self.lens, b.scale, self.ws,
+                         b.key_scale, b.value_scale, stream=stream)
+        return self.out
+
+
+EDGES = [0, 1, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 0, 255, 257, 500]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("head,block", [(64, 8), (64, 16), (128, 8), (128, 16), (128, 64), (256, 16),
+                                        (256, 256), (64, 128)])
+def test_decode_edge_lengths(dtype, head, block):
+    r = Run(Batch(EDGES, 8, 2, head, block, dtype, seed=head + block))
+    assert_decode(r(), r.batch)
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("group", list(range(1, 17)))
+@pytest.mark.parametrize("head", [64, 128, 256])
+def test_decode_groups(head, group):
+    hkv = 1 + group % 3
+    for dtype in ("bf16", "fp32"):
+        r = Run(Batch([3, 100, 45], hkv * group, hkv, head, 16, dtype, seed=group))
+        assert_decode(r(), r.batch, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,heads,hkv,head,block", [
+    ([4096], 8, 1, 128, 16),              # one pair over many CTAs
+    ([5000, 1, 0, 3001], 4, 4, 64, 16),
+    ([20001], 16, 1, 64, 32),
+    ([2500, 777], 12, 2, 256, 8),
+    ([300] * 40, 40, 40, 128, 16),        # more pairs than CTAs
+    (list(range(0, 900, 7)), 7, 1, 128, 8),
+])
+def test_decode_larger(lens, heads, hkv, head, block, dtype):
+    r = Run(Batch(lens, heads, hkv, head, block, dtype, seed=len(lens)))
+    first = r().clone()
+    assert_decode(first, r.batch)
+    # again on the same workspace, and the same bits
+    r.out.fill_(55.0)
+    assert torch.equal(r(), first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_decode_peaked_and_scaled(dtype):
+    # large scores (weights close to 0 and 1), tensor scales, large queries
+    r = Run(Batch([50, 700, 33], 6, 2, 128, 16, dtype, seed=5, key_scale=4.0, value_scale=2.0 ** -6,
+                  query_std=30.0))
+    assert_decode(r(), r.batch)
+    r = Run(Batch([50, 700, 33], 6, 2, 128, 16, dtype, seed=6, query_std=2.0 ** -40))
+    assert_decode(r(), r.batch)
+    r = Run(Batch([50, 700, 33], 6, 2, 128, 16, dtype, seed=7, key_scale=2.0 ** -30, query_std=2.0 ** 30))
+    assert_decode(r(), r.batch)
+    b = Batch([64, 90], 4, 2, 64, 16, dtype, seed=8)
+    b.scale = -0.3
+    assert_decode(Run(b)(), b)
+    b.scale = 0.0
+    assert_decode(Run(b)(), b)
+
+
+def test_decode_rising_scores():
+    # the running maximum moves at every tile, by more and more
+    b = Batch([600], 4, 1, 64, 16, "bf16", seed=9)
+    ramp = np.linspace(0.0, 60.0, 600)[:, None, None] * np.ones((1, 1, 64))
+    fp4.write(b.cache, ramp, host(b.value), b.slots)
+    b.query = torch.ones_like(b.query)
+    assert_decode(Run(b)(), b)
+    fp4.write(b.cache, ramp[::-1], host(b.value), b.slots)
+    assert_decode(Run(b)(), b)
+
+
+def test_decode_nan_and_infinity():
+    b = Batch([40, 60, 50], 4, 2, 64, 16, "bf16", seed=10)
+    q = b.query.clone()
+    q[0, 1, 5] = float("nan")
+    q[2, 3, 9] = float("inf")
+    b.query = q
+    # a NaN key of sequence 1's first KV head, token 20
+    slot = b.slots[40 + 20]
+    k, v = fp4.read(b.cache, [slot])
+    k[0, 0, 3] = np.nan
+    fp4.write(b.cache, k, v, [slot])
+    r = Run(b)
+    got = host(r())
+    bad = np.zeros(got.shape, dtype=bool)
+    bad[0, 1] = bad[2, 3] = bad[1, :2] = True
+    assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+
+
+def test_decode_takes_strided_queries_and_padded_tables():
+    b = Batch([5, 60, 33], 6, 2, 128, 16, seed=11, width=40)
+    r = Run(b)
+    wide = torch.randn((3, 10 * 128), device="cuda").bfloat16()
+    wide[:, 128:7 * 128] = r.query.flatten(1)
+    r.query = wide[:, 128:7 * 128].unflatten(1, (6, 128))
+    assert not r.query.is_contiguous()
+    assert_decode(r(), b)
+    with pytest.raises(ValueError):
+        pa.pa_decode_fp4(r.out, r.query.transpose(0, 1).contiguous().transpose(0, 1), r.cache,
+                         r.tables, r.lens, b.scale, r.ws)
+    with pytest.raises(ValueError):
+        pa.pa_decode_fp4(r.out[:, :, ::2], r.query[:, :, ::2], r.cache, r.tables, r.lens, b.scale, r.ws)
+
+
+def test_decode_length_errors_touch_nothing_else():
+    b = Batch([16, 40, 8], 4, 2, 64, 16, seed=12, width=3)
+    r = Run(b)
+    r.lens[0] = 49                       # three blocks hold 48
+    got = r()
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SEQ_LEN
+    ref = b.reference()[0]
+    assert np.abs(host(got)[1:] - ref[1:]).max() < 0.05
+    r.lens[0] = -4                       # as an empty sequence
+    r.lens[1] = (1 << 31) - 1
+    got = r()
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SEQ_LEN
+    assert not got[0].any() and np.abs(host(got)[2] - ref[2]).max() < 0.05
+
+
+def test_decode_block_ids_outside_the_pool_count_as_zeros():
+    b = Batch([48, 20], 4, 2, 64, 16, seed=13)
+    r = Run(b)
+    for bad in (-1, b.cache.shape[0], -(1 << 31), (1 << 31) - 1):
+        r.tables[0, 1] = bad
+        got = host(r())
+        assert pa.pa_get_device_error() == pa.PA_DEVERR_BLOCK_ID
+        z = Batch([48, 20], 4, 2, 64, 16, seed=13)
+        fp4.write(z.cache, np.zeros((16, 2, 64)), np.zeros((16, 2, 64)),
+                  z.tables[0, 1].astype(np.int64) * 16 + np.arange(16))
+        assert_decode(r.out, z)
+        assert np.isfinite(got).all()
+
+
+def test_decode_rows_behind_the_batch_stay():
+    b = Batch([30, 0, 70], 4, 2, 64, 16, seed=14)
+    r = Run(b)
+    big = torch.full((5, 4, 64), 33.0, dtype=torch.bfloat16, device="cuda")
+    r.out = big[:3]
+    before = r.cache.clone()
+    assert_decode(r(), b)
+    assert (big[3:] == 33).all() and torch.equal(before, r.cache)
+
+
+def test_decode_past_32_bit_offsets():
+    # a pool of more than 4 GB; the sequence's blocks lie at its end
+    blocks = 260_000
+    cache = torch.zeros((blocks, 8, 2, 9 * 128), dtype=torch.uint8, device="cuda")
+    b = Batch([100], 16, 8, 128, 16, seed=15, spare=0)
+    first = blocks - b.cache.shape[0]
+    cache[first:] = dev(b.cache)
+    r = Run(b)
+    r.cache = cache
+    r.tables = dev(np.where(b.tables < (1 << 30), b.tables + first, b.tables).astype(np.int32))
+    assert_decode(r(), b)
+    ko = torch.empty((100, 8, 128), dtype=torch.float32, device="cuda")
+    vo = torch.empty_like(ko)
+    slots = dev(b.slots + first * 16)
+    pa.pa_gather_cache_fp4(ko, vo, cache, slots)
+    rk, rv = fp4.read(b.cache, b.slots)
+    assert same(host(ko), rk) and same(host(vo), rv)
+    pa.pa_reshape_and_cache_fp4(cache, vo, ko, slots)
+    pa.pa_gather_cache_fp4(ko, vo, cache, slots)
+    assert same(host(ko), fp4.dequantise(*fp4.quantise(rv)))
+    assert not cache[:first].any()
+
+
+def test_decode_many_sequences():
+    lens = [1 + (i * 7) % 19 for i in range(3001)]
+    r = Run(Batch(lens, 2, 1, 64, 8, seed=16))
+    assert_decode(r(), r.batch)
+
+
+def test_two_graphs_share_a_workspace_and_lengths_grow():
+    a = Run(Batch([70, 1, 300], 8, 2, 128, 16, seed=17))
+    b = Run(Batch([9, 2000], 4, 1, 128, 16, seed=18), workspace=None)
+    size = max(a.ws.numel(), b.ws.numel())
+    a.ws = b.ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    a(), b()
+    torch.cuda.synchronize()
+    graphs = []
+    for r in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r()
+        graphs.append(g)
+    for _ in range(3):
+        a.out.fill_(5), b.out.fill_(5)
+        for g in graphs:
+            g.replay()
+        assert_decode(a.out, a.batch)
+        assert_decode(b.out, b.batch)
+    # the captured call on shorter and on empty sequences
+    for lens in ([33, 1, 299], [0, 0, 17], [0, 0, 0]):
+        a.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        a.batch.lens = np.array(lens, dtype=np.int32)
+        graphs[0].replay()
+        assert_decode(a.out, a.batch)
+
+
+def test_two_streams_at_once():
+    runs = [Run(Batch([900, 31, 40 + i], 8, 2, 64, 16, seed=19 + i)) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, s in zip(runs, streams):
+            r(stream=s)
+    torch.cuda.synchronize()
+    for r in runs:
+        assert_decode(r.out, r.batch)
+
+
+def test_decode_refuses_small_workspaces():
+    r = Run(Batch([40], 4, 2, 64, 16))
+    r.ws = r.ws[:-256]
+    with pytest.raises(pa.PAError) as e:
+        r()
+    assert e.value.status == pa.PA_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------------------
+# tables
+# ---------------------------------------------------------------------------
+
+class Tables:
+    """A step of the tables on the device and in the oracle."""
+
+    def __init__(self, lens, new, block, width=None, ring=True, spare=5, seed=0, most=None):
+        rng = np.random.default_rng(seed)
+        lens, new = np.asarray(lens, dtype=np.int64), np.asarray(new, dtype=np.int64)
+        total = np.maximum(-(-(lens + np.maximum(new, 0)) // block), 0)
+        self.block, self.blocks = block, int(total.sum()) + spare
+        have = -(-lens // block) if ring else total
+        width = int(max(1, total.max(initial=1))) if width is None else width
+        perm = rng.permutation(self.blocks).astype(np.int32)
+        self.tables = np.full((len(lens), width), -7, dtype=np.int32)
+        at = 0
+        for r, c in enumerate(have):
+            self.tables[r, :c] = perm[at:at + c]
+            at += c
+        self.lens, self.new = lens.astype(np.int32), new.astype(np.int32)
+        self.ring = self.state = None
+        if ring:
+            front = int(rng.integers(0, self.blocks - at))
+            self.ring = np.roll(perm[at:], front)
+            self.state = np.array([front, self.blocks - at], dtype=np.int32)
+        self.most = int(max(new.sum(), 0)) + 3 if most is None else most
+
+    def check(self, in_place=False, error=0):
+        t, ln, new = dev(self.tables), dev(self.lens), dev(self.new)
+        ring = None if self.ring is None else dev(self.ring)
+        state = None if self.state is None else dev(self.state)
+        n = len(self.lens)
+        slots = torch.full((self.most,), 99, dtype=torch.int64, device="cuda")
+        pos = torch.full((self.most,), 99, dtype=torch.int32, device="cuda")
+        starts = torch.full((n + 1,), 99, dtype=torch.int32, device="cuda")
+        lo = ln if in_place else torch.full_like(ln, 99)
+        so = state if in_place or state is None else torch.full_like(state, 99)
+        pa.pa_extend_tables(t, ln, new, self.block, self.blocks, slots, pos, starts,
+                            seq_lens_out=lo, free_blocks=ring, free_state=state, free_state_out=so)
+        assert pa.pa_get_device_error() == error
+        want = fp4.extend_tables(self.tables, self.lens, self.new, self.block, self.blocks,
+                                 self.most, self.ring, self.state)
+        assert want[6] == (error in (pa.PA_DEVERR_SEQ_LEN, pa.PA_DEVERR_BLOCKS))
+        for name, got, ref in (("tables", t, want[0]), ("lens", lo, want[1]), ("slots", slots, want[3]),
+                               ("positions", pos, want[4]), ("starts", starts, want[5])):
+            assert np.array_equal(host(got), ref), name
+        if state is not None:
+            assert host(so).tolist() == list(want[2])
+        if not in_place:
+            assert np.array_equal(host(ln), self.lens)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("ring", [True, False])
+@pytest.mark.parametrize("block", [1, 8, 16, 256])
+def test_tables(block, ring, in_place):
+    rng = np.random.default_rng(block)
+    Tables([0, 1, 15, 16, 17, 255, 256, 40], [1, 0, 1, 1, 300, 1, 1, 0], block, ring=ring).check(in_place)
+    Tables([5], [1], block, ring=ring).check(in_place)
+    Tables([0], [0], block, ring=ring).check(in_place)
+    Tables(rng.integers(0, 200, 333), rng.integers(0, 40, 333), block, ring=ring).check(in_place)
+    Tables(rng.integers(0, 50, 700), np.ones(700, int), block, ring=ring).check(in_place)
+
+
+def test_tables_many_requests_and_tokens():
+    rng = np.random.default_rng(3)
+    Tables(rng.integers(0, 30, 8192), rng.integers(0, 3, 8192), 16).check(True)
+    Tables(rng.integers(0, 3, 2049), np.where(np.arange(2049) == 1000, 50_001, 0), 8).check()
+    Tables([3, 9], [70_000, 1], 16, most=90_000).check()
+
+
+def test_tables_refuse_whole_steps():
+    for kw in (dict(lens=[3, 5], new=[1, -1]), dict(lens=[3, -5], new=[1, 1]),
+               dict(lens=[3, 30], new=[14, 3], width=2),
+               dict(lens=[3, 30], new=[14, 4], most=17),
+               dict(lens=[3, 3, 3], new=[(1 << 31) - 1, (1 << 31) - 1, 5], width=4, most=8, spare=9)):
+        if max(kw["new"]) > 1000:
+            t = Tables([3, 3, 3], [1, 1, 5], 16, width=4, most=8)
+            t.new = np.array(kw["new"], dtype=np.int32)
+            # the oracle walks tokens: it meets the end of the row
+            t.check(error=pa.PA_DEVERR_SEQ_LEN)
+            continue
+        for in_place in (False, True):
+            Tables(block=16, **kw).check(in_place, error=pa.PA_DEVERR_SEQ_LEN)
+    t = Tables([3, 16, 40], [1, 1, 100], 16, spare=3)
+    t.state[1] = 6                       # seven are needed
+    t.check(error=pa.PA_DEVERR_BLOCKS)
+    t.check(True, error=pa.PA_DEVERR_BLOCKS)
+    t.state[1] = 7
+    t.check()
+
+
+def test_tables_bad_ids_lose_their_tokens():
+    t = Tables([16, 20], [2, 1], 16)
+    t.ring[:] = t.blocks                 # past the pool
+    t.check(error=pa.PA_DEVERR_BLOCK_ID)
+    t = Tables([16, 20], [2, 1], 16, ring=False)
+    t.tables[1, 1] = -1
+    t.check(error=pa.PA_DEVERR_BLOCK_ID)
+
+
+def test_tables_without_requests():
+    slots = torch.full((5,), 4, dtype=torch.int64, device="cuda")
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    starts = torch.full((1,), 4, dtype=torch.int32, device="cuda")
+    pa.pa_extend_tables(torch.empty((0, 3), dtype=torch.int32, device="cuda"), e, e, 16, 4, slots,
+                        token_starts=starts)
+    assert (slots == -1).all() and (starts == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# the step
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,heads,hkv,head,block", [("bf16", 8, 2, 128, 16), ("bf16", 5, 5, 64, 8),
+                                                        ("fp32", 6, 2, 256, 16)])
+def test_captured_step_serves_growing_sequences(dtype, heads, hkv, head, block):
+    """tables -> write -> decode captured once, replayed for every step: the
+    device's tables agree with the host pool's, the attention with the oracle
+    fed the same tokens."""
+    rng = np.random.default_rng(head)
+    prompts = [3, block, 0, 4 * block - 1]
+    blocks, width, steps = 40, 10, 2 * block + 3
+    pool = pa.Pool(blocks, block, free_order=rng.permutation(blocks))
+    seqs = [pool.add_seq(n) for n in prompts]
+    tables, lens = pool.fill_tables(seqs, width)
+    ring = dev(np.array(pool.free_queue(), dtype=np.int32))
+    state = torch.tensor([0, pool.num_free()], dtype=torch.int32, device="cuda")
+    tables, lens = tables.cuda(), lens.cuda()
+    cache = torch.randint(0, 256, (blocks, hkv, block // 8, 9 * head), dtype=torch.uint8, device="cuda")
+    # prompts
+    n = sum(prompts)
+    pk = rounded(rng.standard_normal((n, hkv, head)), dtype)
+    pv = rounded(rng.standard_normal((n, hkv, head)), dtype)
+    slots0 = torch.full((n + 2,), -1, dtype=torch.int64, device="cuda")
+    pa.pa_extend_tables(tables, torch.zeros_like(lens), lens, block, blocks, slots0,
+                        seq_lens_out=torch.empty_like(lens))
+    pa.pa_reshape_and_cache_fp4(cache, dev(pk), dev(pv), slots0[:n])
+    ref = cache.cpu().numpy().copy()
+    fp4.write(ref, host(pk), host(pv), host(slots0[:n]))
+
+    s = len(prompts)
+    new = torch.ones(s, dtype=torch.int32, device="cuda")
+    slots = torch.empty(s, dtype=torch.int64, device="cuda")
+    qkv = torch.zeros((s, (heads + 2 * hkv) * head), dtype=TORCH[dtype], device="cuda")
+    q, k, v = qkv.split([heads * head, hkv * head, hkv * head], dim=1)
+    q, k, v = q.unflatten(1, (heads, head)), k.unflatten(1, (hkv, head)), v.unflatten(1, (hkv, head))
+    out = torch.empty((s, heads, head), dtype=TORCH[dtype], device="cuda")
+    ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(cache, heads), "cuda")
+
+    def step():
+        pa.pa_extend_tables(tables, lens, new, block, blocks, slots, free_blocks=ring, free_state=state)
+        pa.pa_reshape_and_cache_fp4(cache, k, v, slots)
+        pa.pa_decode_fp4(out, q, cache, tables, lens, head ** -0.5, ws)
+
+    saved = [t.clone() for t in (tables, lens, state, cache)]
+    step()                               # once outside, then put everything back
+    torch.cuda.synchronize()
+    for t, was in zip((tables, lens, state, cache), saved):
+        t.copy_(was)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(steps):
+        x = rounded(rng.standard_normal(tuple(qkv.shape)), dtype)
+        qkv.copy_(x)
+        g.replay()
+        want_slots, pairs = pool.append_tokens(seqs)
+        assert pairs.numel() == 0 and torch.equal(slots.cpu(), want_slots)
+        fp4.write(ref, host(k), host(v), want_slots.numpy())
+        if i % 5 and i != steps - 1:
+            continue
+        b = Batch([1], heads, hkv, head, block, dtype)  # a shell for the bound
+        b.cache, b.query = ref, q.detach().cpu()
+        bt, ln = pool.fill_tables(seqs, width)
+        b.tables, b.lens = bt.numpy(), ln.numpy()
+        assert np.array_equal(host(lens), b.lens)
+        assert_decode(out, b, "step %d" % i)
+    assert host(state)[1] == pool.num_free() and pa.pa_get_device_error() == 0
