@@ -94,13 +94,14 @@ def write(cache: np.ndarray, key, value, slots, key_scale: float = 1.0, value_sc
 def decode(query: np.ndarray, cache: np.ndarray, tables, lens, scale: float,
            key_scale: float = 1.0, value_scale: float = 1.0):
     """Decode attention [S, Hq, D] in binary64.  Also, per output element, the
-    sum of weight * |value| and, per row, the largest scale * sum |q_d k_d|,
-    which bound rounding errors."""
+    sum of weight * |value| and the sum of |value|, and, per row, the largest
+    scale * sum |q_d k_d|, which bound rounding errors."""
     q = query.astype(np.float64)
     s, hq, d = q.shape
     hkv, bs = cache.shape[1], cache.shape[2] * 8
     group = hq // hkv
-    out, mass, reach = np.zeros((s, hq, d)), np.zeros((s, hq, d)), np.zeros((s, hq, 1))
+    out, mass, total = (np.zeros((s, hq, d)) for _ in range(3))
+    reach = np.zeros((s, hq, 1))
     for r in range(s):
         n = int(lens[r])
         if n <= 0:
@@ -114,8 +115,9 @@ def decode(query: np.ndarray, cache: np.ndarray, tables, lens, scale: float,
             w /= w.sum()
             out[r, h] = w @ v[:, h // group]
             mass[r, h] = w @ np.abs(v[:, h // group])
+            total[r, h] = np.abs(v[:, h // group]).sum(0)
             reach[r, h] = abs(scale) * (np.abs(k[:, h // group]) @ np.abs(q[r, h])).max()
-    return out, mass, reach
+    return out, mass, total, reach
 
 
 def extend_tables(tables, lens, new, block_size, num_blocks, max_tokens, ring=None, state=None):

@@ -87,6 +87,11 @@ pa_status device_state(unsigned int** err, int* num_sms) {
   return PA_OK;
 }
 
+long long decode_wait_limit() {
+  const long long limit = g_wait_limit.load();
+  return limit > 0 ? limit : kWaitLimitCycles;
+}
+
 }  // namespace pa
 
 namespace {
@@ -664,8 +669,7 @@ static pa_status decode_impl(void* out, const void* query, const void* cache,
     prm.trace = static_cast<unsigned long long*>(g_trace_buf.load());
     prm.trace_per_role = g_trace_per_role.load();
     prm.trace_bytes = g_trace_bytes.load();
-    const long long limit = g_wait_limit.load();
-    prm.wait_limit = limit > 0 ? limit : pa::kWaitLimitCycles;
+    prm.wait_limit = pa::decode_wait_limit();
     prm.total_items = (int)std::min<long long>((long long)num_seqs * desc->num_kv_heads * max_parts,
                                                (1ll << 31) - 1);
     // With many partitions per sequence most (partition, sequence, head)
@@ -963,8 +967,7 @@ pa_status pa_decode_shared(void* out, const void* query, void* cache, const pa_c
   sp.log2_box_rows = ilog2(R);
   sp.num_stages = pa::shared_stage_slots(D);
   sp.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  const long long limit = g_wait_limit.load();
-  sp.wait_limit = limit > 0 ? limit : pa::kWaitLimitCycles;
+  sp.wait_limit = pa::decode_wait_limit();
   sp.trace = static_cast<unsigned long long*>(g_trace_buf.load());
   sp.trace_per_role = g_trace_per_role.load();
   sp.trace_bytes = g_trace_bytes.load();

@@ -121,11 +121,14 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
 
 pa_status pa_decode_fp4_workspace_size(const pa_cache_desc* desc, int32_t num_heads,
                                        size_t* bytes) {
-  const pa_status st = pa::check_fp4_desc(desc);
+  pa_status st = pa::check_fp4_desc(desc);
   if (st != PA_OK) return st;
   if (!bytes || num_heads < 1 || num_heads % desc->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
   if (num_heads / desc->num_kv_heads > kFp4MaxGroup) return PA_ERR_UNSUPPORTED;
-  *bytes = 256;
+  int sms = 0;
+  if ((st = pa::device_state(nullptr, &sms)) != PA_OK) return st;
+  if (sms > pa::kFp4MaxCtas) return PA_ERR_UNSUPPORTED;
+  *bytes = pa::decode_fp4_workspace_bytes(desc->head_size, num_heads / desc->num_kv_heads, sms);
   return PA_OK;
 }
 
@@ -139,11 +142,12 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
   if (st != PA_OK) return st;
   if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq < 1 || !std::isfinite(scale))
     return PA_ERR_INVALID_ARG;
-  size_t need = 0;
-  if ((st = pa_decode_fp4_workspace_size(desc, num_heads, &need)) != PA_OK) return st;
+  if (num_heads < 1 || num_heads % desc->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (num_heads / desc->num_kv_heads > kFp4MaxGroup || (int64_t)num_seqs * num_heads >= (1ll << 31))
+    return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!out || !query || !cache || !block_tables || !seq_lens || !workspace ||
-      workspace_bytes < need || !aligned(workspace, 256) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(out, 16) ||
       !aligned(query, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
       !aligned(seq_lens, 4) ||
       !stride_ok(query_stride, (int64_t)num_heads * desc->head_size, dtype))
@@ -153,6 +157,9 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
   if (!std::isfinite(p.scale_log2)) return PA_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = pa::device_state(&p.err, &sms)) != PA_OK) return st;
+  size_t need = 0;
+  if ((st = pa_decode_fp4_workspace_size(desc, num_heads, &need)) != PA_OK) return st;
+  if (workspace_bytes < need) return PA_ERR_INVALID_ARG;
   p.out = out;
   p.query = query;
   p.cache = static_cast<const uint8_t*>(cache);
@@ -168,7 +175,9 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
   p.num_seqs = num_seqs;
   p.group = num_heads / desc->num_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
-  return cuda_status(pa::launch_decode_fp4(p, dtype, sms, static_cast<cudaStream_t>(stream)));
+  p.wait_limit = pa::decode_wait_limit();
+  return cuda_status(
+      pa::launch_decode_fp4(p, workspace, dtype, sms, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,

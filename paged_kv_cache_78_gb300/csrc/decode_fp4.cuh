@@ -1,10 +1,37 @@
-// Arguments of the decode attention over a 4-bit pool (see pa_decode_fp4).
+// Arguments of the decode attention over a 4-bit pool (see pa_decode_fp4),
+// and the sizes that its launch and its workspace share.
 #pragma once
 
 #include <stddef.h>
 #include <stdint.h>
 
 namespace pa {
+
+constexpr int kFp4Stage = 32;          // tokens that a warp takes at a time
+constexpr int kFp4HeaderBytes = 8192;  // one counter per CTA
+constexpr int kFp4MaxCtas = kFp4HeaderBytes / 4;
+
+// Two tiles of eight query heads (columns of the matrix instructions) where
+// the registers hold them, one otherwise: groups past eight heads of 256
+// elements then read the keys and values once per tile.
+__host__ __device__ constexpr int fp4_head_tiles(int head_size, int group) {
+  return group > 8 && head_size <= 128 ? 2 : 1;
+}
+
+// Warps of a CTA (one CTA per SM): 16 where a thread's accumulators and query
+// fragments leave room in 128 registers, else 8.
+__host__ __device__ constexpr int fp4_warps(int head_size, int tiles, bool fp32) {
+  return head_size / 16 * tiles * (fp32 ? 8 : 6) <= 48 ? 16 : 8;
+}
+
+// Rows (query heads) of one unit of work, and the floats of its partial
+// result: weighted values, then the maxima, then the sums.
+__host__ __device__ constexpr int fp4_unit_rows(int tiles, int group) {
+  return group < 8 * tiles ? group : 8 * tiles;
+}
+__host__ __device__ constexpr int fp4_partial_floats(int rows, int head_size) {
+  return (rows * (head_size + 2) + 3) / 4 * 4;
+}
 
 struct Fp4DecodeParams {
   void* out;
@@ -13,6 +40,10 @@ struct Fp4DecodeParams {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   unsigned int* err;
+  unsigned int* counters;  // one per CTA, zero between calls
+  float* warp_partials;    // [CTAs][warps][partial]
+  float* cta_partials;     // [CTAs][2][partial]
+  long long wait_limit;
   int64_t query_stride;
   float scale_log2;   // scale * key_scale * log2(e)
   float value_scale;

@@ -114,8 +114,12 @@ cudaError_t launch_fp4_gather(const Fp4Pool& pool, void* key, void* value, int d
 
 // Decode attention over a 4-bit cache.
 struct Fp4DecodeParams;
-cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, int dtype, int num_sms,
-                              cudaStream_t stream);
+size_t decode_fp4_workspace_bytes(int head_size, int group, int num_sms);
+cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, int dtype,
+                              int num_sms, cudaStream_t stream);
+
+// Limit of the tensor-core decodes' pipeline waits (pa_set_decode_wait_limit).
+long long decode_wait_limit();
 
 // Block tables, slot map and positions from request lengths.
 struct TablesParams;

@@ -55,7 +55,7 @@ class Batch:
                           self.key_scale, self.value_scale)
 
 
-def decode_bound(ref, mass, reach, lens, head, dtype):
+def decode_bound(ref, mass, total, reach, lens, head, dtype):
     """How far a decode's outputs may be off, by arithmetic.
 
     Scores: fp32 sums of head products in chains of head / 16 partial sums of
@@ -63,22 +63,26 @@ def decode_bound(ref, mass, reach, lens, head, dtype):
     truncate), and one multiplication and subtraction: 2 * delta relative on a
     weight, delta = (head / 16 + 4) * 2^-22 * reach (plus the query's two
     fp16 parts for fp32 queries, 2^-22).  Weights: rounded to fp16, half a step
-    2^-11 (bf16), or in two parts, 2^-22 (fp32); exp2 within 2^-22.  Sums over
-    tokens: a chain of length n / 16, each step 2^-23.  The result: half a
-    step of its type, 2^-8 or 2^-24."""
+    2^-11 (bf16), or in two parts, 2^-22 (fp32); exp2 within 2^-22.  fp16 has no
+    steps finer than 2^-24, so that a small weight is off by up to 2^-25 where
+    the largest is kept at 2^7 or more: 2^-32 of the sum of |v|, which counts
+    where the values of the large weights are zeros (4-bit values often are).
+    Sums over tokens: a chain of length n / 16, each step 2^-23.  The result:
+    half a step of its type, 2^-8 or 2^-24."""
     n = np.asarray(lens, dtype=np.float64).reshape(-1, 1, 1)
     delta = (head / 16 + 5) * 2.0 ** -22 * reach
     weight = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
     out = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     return (2 * (2 * delta + weight + 2.0 ** -22 + (n / 16 + 16) * 2.0 ** -23) * mass
+            + 2.0 ** -32 * total
             + out * (1 + 2.0 ** -6) * np.abs(ref) + 1e-30)
 
 
 def assert_decode(got: torch.Tensor, batch: Batch, what=""):
-    ref, mass, reach = batch.reference()
+    ref, mass, total, reach = batch.reference()
     g = host(got)
     assert np.isfinite(g).all(), what
-    bound = decode_bound(ref, mass, reach, batch.lens, g.shape[-1], batch.dtype)
+    bound = decode_bound(ref, mass, total, reach, batch.lens, g.shape[-1], batch.dtype)
     worst = float(np.max(np.abs(g - ref) / bound, initial=0.0))
     assert worst <= 1.0, "%s: %.3g times the bound" % (what, worst)
     return worst

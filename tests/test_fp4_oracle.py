@@ -96,13 +96,14 @@ def test_tile_layout_on_a_marked_row():
 
 def test_decode_agrees_with_the_16_bit_oracle():
     b = Batch([0, 1, 9, 70], 6, 2, 64, 16, "fp32", seed=3)
-    ref, mass, reach = b.reference()
+    ref, mass, total, reach = b.reference()
     k, v = fp4.read(b.cache, np.arange(b.cache.shape[0] * 16))
     cache = np.stack([k, v]).reshape(2, -1, 16, 2, 64).astype(np.float32)  # exact
     got = oracle.decode(host(b.query).astype(np.float32), np.nan_to_num(cache), b.tables, b.lens,
                         b.scale)
     assert np.abs(got - ref).max() < 1e-12
-    assert (np.abs(ref) <= mass + 1e-12).all() and (reach[1:] > 0).all()
+    assert (np.abs(ref) <= mass + 1e-12).all() and (mass <= total + 1e-12).all()
+    assert (reach[1:] > 0).all()
 
 
 def test_extend_tables_agrees_with_the_host_pool():
