@@ -17,9 +17,9 @@ size_t partial_floats(int head_size, int group) {
 
 }  // namespace
 
-// Header (the counters), a partial per warp (16 at most), two per CTA.
+// Header (the counters), a partial per warp (16 at most), four per CTA.
 size_t decode_fp4_workspace_bytes(int head_size, int group, int num_sms) {
-  return kFp4HeaderBytes + (size_t)num_sms * (16 + 2) * partial_floats(head_size, group) * 4;
+  return kFp4HeaderBytes + (size_t)num_sms * (16 + 4) * partial_floats(head_size, group) * 4;
 }
 
 cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, int dtype,

@@ -8,8 +8,10 @@
 namespace pa {
 
 constexpr int kFp4Stage = 32;          // tokens that a warp takes at a time
-constexpr int kFp4HeaderBytes = 8192;  // one counter per CTA
-constexpr int kFp4MaxCtas = kFp4HeaderBytes / 4;
+constexpr int kFp4HeaderBytes = 4096;  // three counters per CTA
+
+constexpr int kFp4Gather = 16;         // parts that are merged at once
+constexpr int kFp4MaxCtas = kFp4Gather * kFp4Gather;
 
 // Two tiles of eight query heads (columns of the matrix instructions) where
 // the registers hold them, one otherwise: groups past eight heads of 256
@@ -40,9 +42,9 @@ struct Fp4DecodeParams {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   unsigned int* err;
-  unsigned int* counters;  // one per CTA, zero between calls
+  unsigned int* counters;  // three per CTA, zero between calls
   float* warp_partials;    // [CTAs][warps][partial]
-  float* cta_partials;     // [CTAs][2][partial]
+  float* cta_partials;     // [CTAs][4][partial]: of CTAs, then of groups of CTAs
   long long wait_limit;
   int64_t query_stride;
   float scale_log2;   // scale * key_scale * log2(e)

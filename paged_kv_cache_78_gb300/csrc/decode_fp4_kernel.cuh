@@ -27,6 +27,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "decode_fp4.cuh"
 #include "pa_fp4.cuh"
 
@@ -35,6 +37,7 @@ namespace pa {
 constexpr float kFp4Lift = 7.f;   // weights are 2^(S - m + 7): fp16 keeps small ones
 constexpr float kFp4Slack = 8.f;  // scores may pass the running maximum by this before it moves
 constexpr int kFp4RingBytes = 216 * 1024;
+constexpr int kFp4MaxWork = 1 << 27;  // stages of a launch
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -100,22 +103,25 @@ struct Fp4Place {
   int s, hp, k, n, len;
 };
 
-// What a warp needs to know of a stage that is in its ring.
-struct __align__(16) Fp4Record {
-  int s, hp;
-  int k;
-  int info;  // tokens (1..32), then flags
+// A piece: consecutive stages of one pair in a warp's part.
+struct Fp4Piece {
+  int s, hp;     // the pair
+  int k0, stages;  // its first stage, and how many
+  int n, len;    // stages and tokens of the sequence
 };
-constexpr int kRecBegin = 1 << 8;   // first stage of the pair
-constexpr int kRecFinish = 1 << 9;  // last stage of the pair
-constexpr int kRecLast = 1 << 10;   // last stage of the warp's part
-constexpr int kFp4Records = 8;      // ring of records, at least the stages in flight + 1
+constexpr int kFp4Pieces = 8;  // ring of pieces, at least the stages in flight + 2
 
-// The parts of pairs that a warp leaves behind for the merge: a (ended inside
-// its part, begun before it) in global memory, b (reaches the part's end) in
-// its ring.  Pair numbers, or -1.
-struct Fp4Left {
-  int a, b;
+// The parts of one pair in a CTA: warps `first` .. w, w the last of them,
+// whose run it is.  A part that reaches its warp's end lies in the warp's ring,
+// one that ends before it in global memory.  `at` is the pair's first stage, in
+// all work, and n its stages; s < 0: no run.
+struct Fp4Run {
+  int s, hp, first, at, n;
+};
+
+// A pair that other CTAs have parts of: the first of them, and how many.
+struct Fp4Cross {
+  int s, hp, first, n;
 };
 
 template <typename T, int D, int NT>
@@ -129,13 +135,13 @@ struct Fp4Config {
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kWarpRing = kStages * kStageBytes;
   static constexpr int kBars = kWarps * kWarpRing;
-  static constexpr int kRecs = kBars + 8 * kWarps * kStages;
-  static constexpr int kPre = (kRecs + kWarps * kFp4Records * 16 + 15) / 16 * 16;
-  static constexpr int kLeft = kPre + 8 * (kThreads + 34);
-  static constexpr int kMisc = kLeft + 8 * kWarps;
-  static constexpr int kRuns = kMisc + 64;
-  static constexpr int kSmem = kRuns + 4 * (2 * kWarps + 2);
-  static_assert(kStages >= 2 && kStages < kFp4Records, "ring");
+  static constexpr int kPieces = kBars + 8 * kWarps * kStages;
+  static constexpr int kPre = (kPieces + kWarps * kFp4Pieces * (int)sizeof(Fp4Piece) + 15) / 16 * 16;
+  static constexpr int kRuns = (kPre + 4 * (kThreads + kWarps) + 15) / 16 * 16;
+  static constexpr int kCross = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
+  static constexpr int kGather = (kCross + 2 * (int)sizeof(Fp4Cross) + 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kGather + 8;
+  static_assert(kStages >= 2 && kStages + 2 <= kFp4Pieces, "rings");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(fp4_partial_floats(8 * NT, D) * 4 <= kWarpRing, "a part fits its warp's ring");
 };
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.group;
-  const int head_tiles = (G + 8 * NT - 1) / (8 * NT);
+  const int head_tiles = D == 256 ? (G + 7) / 8 : 1;  // of a KV head (see fp4_head_tiles)
   const int rows = fp4_unit_rows(NT, G);
   const int per_seq = p.num_kv_heads * head_tiles;  // pairs of a sequence
   const int l2bs = p.log2_block_size;
@@ -162,16 +168,22 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * C::kWarpRing;
   const uint32_t bars = smem_u32(smem) + C::kBars + (uint32_t)warp * NS * 8;
-  Fp4Record* recs = reinterpret_cast<Fp4Record*>(smem + C::kRecs) + warp * kFp4Records;
-  long long* pre = reinterpret_cast<long long*>(smem + C::kPre);
-  Fp4Left* left = reinterpret_cast<Fp4Left*>(smem + C::kLeft);
-  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kMisc);
-  int* runs = reinterpret_cast<int*>(smem + C::kRuns);
+  Fp4Piece* pieces = reinterpret_cast<Fp4Piece*>(smem + C::kPieces) + warp * kFp4Pieces;
+  // Stages before each thread's sequences, and all of them; the warps' sums.
+  int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
+  int* pre = warp_sums + W;
+  Fp4Run* runs = reinterpret_cast<Fp4Run*>(smem + C::kRuns);   // [warp][ended before, at its end]
+  Fp4Cross* cross = reinterpret_cast<Fp4Cross*>(smem + C::kCross);  // begun before; ending after
+  volatile int* flag = reinterpret_cast<volatile int*>(cross + 2);
+  const uint32_t gather_bar = smem_u32(smem) + C::kGather;
 
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(bars + 8u * i, 1);
-    fence_mbar_init();
+    runs[2 * warp].s = runs[2 * warp + 1].s = -1;
   }
+  if (tid < 2) cross[tid].s = -1;
+  if (tid == 0) mbar_init(gather_bar, 1);
+  if (lane == 0) fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
 
@@ -180,96 +192,111 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     const int len = p.seq_lens[s];
     *len_out = len;
     if (len <= 0) return 0;
-    if ((((long long)len + (1 << l2bs) - 1) >> l2bs) > p.max_blocks_per_seq) return 0;
-    return (len + kFp4Stage - 1) / kFp4Stage;
+    if (((len - 1) >> l2bs) >= p.max_blocks_per_seq) return 0;
+    return (len - 1) / kFp4Stage + 1;
   };
+  // Sums stop at 2^27 stages (600 GB of reads at 128 elements): lengths that
+  // nobody meant, an error.
   const int chunk = (p.num_seqs + C::kThreads - 1) / C::kThreads;
+  int total;
   {
-    long long mine = 0;
-    for (int i = 0; i < chunk; ++i) {
-      const int s = tid * chunk + i;
-      if (s >= p.num_seqs) break;
+    int mine = 0;
+    for (int s = tid * chunk; s < min((tid + 1) * chunk, p.num_seqs); ++s) {
       int len;
       const int n = stages_of(s, &len);
       if (n == 0 && len > 0 && blockIdx.x == 0) record_error(p.err, PA_DEVERR_SEQ_LEN);
-      mine += n;
+      mine = (int)min((long long)mine + (long long)n * per_seq, (long long)kFp4MaxWork);
     }
-    mine *= per_seq;
-    long long sum = mine;
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum = min(sum + v, kFp4MaxWork);
     }
-    long long* warp_sums = pre + C::kThreads + 1;
     if (lane == 31) warp_sums[warp] = sum;
     __syncthreads();
-    long long base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_sums[w];
-    pre[tid] = base + sum - mine;
-    if (tid == C::kThreads - 1) pre[C::kThreads] = base + sum;
+    const unsigned other = lane < W ? (unsigned)warp_sums[lane] : 0u;
+    const unsigned base = __reduce_add_sync(0xffffffffu, lane < warp ? other : 0u);
+    const unsigned all = __reduce_add_sync(0xffffffffu, other);
+    pre[tid] = (int)base + sum - mine;
+    if (all >= (unsigned)kFp4MaxWork && tid == 0 && blockIdx.x == 0)
+      record_error(p.err, PA_DEVERR_SEQ_LEN);
+    total = all >= (unsigned)kFp4MaxWork ? 0 : (int)all;
     __syncthreads();
   }
-  const long long total = pre[C::kThreads];
-  // Stages of a CTA: an equal share, at least half a stage per warp (fewer
-  // parts to merge where there is little work).
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < W / 2) share = W / 2;
-  const long long cta0 = share * blockIdx.x;
-  const long long cta1 = cta0 + share < total ? cta0 + share : total;
+  // Stages of a CTA: an equal share, at least one per two warps (fewer parts
+  // to merge where there is little work).
+  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, W / 2);
+  const int cta0 = (int)min((long long)share * blockIdx.x, (long long)total);
+  const int cta1 = min(cta0 + share, total);
 
-  auto locate = [&](long long at) -> Fp4Place {
-    int lo = 0, hi = C::kThreads - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    long long acc = pre[lo];
+  // The place of a stage.  All lanes look: the last thread whose sequences
+  // begin at or before it, then the sequence.
+  auto locate = [&](int at) -> Fp4Place {
+    constexpr int kSpan = C::kThreads / 32;
+    const int seg = __popc(__ballot_sync(0xffffffffu, pre[lane * kSpan] <= at)) - 1;
+    const int own = lane < kSpan ? pre[seg * kSpan + lane] : 0x7fffffff;
+    const int off = __popc(__ballot_sync(0xffffffffu, own <= at)) - 1;
+    int acc = __shfl_sync(0xffffffffu, own, off);
     Fp4Place pl;
-    pl.s = lo * chunk;
+    pl.s = (seg * kSpan + off) * chunk;
     while (true) {
       pl.n = stages_of(pl.s, &pl.len);
-      const long long next = acc + (long long)pl.n * per_seq;
+      const int next = acc + pl.n * per_seq;
       if (next > at) break;
       acc = next;
       ++pl.s;
     }
-    const long long rem = at - acc;
-    pl.hp = (int)(rem / pl.n);
-    pl.k = (int)(rem - (long long)pl.hp * pl.n);
+    const int rem = at - acc;
+    pl.hp = rem / pl.n;
+    pl.k = rem - pl.hp * pl.n;
     return pl;
   };
 
   bool ok = true;
-  if (lane == 0) left[warp] = Fp4Left{-1, -1};
-  const long long share_w = (share + W - 1) / W;
-  const long long my0 = cta0 + share_w * warp;
-  const long long my1 = my0 + share_w < cta1 ? my0 + share_w : cta1;
+  const int share_w = (share + W - 1) / W;
+  const int my0 = cta0 + share_w * warp;
+  const int my1 = min(my0 + share_w, cta1);
+  if (warp == W - 1 && cta0 < cta1) {
+    const Fp4Place pl = locate(cta1 - 1);
+    const int at = cta1 - 1 - pl.k;
+    // Ends after this CTA; a pair that also began before counts as begun before.
+    if (lane == 0 && pl.k + 1 < pl.n && at >= cta0)
+      cross[1] = Fp4Cross{pl.s, pl.hp, (int)blockIdx.x, (at + pl.n - 1) / share -
+                                                                       (int)blockIdx.x + 1};
+  }
   if (my0 < my1) {
-    const int count = (int)(my1 - my0);  // a launch has far fewer than 2^31 stages per warp
-    Fp4Place pp = locate(my0);           // the next stage to prepare
-    int prepared = 0, issued = 0;
-    int ids[NS];  // table entries of prepared stages, one block per lane
+    const int count = my1 - my0;
+    const int per_block = l2bs >= 5 ? kFp4Stage / kFp4Tile : 1 << (l2bs - 3);  // tiles of a copy
+    const uint32_t lane_dst = (uint32_t)(lane * per_block) * C::kTileBytes;
+    const size_t block_bytes = ((size_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
 
-    // Record the next stage and fetch its table entries.
-    auto prepare = [&]() -> int {
-      const int tok0 = pp.k * kFp4Stage;
-      const int tokens = min(kFp4Stage, pp.len - tok0);
-      if (lane == 0) {
-        Fp4Record r;
-        r.s = pp.s;
-        r.hp = pp.hp;
-        r.k = pp.k;
-        r.info = tokens | (pp.k == 0 ? kRecBegin : 0) | (pp.k + 1 == pp.n ? kRecFinish : 0) |
-                 (prepared + 1 == count ? kRecLast : 0);
-        recs[prepared % kFp4Records] = r;
-      }
-      const int first = tok0 >> l2bs;
-      const int blocks = ((tok0 + tokens - 1) >> l2bs) - first + 1;
-      int id = 0;
-      if (lane < blocks) id = __ldg(p.block_tables + (size_t)pp.s * p.max_blocks_per_seq + first + lane);
-      if (++prepared < count && ++pp.k == pp.n) {
+    // ---- producer: the next stage to copy, its table entry already fetched ----
+    Fp4Place pp = locate(my0);
+    if (warp == 0 && lane == 0 && pp.k > 0) {
+      const int at = my0 - pp.k, c0 = at / share;
+      cross[0] = Fp4Cross{pp.s, pp.hp, c0, (at + pp.n - 1) / share - c0 + 1};
+    }
+    int entered = 0, fetched = 0, issued = 0;
+    const int32_t* table = nullptr;  // the sequence's row, from this lane's block
+    const uint8_t* head_base = nullptr;
+    auto enter = [&]() {  // a piece begins
+      table = p.block_tables + (size_t)pp.s * p.max_blocks_per_seq + lane;
+      const int h = pp.hp / head_tiles;
+      head_base = p.cache + ((size_t)h << (l2bs - 3)) * C::kTileBytes;
+      if (lane == 0)
+        pieces[entered % kFp4Pieces] =
+            Fp4Piece{pp.s, pp.hp, pp.k, min(pp.n - pp.k, count - fetched), pp.n, pp.len};
+      ++entered;
+    };
+    struct Next {
+      int id, tiles;
+      const uint8_t* base;
+    };
+    auto fetch = [&]() -> Next {
+      if (fetched == 0) {
+        enter();
+      } else if (++pp.k == pp.n) {
         pp.k = 0;
         if (++pp.hp == per_seq) {
           pp.hp = 0;
@@ -278,116 +305,69 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
             pp.n = stages_of(pp.s, &pp.len);
           } while (pp.n == 0);
         }
+        enter();
       }
-      return id;
+      ++fetched;
+      const int tok0 = pp.k * kFp4Stage;
+      Next nx;
+      nx.tiles = min(kFp4Stage / kFp4Tile, (pp.len - tok0 + kFp4Tile - 1) / kFp4Tile);
+      nx.base = head_base + ((tok0 & ((1 << l2bs) - 1)) >> 3) * C::kTileBytes;
+      nx.id = lane * per_block < nx.tiles ? __ldg(table + (tok0 >> l2bs)) : 0;
+      return nx;
     };
-    // Copy the next stage's tiles into its slot: one range per block.
-    auto issue = [&](int id) {
-      __syncwarp();
-      const Fp4Record r = recs[issued % kFp4Records];
-      const int slot = issued % NS;
-      const int tokens = r.info & 255;
-      const int tiles = (tokens + kFp4Tile - 1) / kFp4Tile;
-      const int tok0 = r.k * kFp4Stage;
-      const int in_block = (tok0 & ((1 << l2bs) - 1)) >> 3;  // first tile (blocks of 64 and more)
-      const int per_block = l2bs >= 5 ? kFp4Stage / kFp4Tile : 1 << (l2bs - 3);
-      const int mine = min(per_block, tiles - lane * per_block);
-      const bool live = mine > 0;
-      const bool good = live && id >= 0 && id < p.num_blocks;
+    // One copy per block into slot `slot`.
+    auto issue = [&](const Next& nx, int slot) {
       const uint32_t bar = bars + 8u * slot;
-      const uint32_t dst = ring + slot * C::kStageBytes + lane * per_block * C::kTileBytes;
-      const uint32_t bytes = good ? (uint32_t)mine * C::kTileBytes : 0u;
-      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+      const uint32_t dst = ring + slot * C::kStageBytes + lane_dst;
+      const int mine = min(per_block, nx.tiles - lane * per_block);
+      const bool bad = (unsigned)nx.id >= (unsigned)p.num_blocks;  // false in lanes without a block
       __syncwarp();
-      if (good) {
-        const int h = r.hp / head_tiles;
-        const size_t tile = (((size_t)id * p.num_kv_heads + h) << (l2bs - 3)) + in_block;
-        bulk_load(dst, p.cache + tile * C::kTileBytes, bytes, bar);
-      } else if (live) {
+      if (!__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nx.tiles * C::kTileBytes);
+        if (mine > 0)
+          bulk_load(dst, nx.base + (size_t)nx.id * block_bytes, (uint32_t)mine * C::kTileBytes, bar);
+      } else {
         // A block outside the pool: zero keys and values.
-        record_error(p.err, PA_DEVERR_BLOCK_ID);
-        for (int i = 0; i < mine * C::kTileBytes; i += 16)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i), "r"(0u) : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        const uint32_t bytes = mine > 0 && !bad ? (uint32_t)mine * C::kTileBytes : 0u;
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+        if (bytes) bulk_load(dst, nx.base + (size_t)nx.id * block_bytes, bytes, bar);
+        if (bad) {
+          record_error(p.err, PA_DEVERR_BLOCK_ID);
+          for (int i = 0; i < mine * C::kTileBytes; i += 16)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i), "r"(0u)
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
       }
       ++issued;
     };
 
-    // Prologue: fill the ring, every table entry on its way before the first
-    // is needed.
+    Next next;
+    {
+      // Fill the ring, every table entry on its way before the first is needed.
+      Next first[NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) ids[i] = i < count ? prepare() : 0;
+      for (int i = 0; i < NS; ++i)
+        if (i < count) first[i] = fetch();
+      if (NS < count) next = fetch();
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (i < count) issue(ids[i]);
-    int next_id = NS < count ? prepare() : 0;
+      for (int i = 0; i < NS; ++i)
+        if (i < count) issue(first[i], i);
+    }
 
     uint32_t q[kQParts][NT][kSteps][2];  // Q^T: head g of tile nt, this thread's elements
     float o[NT][kSteps][4];              // O^T: rows 2j, 2j + 1 of chunk g; heads 2t, 2t + 1
     float cs[NT][2], m[NT][2], l[NT][2];
+    int slot = 0;
+    uint32_t parity = 0;
+    bool fresh = true;  // the piece has no maximum yet
 
-    for (int i = 0; i < count; ++i) {
-      const int slot = i % NS;
-      __syncwarp();
-      const Fp4Record r = recs[i % kFp4Records];
-      const int tokens = r.info & 255;
-      const int h = r.hp / head_tiles, ht = r.hp - h * head_tiles;
-      const int head0 = h * G + ht * 8 * NT;  // first query head of the unit
-      const int heads = min(8 * NT, G - ht * 8 * NT);
-      if (i == 0 || (r.info & kRecBegin)) {
-        // ---- the pair's queries ----
-        // fp16 holds a row scaled by a power of two to a maximum in [2^13, 2^14)
-        // (bf16 exactly, unless an element is 2^-30 of the largest).
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int head = nt * 8 + g;
-          float x[D / 4];
-          if (head < heads) {
-            const T* src = static_cast<const T*>(p.query) + r.s * p.query_stride +
-                           (size_t)(head0 + head) * D + t * (D / 4);
-            constexpr int kPer = ElemTraits<T>::kPerChunk;
-#pragma unroll
-            for (int c = 0; c < D / 4 / kPer; ++c)
-              ElemTraits<T>::unpack(ldg_nc_v4(src + c * kPer), x + c * kPer);
-          } else {
-#pragma unroll
-            for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
-          }
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < D / 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const uint32_t ex = max(top >> 23, 14u);
-          const float up = __uint_as_float((267u - ex) << 23);
-          const float down = __uint_as_float((ex - 13u) << 23);
-          cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
-          cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
-#pragma unroll
-          for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float x0 = x[4 * j + 2 * b] * up, x1 = x[4 * j + 2 * b + 1] * up;
-              const uint32_t hi = pack_half2(x0, x1);
-              q[0][nt][j][b] = hi;
-              if constexpr (kF32) q[1][nt][j][b] = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
-            }
-          m[nt][0] = m[nt][1] = -INFINITY;
-          l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
-        }
-      }
-      {
-        const bool w = mbar_wait_bounded(bars + 8u * slot, (i / NS) & 1, p.err, p.wait_limit);
-        ok = __all_sync(0xffffffffu, w);
-        if (!ok) break;
-      }
-      const uint32_t stage = ring + slot * C::kStageBytes;
-
+    // One stage in `stage`, its first `tokens` tokens valid.  One body for whole
+    // and for ragged stages: the branches below are small and the same for the
+    // warp, where a second body would be fetched anew at every sequence's end.
+    auto attend = [&](const uint32_t stage, const int tokens) {
+      const bool ragged = tokens < kFp4Stage;
       // ---- scores of 32 tokens: rows g (tile 2u) and g + 8 (tile 2u + 1) ----
       float sc[2][NT][4];
 #pragma unroll
@@ -446,25 +426,46 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       }
 
       // ---- softmax: the maximum moves only when a score passes it by 2^8 ----
-      const bool whole = tokens == kFp4Stage;
-      float over = -INFINITY;
+      float y[2][NT][4];
+      auto weigh = [&]() {  // exponents; their maximum of this thread
+        float over = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            sc[u][nt][c] *= cs[nt][c & 1];
-            if (!whole && u * 16 + (c >> 1) * 8 + g >= tokens) sc[u][nt][c] = -INFINITY;
-            over = fmaxf(over, sc[u][nt][c] - m[nt][c & 1]);
-          }
-      if (__any_sync(0xffffffffu, over > kFp4Lift + kFp4Slack)) {
+            for (int c = 0; c < 4; ++c)
+              y[u][nt][c] = fmaf(sc[u][nt][c], cs[nt][c & 1], -m[nt][c & 1]);
+        if (ragged) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (u * 16 + (c >> 1) * 8 + g >= tokens) y[u][nt][c] = -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) over = fmaxf(over, y[u][nt][c]);
+        return over;
+      };
+      if (fresh || __any_sync(0xffffffffu, weigh() > kFp4Lift + kFp4Slack)) {
+        fresh = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float top = group_max<4>(fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + 2]),
-                                                 fmaxf(sc[1][nt][c], sc[1][nt][c + 2])));
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int e = c; e < 4; e += 2)
+                if (u * 16 + (e >> 1) * 8 + g < tokens) top = fmaxf(top, sc[u][nt][e] * cs[nt][c]);
+            top = group_max<4>(top);
             const float m_new = fmaxf(m[nt][c], top - kFp4Lift);
             const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m[nt][c] - m_new);
             m[nt][c] = m_new;
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
               o[nt][j][c + 2] *= alpha;
             }
           }
+        weigh();
       }
       uint32_t pt[kQParts][2][NT][2];  // P^T: head g; tokens 2t, 2t + 1 of tile 2u (+ 1)
 #pragma unroll
@@ -483,8 +485,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float w0 = fast_exp2(sc[u][nt][2 * e] - m[nt][0]);
-            const float w1 = fast_exp2(sc[u][nt][2 * e + 1] - m[nt][1]);
+            const float w0 = fast_exp2(y[u][nt][2 * e]);
+            const float w1 = fast_exp2(y[u][nt][2 * e + 1]);
             l[nt][0] += w0;
             l[nt][1] += w1;
             const uint32_t two = pack_half2(w0, w1);
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
               wb[1] = v.w;
             }
             uint32_t two = lds_u16(tile + fp4_value_scales(D) + group * 8 + 2 * t);
-            if (!whole) {
+            if (ragged) {
               // Rows past the sequence's end hold anything: a zero scale.
               const int tok = u * 16 + e * 8 + 2 * t;
               if (tok >= tokens) two = 0;
@@ -552,90 +554,155 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           }
         }
       }
+    };
 
-      // ---- the slot is free: the next stage ----
-      if (issued < count) {
-        issue(next_id);
-        if (prepared < count) next_id = prepare();
+    for (int done = 0, piece = 0; done < count && ok; ++piece) {
+      __syncwarp();
+      const Fp4Piece pc = pieces[piece % kFp4Pieces];
+      const int h = pc.hp / head_tiles, ht = pc.hp - h * head_tiles;
+      const int head0 = h * G + ht * 8 * NT;  // first query head of the unit
+      const int heads = min(8 * NT, G - ht * 8 * NT);
+      // ---- the pair's queries ----
+      // fp16 holds a row scaled by a power of two to a maximum in [2^13, 2^14)
+      // (bf16 exactly, unless an element is 2^-30 of the largest).
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int head = nt * 8 + g;
+        float x[D / 4];
+        if (head < heads) {
+          const T* src = static_cast<const T*>(p.query) + pc.s * p.query_stride +
+                         (size_t)(head0 + head) * D + t * (D / 4);
+          constexpr int kPer = ElemTraits<T>::kPerChunk;
+#pragma unroll
+          for (int c = 0; c < D / 4 / kPer; ++c)
+            ElemTraits<T>::unpack(ldg_nc_v4(src + c * kPer), x + c * kPer);
+        } else {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t ex = max(top >> 23, 14u);
+        const float up = __uint_as_float((267u - ex) << 23);
+        const float down = __uint_as_float((ex - 13u) << 23);
+        cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
+        cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float x0 = x[4 * j + 2 * b] * up, x1 = x[4 * j + 2 * b + 1] * up;
+            const uint32_t hi = pack_half2(x0, x1);
+            q[0][nt][j][b] = hi;
+            if constexpr (kF32) q[1][nt][j][b] = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+          }
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
       }
+      fresh = true;
+      for (int k = pc.k0; k < pc.k0 + pc.stages; ++k) {
+        const bool w = mbar_wait_bounded(bars + 8u * slot, parity, p.err, p.wait_limit);
+        ok = __all_sync(0xffffffffu, w);
+        if (!ok) break;
+        const uint32_t stage = ring + slot * C::kStageBytes;
+        const int tokens = pc.len - k * kFp4Stage;
+        attend(stage, min(tokens, kFp4Stage));
+        // The slot is free: the next stage.
+        if (issued < count) {
+          issue(next, slot);
+          if (fetched < count) next = fetch();
+        }
+        if (++slot == NS) {
+          slot = 0;
+          parity ^= 1;
+        }
+      }
+      if (!ok) break;
+      done += pc.stages;
 
-      // ---- the end of the pair, or of the warp's part ----
-      if (r.info & (kRecFinish | kRecLast)) {
-        const bool begun = (r.info & kRecFinish) ? i - r.k >= 0 : false;
-        // Sums over the tokens' lanes.
-        float ls[NT][2];
+      // ---- the piece is done ----
+      // Sums over the tokens' lanes.
+      float ls[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v = l[nt][c];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+          ls[nt][c] = v;
+        }
+      if (pc.k0 == 0 && pc.stages == pc.n) {
+        // The whole pair: final rows.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = l[nt][c];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-            ls[nt][c] = v;
-          }
-        if (begun) {
-          // The whole pair: final rows.
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int head = nt * 8 + 2 * t + c;
-              if (head >= heads) continue;
-              const float inv = p.value_scale / ls[nt][c];
-              T* dst = static_cast<T*>(p.out) +
-                       ((size_t)r.s * p.num_heads + head0 + head) * D + g * (D / 8);
-              if constexpr (kF32) {
-#pragma unroll
-                for (int j = 0; j < kSteps; j += 2)
-                  *reinterpret_cast<float4*>(dst + 2 * j) =
-                      make_float4(o[nt][j][c] * inv, o[nt][j][c + 2] * inv, o[nt][j + 1][c] * inv,
-                                  o[nt][j + 1][c + 2] * inv);
-              } else {
-#pragma unroll
-                for (int j = 0; j < kSteps; j += 4) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int b = 0; b < 4; ++b)
-                    w[b] = pack_bf16x2(o[nt][j + b][c] * inv, o[nt][j + b][c + 2] * inv);
-                  stg_v4(dst + 2 * j, make_uint4(w[0], w[1], w[2], w[3]));
-                }
-              }
-            }
-        } else {
-          // A part: to the ring at the end of the warp's part (every copy has
-          // landed and been read), to global memory before.
-          const bool last = (r.info & kRecLast) != 0;
-          float* dst = last ? reinterpret_cast<float*>(smem + warp * C::kWarpRing)
-                            : p.warp_partials + ((size_t)blockIdx.x * W + warp) * part_floats;
-          __syncwarp();
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int head = nt * 8 + 2 * t + c;
-              if (head >= heads) continue;
-              float* od = dst + head * D + g * (D / 8);
+            const int head = nt * 8 + 2 * t + c;
+            if (head >= heads) continue;
+            const float inv = p.value_scale / ls[nt][c];
+            T* dst = static_cast<T*>(p.out) +
+                     ((size_t)pc.s * p.num_heads + head0 + head) * D + g * (D / 8);
+            if constexpr (kF32) {
 #pragma unroll
               for (int j = 0; j < kSteps; j += 2)
-                *reinterpret_cast<float4*>(od + 2 * j) =
-                    make_float4(o[nt][j][c], o[nt][j][c + 2], o[nt][j + 1][c], o[nt][j + 1][c + 2]);
-              if (g == 0) {
-                dst[rows * D + head] = m[nt][c];
-                dst[rows * D + rows + head] = ls[nt][c];
+                *reinterpret_cast<float4*>(dst + 2 * j) =
+                    make_float4(o[nt][j][c] * inv, o[nt][j][c + 2] * inv, o[nt][j + 1][c] * inv,
+                                o[nt][j + 1][c + 2] * inv);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kSteps; j += 4) {
+                uint32_t w[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                  w[b] = pack_bf16x2(o[nt][j + b][c] * inv, o[nt][j + b][c + 2] * inv);
+                stg_v4(dst + 2 * j, make_uint4(w[0], w[1], w[2], w[3]));
               }
             }
-          if (lane == 0) {
-            const int pair = r.s * per_seq + r.hp;
-            if (last) left[warp].b = pair;
-            else left[warp].a = pair;
           }
+      } else {
+        // A part: to the ring at the end of the warp's part (every copy has
+        // landed and been read), to global memory before.
+        const bool last = done == count;
+        float* dst = last ? reinterpret_cast<float*>(smem + warp * C::kWarpRing)
+                          : p.warp_partials + ((size_t)blockIdx.x * W + warp) * part_floats;
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int head = nt * 8 + 2 * t + c;
+            if (head >= heads) continue;
+            float* od = dst + head * D + g * (D / 8);
+#pragma unroll
+            for (int j = 0; j < kSteps; j += 2)
+              *reinterpret_cast<float4*>(od + 2 * j) =
+                  make_float4(o[nt][j][c], o[nt][j][c + 2], o[nt][j + 1][c], o[nt][j + 1][c + 2]);
+            if (g == 0) {
+              dst[rows * D + head] = m[nt][c];
+              dst[rows * D + rows + head] = ls[nt][c];
+            }
+          }
+        // The warp with the pair's last part in this CTA says where the parts are.
+        if (lane == 0 && (pc.k0 + pc.stages == pc.n || my0 + done == cta1)) {
+          const int at = my0 + done - pc.stages - pc.k0;
+          runs[2 * warp + last] =
+              Fp4Run{pc.s, pc.hp, at <= cta0 ? 0 : (at - cta0) / share_w, at, pc.n};
         }
       }
     }
     if (!ok) {
       // A wait gave up: this warp's copies in flight end before it leaves.
-      for (int i = max(0, issued - NS); i < issued; ++i)
-        mbar_wait_bounded(bars + 8u * (i % NS), (i / NS) & 1, p.err);
+      // Slot i's last copy is its (issued - 1 - i) / NS + 1-th.
+      for (int i = 0; i < NS && i < issued; ++i)
+        mbar_wait_bounded(bars + 8u * i, ((issued - 1 - i) / NS) & 1, p.err);
     }
   }
 
@@ -647,128 +714,163 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         stg_v4(dst + i, make_uint4(0u, 0u, 0u, 0u));
     }
 
-  // ---- merge over the CTA's warps ----
+  // ---- merges ----
+  // First over the CTA's warps; then, for pairs that reach over the CTA's ends,
+  // over CTAs, each by the last to arrive, up to kFp4Gather parts at a time (one
+  // SM would take 8 us for a part of 8 heads of 256 elements from every SM): the
+  // groups of a pair's CTAs, then their results, copied into the rings' memory.
+  // A CTA has two counters for groups, of the pair that it begins and of the one
+  // that it continues, and one for the results of the pair that it begins.  One
+  // short body for all: code that runs once is paid by its length (unrolled over
+  // the 16 parts it took 2 us longer).
   if (cta0 >= cta1) return;  // the same for the whole CTA
-  __syncthreads();
-  // The pairs that reach over the CTA's ends (the same for every thread).
-  const Fp4Place first = locate(cta0), final_ = locate(cta1 - 1);
-  const int head_pair = first.k > 0 ? first.s * per_seq + first.hp : -1;
-  const int tail_pair = final_.k + 1 < final_.n ? final_.s * per_seq + final_.hp : -1;
-  // Runs of parts of one pair: part 2w is warp w's a, part 2w + 1 its b; runs[]
-  // holds the first part of each run, and the end.
-  if (tid == 0) {
-    int count = 0, last_pair = -1, end = 0;
-    for (int i = 0; i < 2 * W; ++i) {
-      const int pair = (i & 1) ? left[i >> 1].b : left[i >> 1].a;
-      if (pair < 0) continue;
-      if (pair != last_pair) runs[count++] = i;
-      last_pair = pair;
-      end = i + 1;
-    }
-    runs[count] = end;
-    misc[0] = count;
-  }
-  __syncthreads();
-  const int num_runs = misc[0];
-  auto part_at = [&](int i) -> const float* {
-    return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * C::kWarpRing)
-                   : p.warp_partials + ((size_t)blockIdx.x * W + (i >> 1)) * part_floats;
-  };
-  auto part_pair = [&](int i) { return (i & 1) ? left[i >> 1].b : left[i >> 1].a; };
-  constexpr int kLaneCols = D / 32;
-  auto write_row = [&](int pair, int head, const float* acc, float sum) {
-    const int s = pair / per_seq, hp = pair - s * per_seq;
-    const int h = hp / head_tiles, ht = hp - h * head_tiles;
-    const float inv = p.value_scale / sum;
-    T* dst = static_cast<T*>(p.out) +
-             ((size_t)s * p.num_heads + h * G + ht * 8 * NT + head) * D + lane * kLaneCols;
-#pragma unroll
-    for (int e = 0; e < kLaneCols; ++e) dst[e] = ElemTraits<T>::from_float(acc[e] * inv);
-  };
-  auto heads_of = [&](int pair) {
-    const int ht = pair % head_tiles;  // per_seq is a multiple of head_tiles
-    return min(8 * NT, G - ht * 8 * NT);
-  };
-  for (int unit = warp; unit < num_runs * rows; unit += W) {
-    const int run = unit / rows, head = unit - run * rows;
-    const int i0 = runs[run], i1 = runs[run + 1];
-    const int pair = part_pair(i0);
-    if (head >= heads_of(pair)) continue;
-    float top = -INFINITY;
-    for (int i = i0; i < i1; ++i)
-      if (part_pair(i) == pair) top = fmaxf(top, part_at(i)[rows * D + head]);
-    float acc[kLaneCols], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kLaneCols; ++e) acc[e] = 0.f;
-    for (int i = i0; i < i1; ++i) {
-      if (part_pair(i) != pair) continue;
-      const float* src = part_at(i);
-      const float mi = src[rows * D + head];
-      const float w = mi == top ? 1.f : fast_exp2(mi - top);
-      sum = fmaf(src[rows * D + rows + head], w, sum);
-#pragma unroll
-      for (int e = 0; e < kLaneCols; ++e)
-        acc[e] = fmaf(src[head * D + lane * kLaneCols + e], w, acc[e]);
-    }
-    if (pair != head_pair && pair != tail_pair) {
-      write_row(pair, head, acc, sum);
+  constexpr int kVec = D == 256 ? 4 : 2;   // columns of a lane
+  constexpr int kSplit = D / (32 * kVec);  // units of a head
+  static_assert(W <= kFp4Gather, "a run's parts");
+  static_assert(kFp4Gather * fp4_partial_floats(8 * NT, D) * 4 <= C::kBars, "gathered parts");
+  const uint32_t part_bytes = 4u * part_floats;
+  uint32_t gathers = 0;
+  for (int phase = 0; phase < 3; ++phase) {
+    __syncthreads();
+    uint32_t live;
+    if (phase == 0) {
+      live = __ballot_sync(0xffffffffu, lane < 2 * W && runs[lane % (2 * W)].s >= 0);
     } else {
-      float* dst = p.cta_partials +
-                   ((size_t)blockIdx.x * 2 + (pair == head_pair ? 0 : 1)) * part_floats;
-#pragma unroll
-      for (int e = 0; e < kLaneCols; ++e) dst[head * D + lane * kLaneCols + e] = acc[e];
-      if (lane == 0) {
-        dst[rows * D + head] = top;
-        dst[rows * D + rows + head] = sum;
+      if (tid < 2) {
+        const Fp4Cross cr = cross[tid];
+        bool go = cr.s >= 0 && (phase == 1 || (flag[tid] && cr.n > kFp4Gather));
+        if (go) {
+          const int group = ((int)blockIdx.x - cr.first) / kFp4Gather;
+          const int wait = phase == 2 ? (cr.n + kFp4Gather - 1) / kFp4Gather
+                                      : min(kFp4Gather, cr.n - group * kFp4Gather);
+          unsigned int* counter = p.counters + 3 * cr.first +
+                                  (phase == 2 ? 2 : 3 * group * kFp4Gather + (group == 0));
+          unsigned int before;
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(counter)
+                       : "memory");
+          go = before == (unsigned)wait - 1;
+          if (go) *counter = 0u;
+        }
+        flag[tid] = go;
       }
+      __syncthreads();
+      live = (flag[0] ? 1u : 0u) | (flag[1] ? 2u : 0u);
+      if (live == 0) return;
     }
-  }
-  if (head_pair < 0 && tail_pair < 0) return;
-
-  // ---- merge over CTAs, by the last of a pair's CTAs to arrive ----
-  __threadfence();
-  __syncthreads();
-  // CTAs of a pair: from the one with its first stage to the one with its last.
-  const long long head_at = cta0 - first.k, tail_at = cta1 - 1 - final_.k;
-  for (int which = 0; which < 2; ++which) {
-    const int pair = which == 0 ? head_pair : tail_pair;
-    if (pair < 0 || (which == 1 && tail_pair == head_pair)) continue;
-    const long long at = which == 0 ? head_at : tail_at;
-    const int n = which == 0 ? first.n : final_.n;
-    const int c0 = (int)(at / share), c1 = (int)((at + n - 1) / share);
-    if (tid == 0) {
-      const unsigned int before = atomicAdd(p.counters + c0, 1u);
-      const bool last = before == (unsigned)(c1 - c0);
-      if (last) p.counters[c0] = 0u;
-      misc[1] = last;
-    }
-    __syncthreads();
-    const bool last = misc[1] != 0;
-    __syncthreads();
-    if (!last) continue;
-    __threadfence();
-    for (int head = warp; head < heads_of(pair); head += W) {
-      auto src_of = [&](int c) {
-        return p.cta_partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats;
-      };
-      float top = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(src_of(c) + rows * D + head));
-      top = group_max<1>(top);
-      float acc[kLaneCols], sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < kLaneCols; ++e) acc[e] = 0.f;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float* src = src_of(c);
-        const float mi = __ldcg(src + rows * D + head);
+    // Phase 0: a warp takes units of all runs in turn; after that, one pair at
+    // a time.
+    const int passes = phase == 0 ? 1 : 2;
+    for (int pass = 0; pass < passes; ++pass) {
+      if (phase > 0 && !(live >> pass & 1)) continue;
+      Fp4Cross cr;
+      int n = 0, g0 = 0;
+      if (phase > 0) {
+        // Of CTA j of the pair: its part (slot 0; 1 if j is the first), its
+        // group's result (2; 3).
+        cr = cross[pass];
+        g0 = phase == 2 ? 0 : ((int)blockIdx.x - cr.first) / kFp4Gather * kFp4Gather;
+        n = phase == 2 ? (cr.n + kFp4Gather - 1) / kFp4Gather : min(kFp4Gather, cr.n - g0);
+        // Copies read and write after this CTA's accesses to the rings and the
+        // other CTAs' stores.
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncthreads();
+        if (warp == 0) {
+          asm volatile("fence.proxy.async;" ::: "memory");
+          if (lane == 0) mbar_arrive_expect_tx(gather_bar, (uint32_t)n * part_bytes);
+          __syncwarp();
+          if (lane < n) {
+            const int j = phase == 2 ? lane * kFp4Gather : g0 + lane;
+            const int slot = (phase == 2 ? 2 : 0) + (j == 0);
+            bulk_load(smem_u32(smem) + lane * part_bytes,
+                      p.cta_partials + ((size_t)(cr.first + j) * 4 + slot) * part_floats,
+                      part_bytes, gather_bar);
+          }
+        }
+        mbar_wait_bounded(gather_bar, gathers & 1, p.err);
+        ++gathers;
+      }
+      const int per_run = rows * kSplit;
+      const int all_units = phase == 0 ? __popc(live) * per_run : per_run;
+      for (int u = warp; u < all_units; u += W) {
+        const int unit = u % per_run;
+        const int head = unit / kSplit;
+        const int col = unit * 32 * kVec + lane * kVec;
+        // Parts i < n lie `step` bytes apart from `base` on, but for part `odd`.
+        const uint8_t* base = smem;
+        const float* odd_part = nullptr;
+        uint32_t step = part_bytes;
+        int odd = -1, s, hp;
+        float* to = nullptr;  // the merged part, or NULL: final rows
+        if (phase == 0) {
+          uint32_t left = live;
+          for (int skip = u / per_run; skip > 0; --skip) left &= left - 1;
+          const int which = __ffs(left) - 1;
+          const Fp4Run run = runs[which];
+          s = run.s;
+          hp = run.hp;
+          n = (which >> 1) - run.first + 1;
+          base = smem + run.first * C::kWarpRing;
+          step = C::kWarpRing;
+          if (!(which & 1)) {
+            odd = n - 1;
+            odd_part = p.warp_partials + ((size_t)blockIdx.x * W + (which >> 1)) * part_floats;
+          }
+          const bool before = run.at < cta0;
+          if (before || run.at + run.n > cta1)
+            to = p.cta_partials + ((size_t)blockIdx.x * 4 + !before) * part_floats;
+        } else {
+          s = cr.s;
+          hp = cr.hp;
+          if (phase == 1 && cr.n > kFp4Gather)
+            to = p.cta_partials + ((size_t)(cr.first + g0) * 4 + 2 + (g0 == 0)) * part_floats;
+        }
+        const int h = hp / head_tiles, ht = hp - h * head_tiles;
+        if (head >= G - ht * 8 * NT) continue;
+        auto part = [&](int i) {
+          return i == odd ? odd_part : reinterpret_cast<const float*>(base + i * step);
+        };
+        float mi = -INFINITY, li = 0.f;
+        if (lane < n) {
+          const float* src = part(lane) + rows * D + head;
+          mi = src[0];
+          li = src[rows];
+        }
+        const float top = group_max<1>(mi);
         const float w = mi == top ? 1.f : fast_exp2(mi - top);
-        sum = fmaf(__ldcg(src + rows * D + rows + head), w, sum);
+        float sum = lane < n ? li * w : 0.f, acc[kVec];
 #pragma unroll
-        for (int e = 0; e < kLaneCols; ++e)
-          acc[e] = fmaf(__ldcg(src + head * D + lane * kLaneCols + e), w, acc[e]);
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          const float* src = part(i) + col;
+#pragma unroll
+          for (int e = 0; e < kVec; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + e);
+            acc[e] = fmaf(v.x, wi, acc[e]);
+            acc[e + 1] = fmaf(v.y, wi, acc[e + 1]);
+          }
+        }
+        const float inv = to ? 1.f : p.value_scale / sum;
+        T* dst = static_cast<T*>(p.out) + ((size_t)s * p.num_heads + h * G + ht * 8 * NT) * D + col;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 v = make_float2(acc[e] * inv, acc[e + 1] * inv);
+          if (to) *reinterpret_cast<float2*>(to + col + e) = v;
+          else if constexpr (kF32) *reinterpret_cast<float2*>(dst + e) = v;
+          else *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(v.x, v.y);
+        }
+        if (to && col == head * D) {  // the head's first lane
+          to[rows * D + head] = top;
+          to[rows * D + rows + head] = sum;
+        }
       }
-      write_row(pair, head, acc, sum);
     }
+    if (cross[0].s < 0 && cross[1].s < 0) return;
   }
 }
 
