@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kFp4MaxGroup = 16;
 constexpr int32_t kMaxTableTokens = 1 << 30;
-constexpr int64_t kMaxGridUnits = (int64_t)256 * ((1ll << 31) - 1);
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -47,6 +46,11 @@ bool stride_ok(int64_t stride, int64_t row, int32_t dtype) {
   return stride >= row && stride * (dtype == PA_BF16 ? 2 : 4) % 16 == 0;
 }
 
+// One grid holds the call: a CTA per eight tokens and two heads, or more.
+bool grid_ok(const pa_cache_desc* d, int64_t num_tokens) {
+  return (num_tokens + 7) / 8 * d->num_kv_heads < (1ll << 31);
+}
+
 pa::Fp4Pool pool_of(const void* cache, const pa_cache_desc* d) {
   pa::Fp4Pool p;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
@@ -67,7 +71,7 @@ pa_status check_fp4_desc(const pa_cache_desc* d) {
   if (!is_pow2(d->block_size) || d->block_size < 8 || d->block_size > 256)
     return PA_ERR_INVALID_ARG;
   if (d->head_size != 64 && d->head_size != 128 && d->head_size != 256) return PA_ERR_UNSUPPORTED;
-  if (d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (d->num_kv_heads > 65535 || fp4_block_bytes(d) > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
@@ -91,7 +95,7 @@ pa_status pa_reshape_and_cache_fp4(void* cache, const pa_cache_desc* desc, const
   const int64_t row = (int64_t)desc->num_kv_heads * desc->head_size;
   if (!cache || !key || !value || !slot_mapping || !aligned(cache, 16) || !aligned(key, 16) ||
       !aligned(value, 16) || !aligned(slot_mapping, 8) || !stride_ok(key_stride, row, dtype) ||
-      !stride_ok(value_stride, row, dtype) || num_tokens * row / 8 > kMaxGridUnits)
+      !stride_ok(value_stride, row, dtype) || !grid_ok(desc, num_tokens))
     return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = pa::device_state(&err, nullptr)) != PA_OK) return st;
@@ -110,7 +114,7 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
   if (num_tokens == 0) return PA_OK;
   const int64_t row = (int64_t)desc->num_kv_heads * desc->head_size;
   if (!cache || !key || !value || !slot_mapping || !aligned(cache, 16) || !aligned(key, 16) ||
-      !aligned(value, 16) || !aligned(slot_mapping, 8) || num_tokens * row / 8 > kMaxGridUnits)
+      !aligned(value, 16) || !aligned(slot_mapping, 8) || !grid_ok(desc, num_tokens))
     return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = pa::device_state(&err, nullptr)) != PA_OK) return st;

@@ -116,12 +116,14 @@ constexpr int kFp4Pieces = 8;  // ring of pieces, at least the stages in flight 
 // one that ends before it in global memory.  `at` is the pair's first stage, in
 // all work, and n its stages; s < 0: no run.
 struct Fp4Run {
-  int s, hp, first, at, n;
+  int s, head0, heads;  // the pair's sequence and query heads
+  int first, at, n;
 };
 
 // A pair that other CTAs have parts of: the first of them, and how many.
 struct Fp4Cross {
-  int s, hp, first, n;
+  int s, head0, heads;
+  int first, n;
 };
 
 template <typename T, int D, int NT>
@@ -169,6 +171,12 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * C::kWarpRing;
   const uint32_t bars = smem_u32(smem) + C::kBars + (uint32_t)warp * NS * 8;
   Fp4Piece* pieces = reinterpret_cast<Fp4Piece*>(smem + C::kPieces) + warp * kFp4Pieces;
+  // First query head and heads of a pair.
+  auto heads_of = [&](int hp, int* heads) -> int {
+    const int h = hp / head_tiles, ht = hp - h * head_tiles;
+    *heads = min(8 * NT, G - ht * 8 * NT);
+    return h * G + ht * 8 * NT;
+  };
   // Stages before each thread's sequences, and all of them; the warps' sums.
   int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
   int* pre = warp_sums + W;
@@ -261,21 +269,25 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     const Fp4Place pl = locate(cta1 - 1);
     const int at = cta1 - 1 - pl.k;
     // Ends after this CTA; a pair that also began before counts as begun before.
-    if (lane == 0 && pl.k + 1 < pl.n && at >= cta0)
-      cross[1] = Fp4Cross{pl.s, pl.hp, (int)blockIdx.x, (at + pl.n - 1) / share -
-                                                                       (int)blockIdx.x + 1};
+    if (lane == 0 && pl.k + 1 < pl.n && at >= cta0) {
+      int heads;
+      const int head0 = heads_of(pl.hp, &heads), b = (int)blockIdx.x;
+      cross[1] = Fp4Cross{pl.s, head0, heads, b, (at + pl.n - 1) / share - b + 1};
+    }
   }
   if (my0 < my1) {
     const int count = my1 - my0;
     const int per_block = l2bs >= 5 ? kFp4Stage / kFp4Tile : 1 << (l2bs - 3);  // tiles of a copy
     const uint32_t lane_dst = (uint32_t)(lane * per_block) * C::kTileBytes;
-    const size_t block_bytes = ((size_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
+    const uint32_t block_bytes = ((uint32_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
 
     // ---- producer: the next stage to copy, its table entry already fetched ----
     Fp4Place pp = locate(my0);
     if (warp == 0 && lane == 0 && pp.k > 0) {
+      int heads;
+      const int head0 = heads_of(pp.hp, &heads);
       const int at = my0 - pp.k, c0 = at / share;
-      cross[0] = Fp4Cross{pp.s, pp.hp, c0, (at + pp.n - 1) / share - c0 + 1};
+      cross[0] = Fp4Cross{pp.s, head0, heads, c0, (at + pp.n - 1) / share - c0 + 1};
     }
     int entered = 0, fetched = 0, issued = 0;
     const int32_t* table = nullptr;  // the sequence's row, from this lane's block
@@ -325,13 +337,13 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       if (!__any_sync(0xffffffffu, bad)) {
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nx.tiles * C::kTileBytes);
         if (mine > 0)
-          bulk_load(dst, nx.base + (size_t)nx.id * block_bytes, (uint32_t)mine * C::kTileBytes, bar);
+          bulk_load(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, (uint32_t)mine * C::kTileBytes, bar);
       } else {
         // A block outside the pool: zero keys and values.
         const uint32_t bytes = mine > 0 && !bad ? (uint32_t)mine * C::kTileBytes : 0u;
         const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
         if (lane == 0) mbar_arrive_expect_tx(bar, sum);
-        if (bytes) bulk_load(dst, nx.base + (size_t)nx.id * block_bytes, bytes, bar);
+        if (bytes) bulk_load(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, bytes, bar);
         if (bad) {
           record_error(p.err, PA_DEVERR_BLOCK_ID);
           for (int i = 0; i < mine * C::kTileBytes; i += 16)
@@ -559,9 +571,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     for (int done = 0, piece = 0; done < count && ok; ++piece) {
       __syncwarp();
       const Fp4Piece pc = pieces[piece % kFp4Pieces];
-      const int h = pc.hp / head_tiles, ht = pc.hp - h * head_tiles;
-      const int head0 = h * G + ht * 8 * NT;  // first query head of the unit
-      const int heads = min(8 * NT, G - ht * 8 * NT);
+      int heads;
+      const int head0 = heads_of(pc.hp, &heads);
       // ---- the pair's queries ----
       // fp16 holds a row scaled by a power of two to a maximum in [2^13, 2^14)
       // (bf16 exactly, unless an element is 2^-30 of the largest).
@@ -647,7 +658,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           for (int c = 0; c < 2; ++c) {
             const int head = nt * 8 + 2 * t + c;
             if (head >= heads) continue;
-            const float inv = p.value_scale / ls[nt][c];
+            const float inv = __fdividef(p.value_scale, ls[nt][c]);
             T* dst = static_cast<T*>(p.out) +
                      ((size_t)pc.s * p.num_heads + head0 + head) * D + g * (D / 8);
             if constexpr (kF32) {
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         if (lane == 0 && (pc.k0 + pc.stages == pc.n || my0 + done == cta1)) {
           const int at = my0 + done - pc.stages - pc.k0;
           runs[2 * warp + last] =
-              Fp4Run{pc.s, pc.hp, at <= cta0 ? 0 : (at - cta0) / share_w, at, pc.n};
+              Fp4Run{pc.s, head0, heads, at <= cta0 ? 0 : (at - cta0) / share_w, at, pc.n};
         }
       }
     }
@@ -791,25 +802,25 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         mbar_wait_bounded(gather_bar, gathers & 1, p.err);
         ++gathers;
       }
+      // Units of run r are [r * per_run, (r + 1) * per_run); unit u is warp
+      // u mod W's.  Parts i < n lie `step` bytes apart from `base` on, but for
+      // part `odd`.
       const int per_run = rows * kSplit;
-      const int all_units = phase == 0 ? __popc(live) * per_run : per_run;
-      for (int u = warp; u < all_units; u += W) {
-        const int unit = u % per_run;
-        const int head = unit / kSplit;
-        const int col = unit * 32 * kVec + lane * kVec;
-        // Parts i < n lie `step` bytes apart from `base` on, but for part `odd`.
+      uint32_t left = phase == 0 ? live : 1u;
+      for (int u0 = 0; left; left &= left - 1, u0 += per_run) {
+        int unit = (warp - u0) & (W - 1);
+        if (unit >= per_run) continue;
         const uint8_t* base = smem;
         const float* odd_part = nullptr;
         uint32_t step = part_bytes;
-        int odd = -1, s, hp;
+        int odd = -1;
         float* to = nullptr;  // the merged part, or NULL: final rows
         if (phase == 0) {
-          uint32_t left = live;
-          for (int skip = u / per_run; skip > 0; --skip) left &= left - 1;
           const int which = __ffs(left) - 1;
           const Fp4Run run = runs[which];
-          s = run.s;
-          hp = run.hp;
+          cr.s = run.s;
+          cr.head0 = run.head0;
+          cr.heads = run.heads;
           n = (which >> 1) - run.first + 1;
           base = smem + run.first * C::kWarpRing;
           step = C::kWarpRing;
@@ -820,53 +831,53 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           const bool before = run.at < cta0;
           if (before || run.at + run.n > cta1)
             to = p.cta_partials + ((size_t)blockIdx.x * 4 + !before) * part_floats;
-        } else {
-          s = cr.s;
-          hp = cr.hp;
-          if (phase == 1 && cr.n > kFp4Gather)
-            to = p.cta_partials + ((size_t)(cr.first + g0) * 4 + 2 + (g0 == 0)) * part_floats;
+        } else if (phase == 1 && cr.n > kFp4Gather) {
+          to = p.cta_partials + ((size_t)(cr.first + g0) * 4 + 2 + (g0 == 0)) * part_floats;
         }
-        const int h = hp / head_tiles, ht = hp - h * head_tiles;
-        if (head >= G - ht * 8 * NT) continue;
         auto part = [&](int i) {
           return i == odd ? odd_part : reinterpret_cast<const float*>(base + i * step);
         };
-        float mi = -INFINITY, li = 0.f;
-        if (lane < n) {
-          const float* src = part(lane) + rows * D + head;
-          mi = src[0];
-          li = src[rows];
-        }
-        const float top = group_max<1>(mi);
-        const float w = mi == top ? 1.f : fast_exp2(mi - top);
-        float sum = lane < n ? li * w : 0.f, acc[kVec];
+        for (; unit < cr.heads * kSplit; unit += W) {
+          const int head = unit / kSplit;
+          const int col = unit * 32 * kVec + lane * kVec;
+          float mi = -INFINITY, li = 0.f;
+          if (lane < n) {
+            const float* src = part(lane) + rows * D + head;
+            mi = src[0];
+            li = src[rows];
+          }
+          const float top = warp_max_redux(mi);
+          const float w = mi == top ? 1.f : fast_exp2(mi - top);
+          float sum = lane < n ? li * w : 0.f, acc[kVec];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          for (int o = 1; o < kFp4Gather; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          sum = __shfl_sync(0xffffffffu, sum, 0);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-#pragma unroll 2
-        for (int i = 0; i < n; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);
-          const float* src = part(i) + col;
+          for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float* src = part(i) + col;
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(src + e);
+              acc[e] = fmaf(v.x, wi, acc[e]);
+              acc[e + 1] = fmaf(v.y, wi, acc[e + 1]);
+            }
+          }
+          const float inv = to ? 1.f : __fdividef(p.value_scale, sum);
+          T* dst = static_cast<T*>(p.out) + ((size_t)cr.s * p.num_heads + cr.head0) * D + col;
 #pragma unroll
           for (int e = 0; e < kVec; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(src + e);
-            acc[e] = fmaf(v.x, wi, acc[e]);
-            acc[e + 1] = fmaf(v.y, wi, acc[e + 1]);
+            const float2 v = make_float2(acc[e] * inv, acc[e + 1] * inv);
+            if (to) *reinterpret_cast<float2*>(to + col + e) = v;
+            else if constexpr (kF32) *reinterpret_cast<float2*>(dst + e) = v;
+            else *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(v.x, v.y);
           }
-        }
-        const float inv = to ? 1.f : p.value_scale / sum;
-        T* dst = static_cast<T*>(p.out) + ((size_t)s * p.num_heads + h * G + ht * 8 * NT) * D + col;
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 v = make_float2(acc[e] * inv, acc[e + 1] * inv);
-          if (to) *reinterpret_cast<float2*>(to + col + e) = v;
-          else if constexpr (kF32) *reinterpret_cast<float2*>(dst + e) = v;
-          else *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(v.x, v.y);
-        }
-        if (to && col == head * D) {  // the head's first lane
-          to[rows * D + head] = top;
-          to[rows * D + rows + head] = sum;
+          if (to && col == head * D) {  // the head's first lane
+            to[rows * D + head] = top;
+            to[rows * D + rows + head] = sum;
+          }
         }
       }
     }

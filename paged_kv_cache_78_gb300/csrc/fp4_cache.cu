@@ -1,9 +1,14 @@
 // Quantising write into the 4-bit pool, and reading tokens back, for sm_103a.
 //
-// Both move a group of 16 elements per thread: 32 bytes (bf16) or 64 bytes
-// (fp32) on one side, eight bytes of codes and one scale byte on the other.
-// Consecutive threads take a token's groups, then its heads, so the wide side
-// is read or written in whole lines.
+// Both move a group of 16 elements of a token's key and the same of its value
+// per thread: 32 bytes (bf16) or 64 bytes (fp32) each on one side, eight bytes of
+// codes and one scale byte on the other, and are bound by memory; a thread takes
+// key and value so that addresses are worked out once for both (one of them per
+// thread spent 62% of the issue slots, most of it on addresses).  A CTA takes
+// eight consecutive tokens and some of their heads, lanes a group's tokens, then
+// the next group.  Tokens that follow one another usually lie in one tile, so
+// that a warp's codes and scales are whole sectors of 32 bytes, and the wide
+// side is anyway.
 #include "pa_fp4.cuh"
 #include "pa_launch.h"
 
@@ -11,144 +16,187 @@ namespace pa {
 
 namespace {
 
-// The thread's group: token t, keys or values, head h, group j.
-struct Fp4Unit {
-  int64_t t;
-  int kv, h, j;
-};
+constexpr int kFp4Threads = 256;
 
-__device__ __forceinline__ Fp4Unit fp4_unit(int64_t i, int groups, int num_kv_heads) {
-  const int row_units = num_kv_heads * groups;
-  Fp4Unit u;
-  u.t = i / (2 * row_units);
-  int r = (int)(i - u.t * 2 * row_units);
-  u.kv = r >= row_units;
-  r -= u.kv ? row_units : 0;
-  u.h = r / groups;
-  u.j = r - u.h * groups;
-  return u;
-}
-
-// Where the group's codes and scale lie in its tile.
+// The thread's token, head and group; false where there is none.
 template <int D>
-__device__ __forceinline__ void fp4_places(const Fp4Unit& u, int row, int* codes, int* scale) {
-  constexpr int kGroups = D / kFp4Group;
-  *codes = u.kv ? fp4_value_codes(D) + u.j * 64 + row * 8 : row * (D / 2) + u.j * 8;
-  *scale = u.kv ? fp4_value_scales(D) + u.j * 8 + row : fp4_key_scales(D) + row * kGroups + u.j;
+__device__ __forceinline__ bool fp4_unit(int num_tokens, int num_kv_heads, int* t, int* h, int* j) {
+  constexpr int kUnits = kFp4Tile * D / kFp4Group;  // of one head of eight tokens
+  constexpr int kHeads = kFp4Threads / kUnits;
+  const unsigned chunks = ((unsigned)num_kv_heads + kHeads - 1) / kHeads;
+  const unsigned block = blockIdx.x / chunks;
+  const int i = threadIdx.x % kUnits;
+  *h = (int)(blockIdx.x - block * chunks) * kHeads + (int)threadIdx.x / kUnits;
+  *t = (int)block * kFp4Tile + i % kFp4Tile;
+  *j = i / kFp4Tile;
+  return *h < num_kv_heads && *t < num_tokens;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* src, float* x) {
-  constexpr int kPer = ElemTraits<T>::kPerChunk;
+// Where group j of a tile's row has its codes and its scale.
+template <int D>
+__device__ __forceinline__ void fp4_places(int row, int j, int kv, int* codes, int* scale) {
+  *codes = kv ? fp4_value_codes(D) + j * 64 + row * 8 : row * (D / 2) + j * 8;
+  *scale = kv ? fp4_value_scales(D) + j * 8 + row : fp4_key_scales(D) + row * (D / kFp4Group) + j;
+}
+
+// The group's largest magnitude; a NaN if there is one, and the largest number
+// for an infinity.
+__device__ __forceinline__ float largest(const uint4* w, const __nv_bfloat16*) {
+  __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-  for (int c = 0; c < 16 / kPer; ++c) ElemTraits<T>::unpack(ldg_nc_v4(src + c * kPer), x + c * kPer);
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    fp4_write_kernel(Fp4Pool pool, const T* __restrict__ key, const T* __restrict__ value,
-                     int64_t key_stride, int64_t value_stride,
-                     const int64_t* __restrict__ slot_mapping, int64_t num_tokens, float key_scale,
-                     float value_scale, unsigned int* err) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  constexpr int kGroups = D / kFp4Group;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= num_tokens * 2 * pool.num_kv_heads * kGroups) return;
-  const Fp4Unit u = fp4_unit(i, kGroups, pool.num_kv_heads);
-  const int64_t slot = __ldg(slot_mapping + u.t);
-  if (slot < 0) return;
-  if (slot >= pool.num_slots) {
-    if (u.kv == 0 && u.h == 0 && u.j == 0) record_error(err, PA_DEVERR_SLOT);
-    return;
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[e])));
   }
-  const T* src = (u.kv ? value + u.t * value_stride : key + u.t * key_stride) + u.h * D + u.j * 16;
-  float x[16];
-  load16(src, x);
-  const float tensor_scale = u.kv ? value_scale : key_scale;
-  // The largest magnitude by its bits, which order NaNs above everything.
-  uint32_t top = 0;
+  const float x = __bfloat162float(__hmax_nan(top.x, top.y));
+  return x == INFINITY ? 3.0e38f : x;
+}
+__device__ __forceinline__ float largest(const uint4* w, const float*) {
+  uint32_t top = 0;  // bits order NaNs above everything
 #pragma unroll
-  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-  const float inv_tensor = __frcp_rn(tensor_scale);
-  const uint32_t code = fp4_scale_code(__uint_as_float(top) * inv_tensor);
+  for (int c = 0; c < 4; ++c)
+    top = max(max(top, max(w[c].x & 0x7fffffffu, w[c].y & 0x7fffffffu)),
+              max(w[c].z & 0x7fffffffu, w[c].w & 0x7fffffffu));
+  return top == 0x7f800000u ? 3.0e38f : __uint_as_float(top);
+}
+
+// A group to its codes; returns the scale's code.
+template <typename T>
+__device__ __forceinline__ uint32_t quantise16(const uint4* w, float tensor_scale, uint2* codes) {
+  constexpr int kPer = ElemTraits<T>::kPerChunk;
+  float x[16], q[16];
+#pragma unroll
+  for (int c = 0; c < 16 / kPer; ++c) ElemTraits<T>::unpack(w[c], x + c * kPer);
+  const float inv_tensor = fast_rcp(tensor_scale);  // exact: a power of two
+  const uint32_t code = fp4_scale_code(largest(w, static_cast<const T*>(nullptr)) * inv_tensor);
   const float s = e4m3_to_float(code);
-  const float r = s > 0.f ? __frcp_rn(s) * inv_tensor : 0.f;
-  float q[16];
+  const float r = s > 0.f ? fast_rcp(s) * inv_tensor : 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     if constexpr (sizeof(T) == 2) q[e] = fp4_quotient_bf16(x[e], r);
     else q[e] = fp4_quotient_f32(x[e], s * tensor_scale, r);
   }
-  int at_codes, at_scale;
-  fp4_places<D>(u, (int)(slot & 7), &at_codes, &at_scale);
-  uint8_t* tile = pool.cache +
-                  fp4_tile_offset(slot, u.h, pool.num_kv_heads, pool.log2_block_size, D);
-  *reinterpret_cast<uint2*>(tile + at_codes) = make_uint2(e2m1_pack8(q), e2m1_pack8(q + 8));
-  tile[at_scale] = (uint8_t)code;
+  *codes = make_uint2(e2m1_pack8(q), e2m1_pack8(q + 8));
+  return code;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    fp4_gather_kernel(Fp4Pool pool, T* __restrict__ key, T* __restrict__ value,
-                      const int64_t* __restrict__ slot_mapping, int64_t num_tokens,
-                      float key_scale, float value_scale, unsigned int* err) {
+__global__ void __launch_bounds__(kFp4Threads)
+    fp4_write_kernel(Fp4Pool pool, const T* __restrict__ key, const T* __restrict__ value,
+                     int64_t key_stride, int64_t value_stride,
+                     const int64_t* __restrict__ slot_mapping, int num_tokens, float key_scale,
+                     float value_scale, unsigned int* err) {
+  constexpr int kChunks = sizeof(T);  // 16-byte loads of a group
+  int t, h, j;
+  const bool live = fp4_unit<D>(num_tokens, pool.num_kv_heads, &t, &h, &j);
   grid_dependents_launch();
   grid_dependency_wait();
-  constexpr int kGroups = D / kFp4Group;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= num_tokens * 2 * pool.num_kv_heads * kGroups) return;
-  const Fp4Unit u = fp4_unit(i, kGroups, pool.num_kv_heads);
-  const int64_t slot = __ldg(slot_mapping + u.t);
+  if (!live) return;
+  const int64_t slot = __ldg(slot_mapping + t);
+  // The rows are read whatever the slot says: the loads need not wait for it.
+  uint4 w[2][kChunks];
+  const T* src[2] = {key + t * key_stride + h * D + j * 16,
+                     value + t * value_stride + h * D + j * 16};
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      w[kv][c] = ldg_nc_v4(reinterpret_cast<const uint4*>(src[kv]) + c);
   if (slot < 0) return;
   if (slot >= pool.num_slots) {
-    if (u.kv == 0 && u.h == 0 && u.j == 0) record_error(err, PA_DEVERR_SLOT);
+    if (h == 0 && j == 0) record_error(err, PA_DEVERR_SLOT);
     return;
   }
-  int at_codes, at_scale;
-  fp4_places<D>(u, (int)(slot & 7), &at_codes, &at_scale);
-  const uint8_t* tile = pool.cache +
-                        fp4_tile_offset(slot, u.h, pool.num_kv_heads, pool.log2_block_size, D);
-  const uint2 w = *reinterpret_cast<const uint2*>(tile + at_codes);
-  const float s = e4m3_to_float(tile[at_scale]) * (u.kv ? value_scale : key_scale);
-  uint32_t h[8];
-  e2m1x8_to_half2(w.x, h);
-  e2m1x8_to_half2(w.y, h + 4);
-  float x[16];
+  uint8_t* tile =
+      pool.cache + fp4_tile_offset(slot, h, pool.num_kv_heads, pool.log2_block_size, D);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[2 * e] = half_lo(h[e]) * s;
-    x[2 * e + 1] = half_hi(h[e]) * s;
-  }
-  T* dst = (u.kv ? value : key) + (u.t * pool.num_kv_heads + u.h) * D + u.j * 16;
-  uint4* d4 = reinterpret_cast<uint4*>(dst);
-  if constexpr (sizeof(T) == 2) {
-    // Six significant bits: exact in bf16.
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      stg_v4(d4 + c, make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]),
-                                pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
-                                pack_bf16x2(x[8 * c + 4], x[8 * c + 5]),
-                                pack_bf16x2(x[8 * c + 6], x[8 * c + 7])));
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      stg_v4(d4 + c, make_uint4(__float_as_uint(x[4 * c]), __float_as_uint(x[4 * c + 1]),
-                                __float_as_uint(x[4 * c + 2]), __float_as_uint(x[4 * c + 3])));
+  for (int kv = 0; kv < 2; ++kv) {
+    uint2 codes;
+    const uint32_t scale = quantise16<T>(w[kv], kv ? value_scale : key_scale, &codes);
+    int at_codes, at_scale;
+    fp4_places<D>((int)(slot & 7), j, kv, &at_codes, &at_scale);
+    *reinterpret_cast<uint2*>(tile + at_codes) = codes;
+    tile[at_scale] = (uint8_t)scale;
   }
 }
 
-constexpr int kFp4Threads = 256;
+// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    stg_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+    stg_v4(static_cast<uint8_t*>(p) + 16, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
 
-unsigned fp4_grid(const Fp4Pool& pool, int64_t num_tokens) {
-  const int64_t units = num_tokens * 2 * pool.num_kv_heads * (pool.head_size / kFp4Group);
-  return (unsigned)((units + kFp4Threads - 1) / kFp4Threads);
+template <typename T, int D>
+__global__ void __launch_bounds__(kFp4Threads)
+    fp4_gather_kernel(Fp4Pool pool, T* __restrict__ key, T* __restrict__ value,
+                      const int64_t* __restrict__ slot_mapping, int num_tokens, float key_scale,
+                      float value_scale, bool wide, unsigned int* err) {
+  int t, h, j;
+  const bool live = fp4_unit<D>(num_tokens, pool.num_kv_heads, &t, &h, &j);
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (!live) return;
+  const int64_t slot = __ldg(slot_mapping + t);
+  if (slot < 0) return;
+  if (slot >= pool.num_slots) {
+    if (h == 0 && j == 0) record_error(err, PA_DEVERR_SLOT);
+    return;
+  }
+  const uint8_t* tile =
+      pool.cache + fp4_tile_offset(slot, h, pool.num_kv_heads, pool.log2_block_size, D);
+  uint2 codes[2];
+  uint32_t scales[2];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    int at_codes, at_scale;
+    fp4_places<D>((int)(slot & 7), j, kv, &at_codes, &at_scale);
+    codes[kv] = *reinterpret_cast<const uint2*>(tile + at_codes);
+    scales[kv] = tile[at_scale];
+  }
+  const int64_t to = ((int64_t)t * pool.num_kv_heads + h) * D + j * 16;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const float s = e4m3_to_float(scales[kv]) * (kv ? value_scale : key_scale);
+    uint32_t c[8];
+    e2m1x8_to_half2(codes[kv].x, c);
+    e2m1x8_to_half2(codes[kv].y, c + 4);
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[2 * e] = half_lo(c[e]) * s;
+      x[2 * e + 1] = half_hi(c[e]) * s;
+    }
+    T* dst = (kv ? value : key) + to;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[8];  // six significant bits: exact in bf16
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+      store32(dst, w, wide);
+    } else {
+      store32(dst, reinterpret_cast<const uint32_t*>(x), wide);
+      store32(dst + 8, reinterpret_cast<const uint32_t*>(x) + 8, wide);
+    }
+  }
+}
+
+unsigned fp4_grid(const Fp4Pool& pool, int num_tokens) {
+  const int heads = kFp4Threads / (kFp4Tile * pool.head_size / kFp4Group);
+  const unsigned chunks = ((unsigned)pool.num_kv_heads + heads - 1) / heads;
+  return (unsigned)((num_tokens + kFp4Tile - 1) / kFp4Tile) * chunks;
 }
 
 template <typename T, int D>
 cudaError_t launch_write(const Fp4Pool& pool, const void* key, const void* value,
                          int64_t key_stride, int64_t value_stride, const int64_t* slot_mapping,
-                         int64_t num_tokens, float key_scale, float value_scale,
+                         int num_tokens, float key_scale, float value_scale,
                          unsigned int* err, cudaStream_t stream) {
   void* args[] = {const_cast<Fp4Pool*>(&pool), &key, &value, &key_stride, &value_stride,
                   &slot_mapping, &num_tokens, &key_scale, &value_scale, &err};
@@ -158,10 +206,11 @@ cudaError_t launch_write(const Fp4Pool& pool, const void* key, const void* value
 
 template <typename T, int D>
 cudaError_t launch_gather(const Fp4Pool& pool, void* key, void* value,
-                          const int64_t* slot_mapping, int64_t num_tokens, float key_scale,
+                          const int64_t* slot_mapping, int num_tokens, float key_scale,
                           float value_scale, unsigned int* err, cudaStream_t stream) {
+  bool wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31) == 0;
   void* args[] = {const_cast<Fp4Pool*>(&pool), &key, &value, &slot_mapping, &num_tokens,
-                  &key_scale, &value_scale, &err};
+                  &key_scale, &value_scale, &wide, &err};
   return launch_overlapped((const void*)fp4_gather_kernel<T, D>, dim3(fp4_grid(pool, num_tokens)),
                            dim3(kFp4Threads), 0, stream, args);
 }
@@ -170,7 +219,7 @@ cudaError_t launch_gather(const Fp4Pool& pool, void* key, void* value,
 
 cudaError_t launch_fp4_write(const Fp4Pool& pool, const void* key, const void* value, int dtype,
                              int64_t key_stride, int64_t value_stride,
-                             const int64_t* slot_mapping, int64_t num_tokens, float key_scale,
+                             const int64_t* slot_mapping, int num_tokens, float key_scale,
                              float value_scale, unsigned int* err, cudaStream_t stream) {
   auto run = [&](auto* launch) {
     return launch(pool, key, value, key_stride, value_stride, slot_mapping, num_tokens, key_scale,
@@ -185,7 +234,7 @@ cudaError_t launch_fp4_write(const Fp4Pool& pool, const void* key, const void* v
 }
 
 cudaError_t launch_fp4_gather(const Fp4Pool& pool, void* key, void* value, int dtype,
-                              const int64_t* slot_mapping, int64_t num_tokens, float key_scale,
+                              const int64_t* slot_mapping, int num_tokens, float key_scale,
                               float value_scale, unsigned int* err, cudaStream_t stream) {
   auto run = [&](auto* launch) {
     return launch(pool, key, value, slot_mapping, num_tokens, key_scale, value_scale, err, stream);

@@ -69,14 +69,24 @@ __device__ __forceinline__ float half_hi(uint32_t h) {
 
 // ---- numbers to codes ---------------------------------------------------------
 
-// e4m3 of max / 6 (nearest, ties to even, at most 448; NaN stays NaN).  The
-// division is rounded to fp32 first, which never moves the quotient onto or
-// past a border of e4m3: a border times six has at most seven significant
-// bits, so a max other than that is off by one of its own last places, more
-// than the division's rounding.
+// 1 / x, off by at most one last place; exact for powers of two.
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// e4m3 of max / 6 for a finite max or NaN (nearest, ties to even, at most 448;
+// NaN stays NaN).  The quotient is first rounded to fp32 (by one step of
+// Newton's iteration on the rounded product, which is enough for a correctly
+// rounded 1 / 6), which never moves it onto or past a border of e4m3: a border
+// times six has at most seven significant bits, so a max other than that is
+// off by one of its own last places, more than the rounding.
 __device__ __forceinline__ uint32_t fp4_scale_code(float max_abs) {
+  constexpr float kSixth = 1.f / 6.f;
+  const float p = max_abs * kSixth;
+  const float q = fmaf(fmaf(-6.f, p, max_abs), kSixth, p);
   uint32_t r;
-  const float q = __fdiv_rn(max_abs, 6.f);
   asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n\tcvt.u32.u16 %0, c;\n\t}"
       : "=r"(r)
       : "f"(q), "f"(0.f));
@@ -102,13 +112,13 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float* q) {
   return w;
 }
 
-// x / s for the conversion to e2m1, s an e4m3 number, r = 1 / s rounded.  The
+// x / s for the conversion to e2m1, s an e4m3 number, r = 1 / s within 2^-22.  The
 // borders of e2m1 are 0.25 .. 5; a quotient has to reach the conversion on its
 // own side of each, or exactly on it.
 //
 // bf16 x: x and border * s are multiples of a common last place of eight
 // significant bits, so a quotient that is not a border is 2^-8 (relative)
-// away from it.  x * r is off by 2^-23; added to 1.5 * 2^12 it rounds to a
+// away from it.  x * r is off by 2^-22; added to 1.5 * 2^12 it rounds to a
 // multiple of 2^-11, which puts a border's own quotient on the border (they
 // are multiples) and moves no other onto or past one (0.25 * 2^-8 > 2^-12).
 // A NaN or infinite sum is as good: the group's scale decides, or 6 does.

@@ -106,10 +106,10 @@ struct Fp4Pool {
 };
 cudaError_t launch_fp4_write(const Fp4Pool& pool, const void* key, const void* value, int dtype,
                              int64_t key_stride, int64_t value_stride,
-                             const int64_t* slot_mapping, int64_t num_tokens, float key_scale,
+                             const int64_t* slot_mapping, int num_tokens, float key_scale,
                              float value_scale, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_fp4_gather(const Fp4Pool& pool, void* key, void* value, int dtype,
-                              const int64_t* slot_mapping, int64_t num_tokens, float key_scale,
+                              const int64_t* slot_mapping, int num_tokens, float key_scale,
                               float value_scale, unsigned int* err, cudaStream_t stream);
 
 // Decode attention over a 4-bit cache.
