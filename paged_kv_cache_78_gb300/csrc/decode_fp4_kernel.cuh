@@ -37,7 +37,8 @@ namespace pa {
 constexpr float kFp4Lift = 7.f;   // weights are 2^(S - m + 7): fp16 keeps small ones
 constexpr float kFp4Slack = 8.f;  // scores may pass the running maximum by this before it moves
 constexpr int kFp4RingBytes = 216 * 1024;
-constexpr int kFp4MaxWork = 1 << 27;  // stages of a launch
+constexpr int kFp4MaxWork = 1 << 27;  // units of a launch
+constexpr int kFp4PairCost = 1;       // see Fp4Place
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -98,23 +99,27 @@ __device__ __forceinline__ float group_max(float v) {  // over lanes that differ
   return v;
 }
 
-// A warp's place in the work: stage k of the n stages of pair (s, hp).
+// The work in units: every pair is kFp4PairCost units (its queries, its end),
+// then one per stage.  A stage belongs to the warp whose part its unit is in.
+// A warp's place: stage k, at unit `at`, of the n stages of pair (s, hp).
 struct Fp4Place {
   int s, hp, k, n, len;
+  int at;
 };
 
 // A piece: consecutive stages of one pair in a warp's part.
 struct Fp4Piece {
-  int s, hp;     // the pair
+  int s, hp;       // the pair
   int k0, stages;  // its first stage, and how many
-  int n, len;    // stages and tokens of the sequence
+  int n, len;      // stages and tokens of the sequence
+  int at;          // the unit of its first stage
 };
 constexpr int kFp4Pieces = 8;  // ring of pieces, at least the stages in flight + 2
 
 // The parts of one pair in a CTA: warps `first` .. w, w the last of them,
 // whose run it is.  A part that reaches its warp's end lies in the warp's ring,
-// one that ends before it in global memory.  `at` is the pair's first stage, in
-// all work, and n its stages; s < 0: no run.
+// one that ends before it in global memory.  `at` is the unit of the pair's
+// first stage, and n its stages; s < 0: no run.
 struct Fp4Run {
   int s, head0, heads;  // the pair's sequence and query heads
   int first, at, n;
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     *heads = min(8 * NT, G - ht * 8 * NT);
     return h * G + ht * 8 * NT;
   };
-  // Stages before each thread's sequences, and all of them; the warps' sums.
+  // Units before each thread's sequences; the warps' sums.
   int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
   int* pre = warp_sums + W;
   Fp4Run* runs = reinterpret_cast<Fp4Run*>(smem + C::kRuns);   // [warp][ended before, at its end]
@@ -195,15 +200,15 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   grid_dependency_wait();
   grid_dependents_launch();
 
-  // ---- the work: stages of every sequence, scanned ----
+  // ---- the work: units of every sequence, scanned ----
   auto stages_of = [&](int s, int* len_out) -> int {
     const int len = p.seq_lens[s];
     *len_out = len;
     if (len <= 0) return 0;
     if (((len - 1) >> l2bs) >= p.max_blocks_per_seq) return 0;
-    return (len - 1) / kFp4Stage + 1;
+    return (int)((unsigned)(len - 1) / kFp4Stage) + 1;
   };
-  // Sums stop at 2^27 stages (600 GB of reads at 128 elements): lengths that
+  // Sums stop at 2^27 units (600 GB of reads at 128 elements): lengths that
   // nobody meant, an error.
   const int chunk = (p.num_seqs + C::kThreads - 1) / C::kThreads;
   int total;
@@ -213,7 +218,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       int len;
       const int n = stages_of(s, &len);
       if (n == 0 && len > 0 && blockIdx.x == 0) record_error(p.err, PA_DEVERR_SEQ_LEN);
-      mine = (int)min((long long)mine + (long long)n * per_seq, (long long)kFp4MaxWork);
+      if (n > 0)
+        mine = (int)min(mine + (long long)(n + kFp4PairCost) * per_seq, (long long)kFp4MaxWork);
     }
     int sum = mine;
 #pragma unroll
@@ -232,32 +238,35 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     total = all >= (unsigned)kFp4MaxWork ? 0 : (int)all;
     __syncthreads();
   }
-  // Stages of a CTA: an equal share, at least one per two warps (fewer parts
-  // to merge where there is little work).
+  // Units of a CTA: an equal share, at least one per two warps (fewer parts to
+  // merge where there is little work).
   const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, W / 2);
   const int cta0 = (int)min((long long)share * blockIdx.x, (long long)total);
   const int cta1 = min(cta0 + share, total);
 
-  // The place of a stage.  All lanes look: the last thread whose sequences
-  // begin at or before it, then the sequence.
-  auto locate = [&](int at) -> Fp4Place {
+  // The first stage whose unit is `unit` or a later one of the same pair.  All
+  // lanes look: the last thread whose sequences begin at or before the unit, then
+  // the sequence.
+  auto locate = [&](int unit) -> Fp4Place {
     constexpr int kSpan = C::kThreads / 32;
-    const int seg = __popc(__ballot_sync(0xffffffffu, pre[lane * kSpan] <= at)) - 1;
+    const int seg = __popc(__ballot_sync(0xffffffffu, pre[lane * kSpan] <= unit)) - 1;
     const int own = lane < kSpan ? pre[seg * kSpan + lane] : 0x7fffffff;
-    const int off = __popc(__ballot_sync(0xffffffffu, own <= at)) - 1;
+    const int off = __popc(__ballot_sync(0xffffffffu, own <= unit)) - 1;
     int acc = __shfl_sync(0xffffffffu, own, off);
     Fp4Place pl;
     pl.s = (seg * kSpan + off) * chunk;
     while (true) {
       pl.n = stages_of(pl.s, &pl.len);
-      const int next = acc + pl.n * per_seq;
-      if (next > at) break;
+      const int next = pl.n > 0 ? acc + (pl.n + kFp4PairCost) * per_seq : acc;
+      if (next > unit) break;
       acc = next;
       ++pl.s;
     }
-    const int rem = at - acc;
-    pl.hp = rem / pl.n;
-    pl.k = rem - pl.hp * pl.n;
+    const int size = pl.n + kFp4PairCost;
+    pl.hp = (unit - acc) / size;
+    const int at = acc + pl.hp * size + kFp4PairCost;
+    pl.k = max(unit - at, 0);
+    pl.at = at + pl.k;
     return pl;
   };
 
@@ -265,31 +274,33 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   const int share_w = (share + W - 1) / W;
   const int my0 = cta0 + share_w * warp;
   const int my1 = min(my0 + share_w, cta1);
+  // The pair of the CTA's last unit ends after the CTA: other CTAs have parts of
+  // it, if this one has.  A pair that also began before counts as begun before.
   if (warp == W - 1 && cta0 < cta1) {
     const Fp4Place pl = locate(cta1 - 1);
-    const int at = cta1 - 1 - pl.k;
-    // Ends after this CTA; a pair that also began before counts as begun before.
-    if (lane == 0 && pl.k + 1 < pl.n && at >= cta0) {
+    const int at = pl.at - pl.k;
+    if (lane == 0 && at >= cta0 && at < cta1 && at + pl.n > cta1) {
       int heads;
       const int head0 = heads_of(pl.hp, &heads), b = (int)blockIdx.x;
       cross[1] = Fp4Cross{pl.s, head0, heads, b, (at + pl.n - 1) / share - b + 1};
     }
   }
-  if (my0 < my1) {
-    const int count = my1 - my0;
-    const int per_block = l2bs >= 5 ? kFp4Stage / kFp4Tile : 1 << (l2bs - 3);  // tiles of a copy
+  Fp4Place pp = {};  // the next stage to copy
+  if (my0 < my1) pp = locate(my0);
+  if (my0 < my1 && pp.at < my1) {
+    const int per_block = min(kFp4Stage / kFp4Tile, 1 << (l2bs - 3));  // tiles of a copy
     const uint32_t lane_dst = (uint32_t)(lane * per_block) * C::kTileBytes;
     const uint32_t block_bytes = ((uint32_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
 
     // ---- producer: the next stage to copy, its table entry already fetched ----
-    Fp4Place pp = locate(my0);
     if (warp == 0 && lane == 0 && pp.k > 0) {
       int heads;
       const int head0 = heads_of(pp.hp, &heads);
-      const int at = my0 - pp.k, c0 = at / share;
+      const int at = pp.at - pp.k, c0 = at / share;
       cross[0] = Fp4Cross{pp.s, head0, heads, c0, (at + pp.n - 1) / share - c0 + 1};
     }
-    int entered = 0, fetched = 0, issued = 0;
+    int entered = 0, issued = 0;
+    bool more = true;                // there is a stage after the ones fetched
     const int32_t* table = nullptr;  // the sequence's row, from this lane's block
     const uint8_t* head_base = nullptr;
     auto enter = [&]() {  // a piece begins
@@ -298,33 +309,39 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       head_base = p.cache + ((size_t)h << (l2bs - 3)) * C::kTileBytes;
       if (lane == 0)
         pieces[entered % kFp4Pieces] =
-            Fp4Piece{pp.s, pp.hp, pp.k, min(pp.n - pp.k, count - fetched), pp.n, pp.len};
+            Fp4Piece{pp.s, pp.hp, pp.k, min(pp.n - pp.k, my1 - pp.at), pp.n, pp.len, pp.at};
       ++entered;
     };
+    enter();
     struct Next {
       int id, tiles;
       const uint8_t* base;
     };
     auto fetch = [&]() -> Next {
-      if (fetched == 0) {
-        enter();
-      } else if (++pp.k == pp.n) {
-        pp.k = 0;
-        if (++pp.hp == per_seq) {
-          pp.hp = 0;
-          do {
-            ++pp.s;
-            pp.n = stages_of(pp.s, &pp.len);
-          } while (pp.n == 0);
-        }
-        enter();
-      }
-      ++fetched;
       const int tok0 = pp.k * kFp4Stage;
       Next nx;
-      nx.tiles = min(kFp4Stage / kFp4Tile, (pp.len - tok0 + kFp4Tile - 1) / kFp4Tile);
+      nx.tiles = min(kFp4Stage / kFp4Tile, (pp.len - tok0 + kFp4Tile - 1) >> 3);
       nx.base = head_base + ((tok0 & ((1 << l2bs) - 1)) >> 3) * C::kTileBytes;
       nx.id = lane * per_block < nx.tiles ? __ldg(table + (tok0 >> l2bs)) : 0;
+      // On to the next stage, if it is this warp's.
+      ++pp.at;
+      if (++pp.k == pp.n) {
+        pp.at += kFp4PairCost;
+        pp.k = 0;
+        more = pp.at < my1;
+        if (more) {
+          if (++pp.hp == per_seq) {
+            pp.hp = 0;
+            do {
+              ++pp.s;
+              pp.n = stages_of(pp.s, &pp.len);
+            } while (pp.n == 0);
+          }
+          enter();
+        }
+      } else {
+        more = pp.at < my1;
+      }
       return nx;
     };
     // One copy per block into slot `slot`.
@@ -356,16 +373,21 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     };
 
     Next next;
+    bool have = false;  // `next` waits for a slot
     {
       // Fill the ring, every table entry on its way before the first is needed.
       Next first[NS];
+      int n = 0;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (i < count) first[i] = fetch();
-      if (NS < count) next = fetch();
+        if (more) {
+          first[i] = fetch();
+          ++n;
+        }
+      if ((have = more)) next = fetch();
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (i < count) issue(first[i], i);
+        if (i < n) issue(first[i], i);
     }
 
     uint32_t q[kQParts][NT][kSteps][2];  // Q^T: head g of tile nt, this thread's elements
@@ -568,7 +590,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       }
     };
 
-    for (int done = 0, piece = 0; done < count && ok; ++piece) {
+    bool last = false;
+    for (int piece = 0; !last; ++piece) {
       __syncwarp();
       const Fp4Piece pc = pieces[piece % kFp4Pieces];
       int heads;
@@ -626,9 +649,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         const int tokens = pc.len - k * kFp4Stage;
         attend(stage, min(tokens, kFp4Stage));
         // The slot is free: the next stage.
-        if (issued < count) {
+        if (have) {
           issue(next, slot);
-          if (fetched < count) next = fetch();
+          if ((have = more)) next = fetch();
         }
         if (++slot == NS) {
           slot = 0;
@@ -636,7 +659,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         }
       }
       if (!ok) break;
-      done += pc.stages;
+      const bool ends = pc.k0 + pc.stages == pc.n;
+      last = pc.at + pc.stages + (ends ? kFp4PairCost : 0) >= my1;
 
       // ---- the piece is done ----
       // Sums over the tokens' lanes.
@@ -681,7 +705,6 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       } else {
         // A part: to the ring at the end of the warp's part (every copy has
         // landed and been read), to global memory before.
-        const bool last = done == count;
         float* dst = last ? reinterpret_cast<float*>(smem + warp * C::kWarpRing)
                           : p.warp_partials + ((size_t)blockIdx.x * W + warp) * part_floats;
         __syncwarp();
@@ -702,10 +725,10 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
             }
           }
         // The warp with the pair's last part in this CTA says where the parts are.
-        if (lane == 0 && (pc.k0 + pc.stages == pc.n || my0 + done == cta1)) {
-          const int at = my0 + done - pc.stages - pc.k0;
-          runs[2 * warp + last] =
-              Fp4Run{pc.s, head0, heads, at <= cta0 ? 0 : (at - cta0) / share_w, at, pc.n};
+        if (lane == 0 && (ends || pc.at + pc.stages == cta1)) {
+          const int at = pc.at - pc.k0;
+          runs[2 * warp + last] = Fp4Run{pc.s, head0, heads, at <= cta0 ? 0 : (at - cta0) / share_w,
+                                         at, pc.n};
         }
       }
     }
