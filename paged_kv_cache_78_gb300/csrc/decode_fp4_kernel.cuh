@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   // Units of a CTA: an equal share, at least one per two warps (fewer parts to
   // merge where there is little work).
   const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, W / 2);
-  const int cta0 = (int)min((long long)share * blockIdx.x, (long long)total);
-  const int cta1 = min(cta0 + share, total);
+  int cta0 = (int)min((long long)share * blockIdx.x, (long long)total);
+  int cta1 = min(cta0 + share, total);
 
   // The first stage whose unit is `unit` or a later one of the same pair.  All
   // lanes look: the last thread whose sequences begin at or before the unit, then
@@ -270,8 +270,22 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     return pl;
   };
 
+  // Where a CTA's share is at most four stages per warp, latency is what counts
+  // and a merge over CTAs (3 to 4 us) costs more than four stages more per warp:
+  // pairs of up to that many stages stay whole, with the CTA of their first unit.
+  if (share <= 4 * W) {
+    auto whole = [&](int unit) {
+      if (unit <= 0 || unit >= total) return unit;
+      const Fp4Place pl = locate(unit);
+      const int first = pl.at - pl.k - kFp4PairCost;  // the pair's first unit
+      return unit > first && pl.n <= 4 * W ? first + kFp4PairCost + pl.n : unit;
+    };
+    cta0 = whole(cta0);
+    cta1 = whole(cta1);
+  }
+
   bool ok = true;
-  const int share_w = (share + W - 1) / W;
+  const int share_w = (cta1 - cta0 + W - 1) / W;
   const int my0 = cta0 + share_w * warp;
   const int my1 = min(my0 + share_w, cta1);
   // The pair of the CTA's last unit ends after the CTA: other CTAs have parts of
