@@ -10,9 +10,9 @@ cudaError_t launch_decode_fp4_d256(const Fp4DecodeParams&, int dtype, int num_sm
 
 namespace {
 
-// Floats of one partial result, whatever the element type.
+// Floats of one partial result at most, whatever the element type.
 size_t partial_floats(int head_size, int group) {
-  return fp4_partial_floats(fp4_unit_rows(fp4_head_tiles(head_size, group), group), head_size);
+  return fp4_partial_floats(fp4_unit_rows(fp4_head_tiles(head_size, group), group), head_size, 2);
 }
 
 }  // namespace

@@ -8,10 +8,11 @@
 namespace pa {
 
 constexpr int kFp4Stage = 32;          // tokens that a warp takes at a time
-constexpr int kFp4HeaderBytes = 4096;  // three counters per CTA
 
 constexpr int kFp4Gather = 16;         // parts that are merged at once
 constexpr int kFp4MaxCtas = kFp4Gather * kFp4Gather;
+constexpr int kFp4Units = 32;          // units of a pair that are merged by themselves
+constexpr int kFp4HeaderBytes = kFp4MaxCtas * 3 * kFp4Units * 4;  // three counters per CTA and unit
 
 // Two tiles of eight query heads (columns of the matrix instructions) where
 // the registers hold them, one otherwise: groups past eight heads of 256
@@ -26,13 +27,18 @@ __host__ __device__ constexpr int fp4_warps(int head_size, int tiles, bool fp32)
   return head_size / 16 * tiles * (fp32 ? 8 : 6) <= 48 ? 16 : 8;
 }
 
-// Rows (query heads) of one unit of work, and the floats of its partial
-// result: weighted values, then the maxima, then the sums.
+// Rows (query heads) of a pair; the units of a head that are merged by
+// themselves; and the floats of a partial result: weighted values, then each
+// unit's maximum, then each unit's sum (units are handed on one by one, so each
+// has its own).
 __host__ __device__ constexpr int fp4_unit_rows(int tiles, int group) {
   return group < 8 * tiles ? group : 8 * tiles;
 }
-__host__ __device__ constexpr int fp4_partial_floats(int rows, int head_size) {
-  return (rows * (head_size + 2) + 3) / 4 * 4;
+__host__ __device__ constexpr int fp4_splits(int head_size, int rows, int warps) {
+  return head_size > 64 && 2 * rows <= warps ? 2 : 1;
+}
+__host__ __device__ constexpr int fp4_partial_floats(int rows, int head_size, int splits) {
+  return (rows * (head_size + 2 * splits) + 3) / 4 * 4;
 }
 
 struct Fp4DecodeParams {
@@ -42,7 +48,7 @@ struct Fp4DecodeParams {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   unsigned int* err;
-  unsigned int* counters;  // three per CTA, zero between calls
+  unsigned int* counters;  // [CTAs][3][kFp4Units], zero between calls
   float* warp_partials;    // [CTAs][warps][partial]
   float* cta_partials;     // [CTAs][4][partial]: of CTAs, then of groups of CTAs
   long long wait_limit;

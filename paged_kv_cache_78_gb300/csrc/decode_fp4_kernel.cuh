@@ -49,6 +49,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Wait for a phase of `bar`, at most `limit` cycles from the first look on; a
+// wait that runs out records PA_DEVERR_TIMEOUT and returns false.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* err,
+                                           long long limit) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (clock64() - t0 < limit)
+    if (mbar_try_wait(bar, parity)) return true;
+  record_error(err, PA_DEVERR_TIMEOUT);
+  return false;
+}
+
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(a));
@@ -70,10 +82,24 @@ __device__ __forceinline__ uint2 lds_u64(uint32_t a) {
   return v;
 }
 
+// N floats of shared memory or of what other CTAs wrote, never from the L1 cache.
+template <int N>
+__device__ __forceinline__ void ld_past_l1(const float* p, float* v) {
+  if constexpr (N == 2) {
+    asm volatile("ld.volatile.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.volatile.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                   : "l"(p + i)
+                   : "memory");
+  }
+}
+
 // c += a . b: a 16 x 16, b 16 x 8, fp16 with fp32 sums.
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
@@ -82,7 +108,25 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, const uint3
 // The 8 x 8 matrix of 16-bit elements that the warp holds, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// a times the low (kHigh: the high) half of s, which the multiplication takes
+// as an operand's half without an instruction of its own.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t half2_mul_by(uint32_t a, uint32_t s) {
+  uint32_t r;
+  if constexpr (kHigh)
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\t"
+        "mul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(s));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\t"
+        "mul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(s));
   return r;
 }
 
@@ -118,17 +162,11 @@ constexpr int kFp4Pieces = 8;  // ring of pieces, at least the stages in flight 
 
 // The parts of one pair in a CTA: warps `first` .. w, w the last of them,
 // whose run it is.  A part that reaches its warp's end lies in the warp's ring,
-// one that ends before it in global memory.  `at` is the unit of the pair's
-// first stage, and n its stages; s < 0: no run.
+// one that ends before it in global memory.  The pair has parts in `ctas` CTAs
+// from cta0 on; s < 0: no run.
 struct Fp4Run {
   int s, head0, heads;  // the pair's sequence and query heads
-  int first, at, n;
-};
-
-// A pair that other CTAs have parts of: the first of them, and how many.
-struct Fp4Cross {
-  int s, head0, heads;
-  int first, n;
+  int first, cta0, ctas;
 };
 
 template <typename T, int D, int NT>
@@ -145,12 +183,10 @@ struct Fp4Config {
   static constexpr int kPieces = kBars + 8 * kWarps * kStages;
   static constexpr int kPre = (kPieces + kWarps * kFp4Pieces * (int)sizeof(Fp4Piece) + 15) / 16 * 16;
   static constexpr int kRuns = (kPre + 4 * (kThreads + kWarps) + 15) / 16 * 16;
-  static constexpr int kCross = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
-  static constexpr int kGather = (kCross + 2 * (int)sizeof(Fp4Cross) + 8 + 15) / 16 * 16;
-  static constexpr int kSmem = kGather + 8;
+  static constexpr int kSmem = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
   static_assert(kStages >= 2 && kStages + 2 <= kFp4Pieces, "rings");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(fp4_partial_floats(8 * NT, D) * 4 <= kWarpRing, "a part fits its warp's ring");
+  static_assert(fp4_partial_floats(8 * NT, D, 2) * 4 <= kWarpRing, "a part fits its warp's ring");
 };
 
 template <typename T, int D, int NT>
@@ -170,7 +206,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   const int rows = fp4_unit_rows(NT, G);
   const int per_seq = p.num_kv_heads * head_tiles;  // pairs of a sequence
   const int l2bs = p.log2_block_size;
-  const int part_floats = fp4_partial_floats(rows, D);
+  // A merge's unit: a head, or half of one where there are two warps per head.
+  constexpr int kSplit = fp4_splits(D, 8 * NT, W);  // units of a head
+  constexpr int kVec = D / 32 / kSplit;             // columns of a lane
+  const int per_run = rows * kSplit;                // units of a pair
+  const int part_floats = fp4_partial_floats(rows, D, kSplit);
 
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * C::kWarpRing;
@@ -186,16 +226,10 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
   int* pre = warp_sums + W;
   Fp4Run* runs = reinterpret_cast<Fp4Run*>(smem + C::kRuns);   // [warp][ended before, at its end]
-  Fp4Cross* cross = reinterpret_cast<Fp4Cross*>(smem + C::kCross);  // begun before; ending after
-  volatile int* flag = reinterpret_cast<volatile int*>(cross + 2);
-  const uint32_t gather_bar = smem_u32(smem) + C::kGather;
-
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(bars + 8u * i, 1);
     runs[2 * warp].s = runs[2 * warp + 1].s = -1;
   }
-  if (tid < 2) cross[tid].s = -1;
-  if (tid == 0) mbar_init(gather_bar, 1);
   if (lane == 0) fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -288,17 +322,6 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   const int share_w = (cta1 - cta0 + W - 1) / W;
   const int my0 = cta0 + share_w * warp;
   const int my1 = min(my0 + share_w, cta1);
-  // The pair of the CTA's last unit ends after the CTA: other CTAs have parts of
-  // it, if this one has.  A pair that also began before counts as begun before.
-  if (warp == W - 1 && cta0 < cta1) {
-    const Fp4Place pl = locate(cta1 - 1);
-    const int at = pl.at - pl.k;
-    if (lane == 0 && at >= cta0 && at < cta1 && at + pl.n > cta1) {
-      int heads;
-      const int head0 = heads_of(pl.hp, &heads), b = (int)blockIdx.x;
-      cross[1] = Fp4Cross{pl.s, head0, heads, b, (at + pl.n - 1) / share - b + 1};
-    }
-  }
   Fp4Place pp = {};  // the next stage to copy
   if (my0 < my1) pp = locate(my0);
   if (my0 < my1 && pp.at < my1) {
@@ -307,12 +330,6 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     const uint32_t block_bytes = ((uint32_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
 
     // ---- producer: the next stage to copy, its table entry already fetched ----
-    if (warp == 0 && lane == 0 && pp.k > 0) {
-      int heads;
-      const int head0 = heads_of(pp.hp, &heads);
-      const int at = pp.at - pp.k, c0 = at / share;
-      cross[0] = Fp4Cross{pp.s, head0, heads, c0, (at + pp.n - 1) / share - c0 + 1};
-    }
     int entered = 0, issued = 0;
     bool more = true;                // there is a stage after the ones fetched
     const int32_t* table = nullptr;  // the sequence's row, from this lane's block
@@ -425,7 +442,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[u][nt][c] = 0.f;
         constexpr int kWords = D / 32;  // of a thread's quarter row
-        uint32_t kw[2][kWords], ks[2][D / 64];  // codes; scales of 16 elements as pairs
+        uint32_t kw[2][kWords], ks[2][(D + 127) / 128];  // codes; scales, two to a word
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t tile = stage + (2 * u + e) * C::kTileBytes;
@@ -436,7 +453,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
             kw[e][0] = v.x;
             kw[e][1] = v.y;
             const uint32_t two = e4m3x2_to_half2(lds_u8(sca));
-            ks[e][0] = __byte_perm(two, 0, 0x1010);
+            ks[e][0] = two;
           } else {
 #pragma unroll
             for (int c = 0; c < kWords / 4; ++c) {
@@ -446,8 +463,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
               kw[e][4 * c + 2] = v.z;
               kw[e][4 * c + 3] = v.w;
               const uint32_t two = e4m3x2_to_half2(lds_u16(sca + 2 * c));
-              ks[e][2 * c] = __byte_perm(two, 0, 0x1010);
-              ks[e][2 * c + 1] = __byte_perm(two, 0, 0x3232);
+              ks[e][c] = two;
             }
           }
         }
@@ -458,8 +474,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           e2m1x8_to_half2(kw[1][w], hi);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            lo[b] = half2_mul(lo[b], ks[0][w / 2]);
-            hi[b] = half2_mul(hi[b], ks[1][w / 2]);
+            // Words 0, 1 of four have the first scale of a pair.
+            lo[b] = w / 2 % 2 ? half2_mul_by<true>(lo[b], ks[0][w / 4])
+                              : half2_mul_by<false>(lo[b], ks[0][w / 4]);
+            hi[b] = w / 2 % 2 ? half2_mul_by<true>(hi[b], ks[1][w / 4])
+                              : half2_mul_by<false>(hi[b], ks[1][w / 4]);
           }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -656,15 +675,16 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       }
       fresh = true;
       for (int k = pc.k0; k < pc.k0 + pc.stages; ++k) {
-        const bool w = mbar_wait_bounded(bars + 8u * slot, parity, p.err, p.wait_limit);
-        ok = __all_sync(0xffffffffu, w);
-        if (!ok) break;
-        const uint32_t stage = ring + slot * C::kStageBytes;
-        const int tokens = pc.len - k * kFp4Stage;
-        attend(stage, min(tokens, kFp4Stage));
-        // The slot is free: the next stage.
+        if (ok) {
+          const bool w = wait_phase(bars + 8u * slot, parity, p.err, p.wait_limit);
+          ok = __all_sync(0xffffffffu, w);
+        }
+        if (ok) attend(ring + slot * C::kStageBytes, min(pc.len - k * kFp4Stage, kFp4Stage));
+        // The slot is free: the next stage.  After a wait that gave up nothing is
+        // copied or computed any more, but the parts are still handed on, so that
+        // the counters come out even.
         if (have) {
-          issue(next, slot);
+          if (ok) issue(next, slot);
           if ((have = more)) next = fetch();
         }
         if (++slot == NS) {
@@ -672,7 +692,6 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           parity ^= 1;
         }
       }
-      if (!ok) break;
       const bool ends = pc.k0 + pc.stages == pc.n;
       last = pc.at + pc.stages + (ends ? kFp4PairCost : 0) >= my1;
 
@@ -733,16 +752,20 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
             for (int j = 0; j < kSteps; j += 2)
               *reinterpret_cast<float4*>(od + 2 * j) =
                   make_float4(o[nt][j][c], o[nt][j][c + 2], o[nt][j + 1][c], o[nt][j + 1][c + 2]);
-            if (g == 0) {
-              dst[rows * D + head] = m[nt][c];
-              dst[rows * D + rows + head] = ls[nt][c];
-            }
+            if (g == 0)
+#pragma unroll
+              for (int sp = 0; sp < kSplit; ++sp) {
+                dst[rows * D + head * kSplit + sp] = m[nt][c];
+                dst[rows * D + per_run + head * kSplit + sp] = ls[nt][c];
+              }
           }
         // The warp with the pair's last part in this CTA says where the parts are.
         if (lane == 0 && (ends || pc.at + pc.stages == cta1)) {
-          const int at = pc.at - pc.k0;
+          const int at = pc.at - pc.k0;  // the pair's first stage
+          const bool here = at >= cta0 && at + pc.n <= cta1;
+          const int c0 = here ? (int)blockIdx.x : at / share;
           runs[2 * warp + last] = Fp4Run{pc.s, head0, heads, at <= cta0 ? 0 : (at - cta0) / share_w,
-                                         at, pc.n};
+                                         c0, here ? 1 : (at + pc.n - 1) / share - c0 + 1};
         }
       }
     }
@@ -763,162 +786,112 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     }
 
   // ---- merges ----
-  // First over the CTA's warps; then, for pairs that reach over the CTA's ends,
-  // over CTAs, each by the last to arrive, up to kFp4Gather parts at a time (one
-  // SM would take 8 us for a part of 8 heads of 256 elements from every SM): the
-  // groups of a pair's CTAs, then their results, copied into the rings' memory.
-  // A CTA has two counters for groups, of the pair that it begins and of the one
-  // that it continues, and one for the results of the pair that it begins.  One
-  // short body for all: code that runs once is paid by its length (unrolled over
-  // the 16 parts it took 2 us longer).
+  // A warp takes some columns of one head of a pair, first over the CTA's warps;
+  // then, for a pair with parts in other CTAs, the last warp to arrive with its
+  // columns merges those, up to kFp4Gather at a time (one SM would take 8 us for
+  // a part of 8 heads of 256 elements from every SM): the groups of the pair's
+  // CTAs, then their results.  Of a CTA's counters for each unit the first is
+  // for the group of the pair that it continues, the second for the first group
+  // of the pair that it begins, the third for the results of that pair's groups;
+  // its four slots hold its part of the pair that it continues, of the one that
+  // it begins, and the groups' results likewise.  One short loop for all levels:
+  // code that runs once is paid by its length (unrolled over 16 parts it took
+  // 2 us longer).
   if (cta0 >= cta1) return;  // the same for the whole CTA
-  constexpr int kVec = D == 256 ? 4 : 2;   // columns of a lane
-  constexpr int kSplit = D / (32 * kVec);  // units of a head
-  static_assert(W <= kFp4Gather, "a run's parts");
-  static_assert(kFp4Gather * fp4_partial_floats(8 * NT, D) * 4 <= C::kBars, "gathered parts");
-  const uint32_t part_bytes = 4u * part_floats;
-  uint32_t gathers = 0;
-  for (int phase = 0; phase < 3; ++phase) {
-    __syncthreads();
-    uint32_t live;
-    if (phase == 0) {
-      live = __ballot_sync(0xffffffffu, lane < 2 * W && runs[lane % (2 * W)].s >= 0);
-    } else {
-      if (tid < 2) {
-        const Fp4Cross cr = cross[tid];
-        bool go = cr.s >= 0 && (phase == 1 || (flag[tid] && cr.n > kFp4Gather));
-        if (go) {
-          const int group = ((int)blockIdx.x - cr.first) / kFp4Gather;
-          const int wait = phase == 2 ? (cr.n + kFp4Gather - 1) / kFp4Gather
-                                      : min(kFp4Gather, cr.n - group * kFp4Gather);
-          unsigned int* counter = p.counters + 3 * cr.first +
-                                  (phase == 2 ? 2 : 3 * group * kFp4Gather + (group == 0));
+  __syncthreads();
+  static_assert(W <= kFp4Gather && 8 * NT * kSplit <= kFp4Units, "merges");
+  uint32_t live = __ballot_sync(0xffffffffu, lane < 2 * W && runs[lane % (2 * W)].s >= 0);
+  for (int u0 = 0; live; live &= live - 1, u0 += per_run) {
+    // Unit u of all runs' is warp u mod W's.
+    int unit = (warp - u0) & (W - 1);
+    if (unit >= per_run) continue;
+    const int which = __ffs(live) - 1;
+    const Fp4Run run = runs[which];
+    for (; unit < run.heads * kSplit; unit += W) {
+      const int col = unit * 32 * kVec + lane * kVec;
+      // Parts i < n lie `step` bytes apart from `base` on, but for part `odd`.
+      const uint8_t* base = smem + run.first * C::kWarpRing;
+      uint32_t step = C::kWarpRing;
+      int n = (which >> 1) - run.first + 1;
+      int odd = (which & 1) ? -1 : n - 1;
+      const float* odd_part =
+          p.warp_partials + ((size_t)blockIdx.x * W + (which >> 1)) * part_floats;
+      for (int level = 0;; ++level) {
+        auto part = [&](int i) {
+          return i == odd ? odd_part : reinterpret_cast<const float*>(base + i * step);
+        };
+        float mi = -INFINITY, li = 0.f, acc[kVec];
+        if (lane < n) {
+          const volatile float* src = part(lane) + rows * D + unit;
+          mi = src[0];
+          li = src[per_run];
+        }
+        const float top = warp_max_redux(mi);
+        const float w = mi == top ? 1.f : fast_exp2(mi - top);
+        float sum = lane < n ? li * w : 0.f;
+#pragma unroll
+        for (int o = 1; o < kFp4Gather; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __shfl_sync(0xffffffffu, sum, 0);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          float v[kVec];
+          ld_past_l1<kVec>(part(i) + col, v);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(v[e], wi, acc[e]);
+        }
+        const int group = ((int)blockIdx.x - run.cta0) / kFp4Gather;
+        const int groups = (run.ctas + kFp4Gather - 1) / kFp4Gather;
+        if (level == (run.ctas == 1 ? 0 : groups == 1 ? 1 : 2)) {
+          const float inv = __fdividef(p.value_scale, sum);
+          T* dst = static_cast<T*>(p.out) + ((size_t)run.s * p.num_heads + run.head0) * D + col;
+#pragma unroll
+          for (int e = 0; e < kVec; e += 2) {
+            if constexpr (kF32)
+              *reinterpret_cast<float2*>(dst + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+            else
+              *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+          }
+          break;
+        }
+        // Hand the part on; whoever is last takes the next level.
+        const int at = level == 0 ? (int)blockIdx.x : run.cta0 + group * kFp4Gather;
+        float* to =
+            p.cta_partials + ((size_t)at * 4 + 2 * level + (at == run.cta0)) * part_floats;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2)
+          *reinterpret_cast<float2*>(to + col + e) = make_float2(acc[e], acc[e + 1]);
+        if (lane == 0) {
+          to[rows * D + unit] = top;
+          to[rows * D + per_run + unit] = sum;
+        }
+        __syncwarp();
+        const int first = level == 0 ? run.cta0 + group * kFp4Gather : run.cta0;
+        const int parts = level == 0 ? min(kFp4Gather, run.ctas - group * kFp4Gather) : groups;
+        int go = 0;
+        if (lane == 0) {
+          unsigned int* counter =
+              p.counters + (first * 3 + (level == 1 ? 2 : first == run.cta0)) * kFp4Units + unit;
           unsigned int before;
           asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
                        : "=r"(before)
                        : "l"(counter)
                        : "memory");
-          go = before == (unsigned)wait - 1;
+          go = before == (unsigned)parts - 1;
           if (go) *counter = 0u;
         }
-        flag[tid] = go;
-      }
-      __syncthreads();
-      live = (flag[0] ? 1u : 0u) | (flag[1] ? 2u : 0u);
-      if (live == 0) return;
-    }
-    // Phase 0: a warp takes units of all runs in turn; after that, one pair at
-    // a time.
-    const int passes = phase == 0 ? 1 : 2;
-    for (int pass = 0; pass < passes; ++pass) {
-      if (phase > 0 && !(live >> pass & 1)) continue;
-      Fp4Cross cr;
-      int n = 0, g0 = 0;
-      if (phase > 0) {
-        // Of CTA j of the pair: its part (slot 0; 1 if j is the first), its
-        // group's result (2; 3).
-        cr = cross[pass];
-        g0 = phase == 2 ? 0 : ((int)blockIdx.x - cr.first) / kFp4Gather * kFp4Gather;
-        n = phase == 2 ? (cr.n + kFp4Gather - 1) / kFp4Gather : min(kFp4Gather, cr.n - g0);
-        // Copies read and write after this CTA's accesses to the rings and the
-        // other CTAs' stores.
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncthreads();
-        if (warp == 0) {
-          asm volatile("fence.proxy.async;" ::: "memory");
-          if (lane == 0) mbar_arrive_expect_tx(gather_bar, (uint32_t)n * part_bytes);
-          __syncwarp();
-          if (lane < n) {
-            const int j = phase == 2 ? lane * kFp4Gather : g0 + lane;
-            const int slot = (phase == 2 ? 2 : 0) + (j == 0);
-            bulk_load(smem_u32(smem) + lane * part_bytes,
-                      p.cta_partials + ((size_t)(cr.first + j) * 4 + slot) * part_floats,
-                      part_bytes, gather_bar);
-          }
-        }
-        mbar_wait_bounded(gather_bar, gathers & 1, p.err);
-        ++gathers;
-      }
-      // Units of run r are [r * per_run, (r + 1) * per_run); unit u is warp
-      // u mod W's.  Parts i < n lie `step` bytes apart from `base` on, but for
-      // part `odd`.
-      const int per_run = rows * kSplit;
-      uint32_t left = phase == 0 ? live : 1u;
-      for (int u0 = 0; left; left &= left - 1, u0 += per_run) {
-        int unit = (warp - u0) & (W - 1);
-        if (unit >= per_run) continue;
-        const uint8_t* base = smem;
-        const float* odd_part = nullptr;
-        uint32_t step = part_bytes;
-        int odd = -1;
-        float* to = nullptr;  // the merged part, or NULL: final rows
-        if (phase == 0) {
-          const int which = __ffs(left) - 1;
-          const Fp4Run run = runs[which];
-          cr.s = run.s;
-          cr.head0 = run.head0;
-          cr.heads = run.heads;
-          n = (which >> 1) - run.first + 1;
-          base = smem + run.first * C::kWarpRing;
-          step = C::kWarpRing;
-          if (!(which & 1)) {
-            odd = n - 1;
-            odd_part = p.warp_partials + ((size_t)blockIdx.x * W + (which >> 1)) * part_floats;
-          }
-          const bool before = run.at < cta0;
-          if (before || run.at + run.n > cta1)
-            to = p.cta_partials + ((size_t)blockIdx.x * 4 + !before) * part_floats;
-        } else if (phase == 1 && cr.n > kFp4Gather) {
-          to = p.cta_partials + ((size_t)(cr.first + g0) * 4 + 2 + (g0 == 0)) * part_floats;
-        }
-        auto part = [&](int i) {
-          return i == odd ? odd_part : reinterpret_cast<const float*>(base + i * step);
-        };
-        for (; unit < cr.heads * kSplit; unit += W) {
-          const int head = unit / kSplit;
-          const int col = unit * 32 * kVec + lane * kVec;
-          float mi = -INFINITY, li = 0.f;
-          if (lane < n) {
-            const float* src = part(lane) + rows * D + head;
-            mi = src[0];
-            li = src[rows];
-          }
-          const float top = warp_max_redux(mi);
-          const float w = mi == top ? 1.f : fast_exp2(mi - top);
-          float sum = lane < n ? li * w : 0.f, acc[kVec];
-#pragma unroll
-          for (int o = 1; o < kFp4Gather; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          sum = __shfl_sync(0xffffffffu, sum, 0);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float* src = part(i) + col;
-#pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-              const float2 v = *reinterpret_cast<const float2*>(src + e);
-              acc[e] = fmaf(v.x, wi, acc[e]);
-              acc[e + 1] = fmaf(v.y, wi, acc[e + 1]);
-            }
-          }
-          const float inv = to ? 1.f : __fdividef(p.value_scale, sum);
-          T* dst = static_cast<T*>(p.out) + ((size_t)cr.s * p.num_heads + cr.head0) * D + col;
-#pragma unroll
-          for (int e = 0; e < kVec; e += 2) {
-            const float2 v = make_float2(acc[e] * inv, acc[e + 1] * inv);
-            if (to) *reinterpret_cast<float2*>(to + col + e) = v;
-            else if constexpr (kF32) *reinterpret_cast<float2*>(dst + e) = v;
-            else *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(v.x, v.y);
-          }
-          if (to && col == head * D) {  // the head's first lane
-            to[rows * D + head] = top;
-            to[rows * D + rows + head] = sum;
-          }
-        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        __syncwarp();
+        n = parts;
+        const float* slot0 = p.cta_partials + ((size_t)first * 4 + 2 * level) * part_floats;
+        base = reinterpret_cast<const uint8_t*>(slot0);
+        step = (level == 0 ? 1u : (uint32_t)kFp4Gather) * 16u * part_floats;
+        odd = first == run.cta0 ? 0 : -1;
+        odd_part = slot0 + part_floats;
       }
     }
-    if (cross[0].s < 0 && cross[1].s < 0) return;
   }
 }
 

@@ -415,6 +415,41 @@ def test_decode_refuses_small_workspaces():
     assert e.value.status == pa.PA_ERR_INVALID_ARG
 
 
+def test_decode_waits_that_give_up_leave_the_workspace_usable():
+    # A limit of one cycle, and more to read than L2 holds, so that most waits
+    # for a copy find it not yet there and give up.
+    head, hkv, block, lens = 128, 8, 16, [120_000, 5, 0, 60_001]
+    counts = [-(-n // block) for n in lens]
+    cache = torch.randint(0, 256, (sum(counts), hkv, block // 8, 9 * head), dtype=torch.uint8,
+                          device="cuda")
+    cache[..., 8 * head:] = 0x38          # every scale is one
+    tables = torch.zeros((4, max(counts)), dtype=torch.int32)
+    ids, at = torch.randperm(sum(counts)).int(), 0
+    for r, c in enumerate(counts):
+        tables[r, :c] = ids[at:at + c]
+        at += c
+    tables, lens = tables.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn((4, 16, head), device="cuda").bfloat16()
+    ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(cache, 16), "cuda")
+
+    def call():
+        out = torch.full_like(q, 5.0)
+        pa.pa_decode_fp4(out, q, cache, tables, lens, head ** -0.5, ws)
+        return out
+
+    first = call()
+    assert pa.pa_get_device_error() == 0 and not (first == 5.0).all(-1).any()
+    pa.pa_set_decode_wait_limit(1)
+    try:
+        call()
+        assert pa.pa_get_device_error() == pa.PA_DEVERR_TIMEOUT
+    finally:
+        pa.pa_set_decode_wait_limit(0)
+    for _ in range(2):
+        assert torch.equal(call(), first)
+    assert pa.pa_get_device_error() == 0
+
+
 # ---------------------------------------------------------------------------
 # tables
 # ---------------------------------------------------------------------------
