@@ -1,18 +1,21 @@
-// Dispatch of the 4-bit decode over head sizes, and its workspace.
+// Dispatch of the 4-bit decode over element types and head sizes, and its workspace.
 #include "decode_fp4.cuh"
 #include "pa_launch.h"
 
 namespace pa {
 
-cudaError_t launch_decode_fp4_d64(const Fp4DecodeParams&, int dtype, int num_sms, cudaStream_t);
-cudaError_t launch_decode_fp4_d128(const Fp4DecodeParams&, int dtype, int num_sms, cudaStream_t);
-cudaError_t launch_decode_fp4_d256(const Fp4DecodeParams&, int dtype, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_bf16_d64(const Fp4DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_bf16_d128(const Fp4DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_bf16_d256(const Fp4DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_f32_d64(const Fp4DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_f32_d128(const Fp4DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_fp4_f32_d256(const Fp4DecodeParams&, int num_sms, cudaStream_t);
 
 namespace {
 
 // Floats of one partial result at most, whatever the element type.
 size_t partial_floats(int head_size, int group) {
-  return fp4_partial_floats(fp4_unit_rows(fp4_head_tiles(head_size, group), group), head_size, 2);
+  return fp4_partial_floats(fp4_unit_rows(fp4_heads(head_size, group), group), head_size, 2);
 }
 
 }  // namespace
@@ -29,10 +32,17 @@ cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, in
   p.warp_partials =
       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFp4HeaderBytes);
   p.cta_partials = p.warp_partials + (size_t)num_sms * 16 * partial_floats(p.head_size, p.group);
+  const bool half = dtype == PA_BF16;
   switch (p.head_size) {
-    case 64: return launch_decode_fp4_d64(p, dtype, num_sms, stream);
-    case 128: return launch_decode_fp4_d128(p, dtype, num_sms, stream);
-    default: return launch_decode_fp4_d256(p, dtype, num_sms, stream);
+    case 64:
+      return half ? launch_decode_fp4_bf16_d64(p, num_sms, stream)
+                  : launch_decode_fp4_f32_d64(p, num_sms, stream);
+    case 128:
+      return half ? launch_decode_fp4_bf16_d128(p, num_sms, stream)
+                  : launch_decode_fp4_f32_d128(p, num_sms, stream);
+    default:
+      return half ? launch_decode_fp4_bf16_d256(p, num_sms, stream)
+                  : launch_decode_fp4_f32_d256(p, num_sms, stream);
   }
 }
 

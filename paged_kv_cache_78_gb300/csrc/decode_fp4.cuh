@@ -14,25 +14,29 @@ constexpr int kFp4MaxCtas = kFp4Gather * kFp4Gather;
 constexpr int kFp4Units = 32;          // units of a pair that are merged by themselves
 constexpr int kFp4HeaderBytes = kFp4MaxCtas * 3 * kFp4Units * 4;  // three counters per CTA and unit
 
-// Two tiles of eight query heads (columns of the matrix instructions) where
-// the registers hold them, one otherwise: groups past eight heads of 256
-// elements then read the keys and values once per tile.
-__host__ __device__ constexpr int fp4_head_tiles(int head_size, int group) {
-  return group > 8 && head_size <= 128 ? 2 : 1;
+// Query heads of a unit of work (columns of the matrix instructions): 4, 8, or
+// 16 where the registers hold them; groups past eight heads of 256 elements read
+// the keys and values once per eight heads.
+__host__ __device__ constexpr int fp4_heads(int head_size, int group) {
+  return group <= 4 ? 4 : group <= 8 || head_size == 256 ? 8 : 16;
 }
 
 // Warps of a CTA (one CTA per SM): 16 where a thread's accumulators and query
 // fragments leave room in 128 registers, else 8.
-__host__ __device__ constexpr int fp4_warps(int head_size, int tiles, bool fp32) {
-  return head_size / 16 * tiles * (fp32 ? 8 : 6) <= 48 ? 16 : 8;
+__host__ __device__ constexpr int fp4_warps(int head_size, int heads, bool fp32) {
+  return (heads == 4 ? head_size / 8 : head_size / 32 * heads) +
+                     head_size / 8 * (heads == 16 ? 2 : 1) * (fp32 ? 2 : 1) <=
+                 48
+             ? 16
+             : 8;
 }
 
 // Rows (query heads) of a pair; the units of a head that are merged by
 // themselves; and the floats of a partial result: weighted values, then each
 // unit's maximum, then each unit's sum (units are handed on one by one, so each
 // has its own).
-__host__ __device__ constexpr int fp4_unit_rows(int tiles, int group) {
-  return group < 8 * tiles ? group : 8 * tiles;
+__host__ __device__ constexpr int fp4_unit_rows(int heads, int group) {
+  return group < heads ? group : heads;
 }
 __host__ __device__ constexpr int fp4_splits(int head_size, int rows, int warps) {
   return head_size > 64 && 2 * rows <= warps ? 2 : 1;

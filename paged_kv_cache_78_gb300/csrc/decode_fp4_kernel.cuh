@@ -169,10 +169,10 @@ struct Fp4Run {
   int first, cta0, ctas;
 };
 
-template <typename T, int D, int NT>
+template <typename T, int D, int H>
 struct Fp4Config {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWarps = fp4_warps(D, NT, kF32);
+  static constexpr int kWarps = fp4_warps(D, H, kF32);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = fp4_tile_bytes(D);
   static constexpr int kStageBytes = kFp4Stage / kFp4Tile * kTileBytes;
@@ -186,28 +186,36 @@ struct Fp4Config {
   static constexpr int kSmem = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
   static_assert(kStages >= 2 && kStages + 2 <= kFp4Pieces, "rings");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(fp4_partial_floats(8 * NT, D, 2) * 4 <= kWarpRing, "a part fits its warp's ring");
+  static_assert(fp4_partial_floats(H, D, 2) * 4 <= kWarpRing, "a part fits its warp's ring");
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
+// H: query heads of a unit, 4, 8 or 16.  With four, the matrix instructions'
+// eight columns are the heads twice, for a value's even and odd elements: a
+// byte's two codes are then used as they come, as the two elements of one token
+// (P zero in the other element's place), where otherwise the codes of two tokens
+// have to be brought together first.
+template <typename T, int D, int H>
+__global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     decode_fp4_kernel(const Fp4DecodeParams p) {
-  using C = Fp4Config<T, D, NT>;
+  using C = Fp4Config<T, D, H>;
   constexpr bool kF32 = C::kF32;
   constexpr int W = C::kWarps;
   constexpr int NS = C::kStages;
-  constexpr int kSteps = D / 16;      // of QK; and 16-row tiles of O^T
+  constexpr bool kNarrow = H == 4;
+  constexpr int NT = H == 16 ? 2 : 1;               // tiles of eight columns
+  constexpr int kSteps = D / 16;                    // of QK
+  constexpr int kTiles = kNarrow ? D / 32 : D / 16;  // of O^T
   constexpr int kQParts = kF32 ? 2 : 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.group;
   const int head_tiles = D == 256 ? (G + 7) / 8 : 1;  // of a KV head (see fp4_head_tiles)
-  const int rows = fp4_unit_rows(NT, G);
+  const int rows = fp4_unit_rows(H, G);
   const int per_seq = p.num_kv_heads * head_tiles;  // pairs of a sequence
   const int l2bs = p.log2_block_size;
   // A merge's unit: a head, or half of one where there are two warps per head.
-  constexpr int kSplit = fp4_splits(D, 8 * NT, W);  // units of a head
+  constexpr int kSplit = fp4_splits(D, H, W);  // units of a head
   constexpr int kVec = D / 32 / kSplit;             // columns of a lane
   const int per_run = rows * kSplit;                // units of a pair
   const int part_floats = fp4_partial_floats(rows, D, kSplit);
@@ -219,8 +227,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   // First query head and heads of a pair.
   auto heads_of = [&](int hp, int* heads) -> int {
     const int h = hp / head_tiles, ht = hp - h * head_tiles;
-    *heads = min(8 * NT, G - ht * 8 * NT);
-    return h * G + ht * 8 * NT;
+    *heads = min(H, G - ht * H);
+    return h * G + ht * H;
   };
   // Units before each thread's sequences; the warps' sums.
   int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
     }
 
     uint32_t q[kQParts][NT][kSteps][2];  // Q^T: head g of tile nt, this thread's elements
-    float o[NT][kSteps][4];              // O^T: rows 2j, 2j + 1 of chunk g; heads 2t, 2t + 1
+    float o[NT][kTiles][4];              // O^T: rows 2j, 2j + 1 of chunk g; columns 2t, 2t + 1
     float cs[NT][2], m[NT][2], l[NT][2];
     int slot = 0;
     uint32_t parity = 0;
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
             m[nt][c] = m_new;
             l[nt][c] *= alpha;
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
+            for (int j = 0; j < kTiles; ++j) {
               o[nt][j][c] *= alpha;
               o[nt][j][c + 2] *= alpha;
             }
@@ -569,22 +577,22 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         constexpr int kWords = D == 64 ? 1 : 2;   // words of a part, per token
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
-          uint32_t x[2][kWords], y[2][kWords], vs[2];
+          // Codes and scales of tokens 2t (wa) and 2t + 1 (wb) of both tiles.
+          uint32_t wa[2][kWords], wb[2][kWords], vs[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t tile = stage + (2 * u + e) * C::kTileBytes;
             const int group = D == 64 ? g >> 1 : g * kParts + part;
-            uint32_t wa[kWords], wb[kWords];
             if constexpr (D == 64) {
               const uint32_t at = tile + fp4_value_codes(D) + group * 64 + t * 16 + (g & 1) * 4;
-              wa[0] = lds_u32(at);
-              wb[0] = lds_u32(at + 8);
+              wa[e][0] = lds_u32(at);
+              wb[e][0] = lds_u32(at + 8);
             } else {
               const uint4 v = lds128(tile + fp4_value_codes(D) + group * 64 + t * 16);
-              wa[0] = v.x;
-              wa[1] = v.y;
-              wb[0] = v.z;
-              wb[1] = v.w;
+              wa[e][0] = v.x;
+              wa[e][1] = v.y;
+              wb[e][0] = v.z;
+              wb[e][1] = v.w;
             }
             uint32_t two = lds_u16(tile + fp4_value_scales(D) + group * 8 + 2 * t);
             if (ragged) {
@@ -594,29 +602,57 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
               else if (tok + 1 >= tokens) two &= 0xffu;
             }
             vs[e] = e4m3x2_to_half2(two);
-            // Bytes of the two tokens' codes of one element.
+          }
+          if constexpr (kNarrow) {
+            // Columns of even elements (g < 4) or of odd ones: the weight in that
+            // half, of token 2t, then of token 2t + 1.
+            const uint32_t first = g < 4 ? 0x4410u : 0x1044u;
+            const uint32_t second = g < 4 ? 0x4432u : 0x3244u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t b2[kQParts][2];
+#pragma unroll
+              for (int qp = 0; qp < kQParts; ++qp) {
+                b2[qp][0] = __byte_perm(pt[qp][u][0][e], 0, first);
+                b2[qp][1] = __byte_perm(pt[qp][u][0][e], 0, second);
+              }
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                uint32_t ha[4], hb[4];
+                e2m1x8_to_half2(wa[e][w], ha);
+                e2m1x8_to_half2(wb[e][w], hb);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const uint32_t a[4] = {half2_mul_by<false>(ha[2 * b], vs[e]),
+                                         half2_mul_by<false>(ha[2 * b + 1], vs[e]),
+                                         half2_mul_by<true>(hb[2 * b], vs[e]),
+                                         half2_mul_by<true>(hb[2 * b + 1], vs[e])};
+#pragma unroll
+                  for (int qp = 0; qp < kQParts; ++qp)
+                    mma_f16(o[0][part * 4 + w * 2 + b], a, b2[qp]);
+                }
+              }
+            }
+          } else {
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
-              x[e][w] = (wa[w] & 0x0f0f0f0fu) | ((wb[w] << 4) & 0xf0f0f0f0u);
-              y[e][w] = ((wa[w] >> 4) & 0x0f0f0f0fu) | (wb[w] & 0xf0f0f0f0u);
-            }
-          }
+              // Bytes of the two tokens' codes of one element: even, then odd ones.
+              uint32_t even[2][4], odd[2][4];
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            uint32_t x0[4], y0[4], x1[4], y1[4];
-            e2m1x8_to_half2(x[0][w], x0);
-            e2m1x8_to_half2(y[0][w], y0);
-            e2m1x8_to_half2(x[1][w], x1);
-            e2m1x8_to_half2(y[1][w], y1);
+              for (int e = 0; e < 2; ++e) {
+                e2m1x8_to_half2((wa[e][w] & 0x0f0f0f0fu) | ((wb[e][w] << 4) & 0xf0f0f0f0u), even[e]);
+                e2m1x8_to_half2(((wa[e][w] >> 4) & 0x0f0f0f0fu) | (wb[e][w] & 0xf0f0f0f0u), odd[e]);
+              }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t a[4] = {half2_mul(x0[b], vs[0]), half2_mul(y0[b], vs[0]),
-                                     half2_mul(x1[b], vs[1]), half2_mul(y1[b], vs[1])};
-              const int j = part * 8 + w * 4 + b;
+              for (int b = 0; b < 4; ++b) {
+                const uint32_t a[4] = {half2_mul(even[0][b], vs[0]), half2_mul(odd[0][b], vs[0]),
+                                       half2_mul(even[1][b], vs[1]), half2_mul(odd[1][b], vs[1])};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int qp = 0; qp < kQParts; ++qp) mma_f16(o[nt][j], a, pt[qp][u][nt]);
+                  for (int qp = 0; qp < kQParts; ++qp)
+                    mma_f16(o[nt][part * 8 + w * 4 + b], a, pt[qp][u][nt]);
+              }
             }
           }
         }
@@ -634,7 +670,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
       // (bf16 exactly, unless an element is 2^-30 of the largest).
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int head = nt * 8 + g;
+        const int head = nt * 8 + (kNarrow ? g & 3 : g);
         float x[D / 4];
         if (head < heads) {
           const T* src = static_cast<const T*>(p.query) + pc.s * p.query_stride +
@@ -669,7 +705,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j)
+        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
       }
@@ -707,58 +743,75 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
           for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
           ls[nt][c] = v;
         }
-      if (pc.k0 == 0 && pc.stages == pc.n) {
-        // The whole pair: final rows.
+      const bool whole = pc.k0 == 0 && pc.stages == pc.n;
+      // A part goes to the ring at the end of the warp's part (every copy has
+      // landed and been read), to global memory before.
+      float* to = last ? reinterpret_cast<float*>(smem + warp * C::kWarpRing)
+                       : p.warp_partials + ((size_t)blockIdx.x * W + warp) * part_floats;
+      __syncwarp();
+      // Chunk g of one head: a final row, or a part's.
+      auto put = [&](int head, const float* v, float max_, float sum) {
+        if (head >= heads) return;
+        if (whole) {
+          const float inv = __fdividef(p.value_scale, sum);
+          T* dst = static_cast<T*>(p.out) +
+                   ((size_t)pc.s * p.num_heads + head0 + head) * D + g * (D / 8);
+          if constexpr (kF32) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < D / 8; e += 4)
+              *reinterpret_cast<float4*>(dst + e) =
+                  make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int head = nt * 8 + 2 * t + c;
-            if (head >= heads) continue;
-            const float inv = __fdividef(p.value_scale, ls[nt][c]);
-            T* dst = static_cast<T*>(p.out) +
-                     ((size_t)pc.s * p.num_heads + head0 + head) * D + g * (D / 8);
-            if constexpr (kF32) {
+            for (int e = 0; e < D / 8; e += 8)
+              stg_v4(dst + e, make_uint4(pack_bf16x2(v[e] * inv, v[e + 1] * inv),
+                                         pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
+                                         pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv),
+                                         pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv)));
+          }
+        } else {
+          float* dst = to + head * D + g * (D / 8);
 #pragma unroll
-              for (int j = 0; j < kSteps; j += 2)
-                *reinterpret_cast<float4*>(dst + 2 * j) =
-                    make_float4(o[nt][j][c] * inv, o[nt][j][c + 2] * inv, o[nt][j + 1][c] * inv,
-                                o[nt][j + 1][c + 2] * inv);
-            } else {
+          for (int e = 0; e < D / 8; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          if (g == 0)
 #pragma unroll
-              for (int j = 0; j < kSteps; j += 4) {
-                uint32_t w[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  w[b] = pack_bf16x2(o[nt][j + b][c] * inv, o[nt][j + b][c + 2] * inv);
-                stg_v4(dst + 2 * j, make_uint4(w[0], w[1], w[2], w[3]));
-              }
+            for (int sp = 0; sp < kSplit; ++sp) {
+              to[rows * D + head * kSplit + sp] = max_;
+              to[rows * D + per_run + head * kSplit + sp] = sum;
             }
+        }
+      };
+      float v[D / 8];
+      if constexpr (kNarrow) {
+        // Lanes t and t ^ 2 have the even and the odd elements of two heads: one
+        // head whole to each.
+        const bool low = t < 2;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            const float keep = low ? o[0][j][c] : o[0][j][c + 1];
+            const float got =
+                __shfl_xor_sync(0xffffffffu, low ? o[0][j][c + 1] : o[0][j][c], 2);
+            v[4 * j + c] = low ? keep : got;
+            v[4 * j + c + 1] = low ? got : keep;
           }
+        put((t & 1) * 2 + (t >> 1), v, low ? m[0][0] : m[0][1], low ? ls[0][0] : ls[0][1]);
       } else {
-        // A part: to the ring at the end of the warp's part (every copy has
-        // landed and been read), to global memory before.
-        float* dst = last ? reinterpret_cast<float*>(smem + warp * C::kWarpRing)
-                          : p.warp_partials + ((size_t)blockIdx.x * W + warp) * part_floats;
-        __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int head = nt * 8 + 2 * t + c;
-            if (head >= heads) continue;
-            float* od = dst + head * D + g * (D / 8);
 #pragma unroll
-            for (int j = 0; j < kSteps; j += 2)
-              *reinterpret_cast<float4*>(od + 2 * j) =
-                  make_float4(o[nt][j][c], o[nt][j][c + 2], o[nt][j + 1][c], o[nt][j + 1][c + 2]);
-            if (g == 0)
-#pragma unroll
-              for (int sp = 0; sp < kSplit; ++sp) {
-                dst[rows * D + head * kSplit + sp] = m[nt][c];
-                dst[rows * D + per_run + head * kSplit + sp] = ls[nt][c];
-              }
+            for (int j = 0; j < kTiles; ++j) {
+              v[2 * j] = o[nt][j][c];
+              v[2 * j + 1] = o[nt][j][c + 2];
+            }
+            put(nt * 8 + 2 * t + c, v, m[nt][c], ls[nt][c]);
           }
+      }
+      if (!whole) {
         // The warp with the pair's last part in this CTA says where the parts are.
         if (lane == 0 && (ends || pc.at + pc.stages == cta1)) {
           const int at = pc.at - pc.k0;  // the pair's first stage
@@ -799,7 +852,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, NT>::kThreads, 1)
   // 2 us longer).
   if (cta0 >= cta1) return;  // the same for the whole CTA
   __syncthreads();
-  static_assert(W <= kFp4Gather && 8 * NT * kSplit <= kFp4Units, "merges");
+  static_assert(W <= kFp4Gather && H * kSplit <= kFp4Units, "merges");
   uint32_t live = __ballot_sync(0xffffffffu, lane < 2 * W && runs[lane % (2 * W)].s >= 0);
   for (int u0 = 0; live; live &= live - 1, u0 += per_run) {
     // Unit u of all runs' is warp u mod W's.
