@@ -504,9 +504,10 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
  * are passed on as they were, slots and positions are all -1, starts all 0.
  * A block id outside [0, num_blocks) records PA_DEVERR_BLOCK_ID and gives its
  * tokens slot -1.  num_seqs is at most PA_MAX_TABLE_REQUESTS, max_tokens at
- * most 2^30 (else PA_ERR_INVALID_ARG); with num_seqs == 0 the slots are all
- * -1.  Buffers that are not the same must not overlap. */
+ * most PA_MAX_TABLE_TOKENS (else PA_ERR_INVALID_ARG); with num_seqs == 0 the
+ * slots are all -1.  Buffers that are not the same must not overlap. */
 #define PA_MAX_TABLE_REQUESTS 8192
+#define PA_MAX_TABLE_TOKENS ((1 << 26) - 1)
 pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
                            const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
                            int32_t block_size, int32_t num_blocks, const int32_t* free_blocks,

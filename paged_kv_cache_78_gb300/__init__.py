@@ -506,29 +506,43 @@ def pa_decode_shared(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor
 # 4-bit pool and device-side tables
 # ---------------------------------------------------------------------------
 
-def _launch_stream(stream, first: torch.Tensor, *others: torch.Tensor) -> int:
-    """The stream to launch on, once every tensor is found on the current device."""
-    dev = first.get_device()
+def _current_device(t: torch.Tensor, name: str) -> int:
+    """The device of t, which has to be the current one (launches go there)."""
+    dev = t.get_device()
     if dev < 0:
-        raise ValueError("every tensor must be a CUDA tensor")
+        raise ValueError("%s must be a CUDA tensor" % name)
     if dev != torch._C._cuda_getDevice():
-        raise ValueError("the tensors are on device %d, which is not the current one" % dev)
-    for t in others:
-        if t.get_device() != dev:
-            raise ValueError("every tensor must be on one device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        raise ValueError("%s is on device %d, which is not the current one" % (name, dev))
+    return dev
 
 
-def _rows(t: torch.Tensor, name: str, heads: int, head_size: int):
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
+    """Address of a contiguous tensor of one type on one device."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on CUDA device %d" % (name, dev))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, heads: int, head_size: int, dev: int):
     """Address and row stride (elements) of [n, heads, head_size] rows, which
     may lie apart (a slice of a fused projection's output)."""
     n, h, d = t.shape
     if h != heads or d != head_size:
         raise ValueError("%s must be [n, %d, %d], got %s" % (name, heads, head_size, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on CUDA device %d" % (name, dev))
     row, inner, one = t.stride()
     if (one != 1 and d > 1) or (inner != d and h > 1):
         raise ValueError("%s: each row's heads must be contiguous" % name)
     return t.data_ptr(), (row if n > 1 else heads * head_size)
+
+
+def _on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -539,20 +553,20 @@ def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torc
     with a scale per 16 elements; key_scale / value_scale are the pool's
     tensor scales (powers of two)."""
     desc = fp4_cache_desc(cache)
-    n = key.shape[0]
     if key.shape != value.shape or key.dim() != 3:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
-    if key.dtype != value.dtype:
+    if key.dtype is not value.dtype:
         raise TypeError("key and value must have the same dtype")
+    n = key.shape[0]
     if slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be [num_tokens]")
-    on = _launch_stream(stream, cache, key, value, slot_mapping)
-    kp, ks = _rows(key, "key", desc.num_kv_heads, desc.head_size)
-    vp, vs = _rows(value, "value", desc.num_kv_heads, desc.head_size)
+    dev = _current_device(cache, "cache")
+    kp, ks = _rows(key, "key", desc.num_kv_heads, desc.head_size, dev)
+    vp, vs = _rows(value, "value", desc.num_kv_heads, desc.head_size, dev)
     _check(lib.pa_reshape_and_cache_fp4(cache.data_ptr(), ctypes.byref(desc), kp, vp,
                                         _dtype_code(key), ks, vs,
-                                        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
-                                        key_scale, value_scale, on),
+                                        _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
+                                        key_scale, value_scale, _on(stream, dev)),
            "pa_reshape_and_cache_fp4")
 
 
@@ -563,18 +577,19 @@ def pa_gather_cache_fp4(key: torch.Tensor, value: torch.Tensor, cache: torch.Ten
     head_size] (bf16 or fp32, contiguous) receive what the slots hold; rows of
     negative slots stay as they were."""
     desc = fp4_cache_desc(cache)
-    n = key.shape[0]
-    if key.shape != value.shape or tuple(key.shape[1:]) != (desc.num_kv_heads, desc.head_size):
+    if key.dim() != 3 or key.shape != value.shape:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
-    if key.dtype != value.dtype:
-        raise TypeError("key and value must have the same dtype")
+    n, h, d = key.shape
+    if h != desc.num_kv_heads or d != desc.head_size:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
     if slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be [num_tokens]")
-    on = _launch_stream(stream, cache, key, value, slot_mapping)
-    _check(lib.pa_gather_cache_fp4(_dev_ptr(key, "key"), _dev_ptr(value, "value"),
-                                   _dtype_code(key), cache.data_ptr(), ctypes.byref(desc),
-                                   _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
-                                   key_scale, value_scale, on),
+    dev = _current_device(cache, "cache")
+    _check(lib.pa_gather_cache_fp4(_arg(key, "key", key.dtype, dev),
+                                   _arg(value, "value", key.dtype, dev), _dtype_code(key),
+                                   cache.data_ptr(), ctypes.byref(desc),
+                                   _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
+                                   key_scale, value_scale, _on(stream, dev)),
            "pa_gather_cache_fp4")
 
 
@@ -599,18 +614,18 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
     s, hq, d = query.shape
     if out.shape != query.shape or d != desc.head_size:
         raise ValueError("query/out must be [num_seqs, num_heads, head_size]")
-    if query.dtype != out.dtype:
+    if query.dtype is not out.dtype:
         raise TypeError("query and out must have the same dtype")
     if block_tables.dim() != 2 or block_tables.shape[0] != s or seq_lens.shape != (s,):
         raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
-    on = _launch_stream(stream, cache, out, query, block_tables, seq_lens, workspace)
-    qp, qs = _rows(query, "query", hq, d)
-    _check(lib.pa_decode_fp4(_dev_ptr(out, "out"), qp, _dtype_code(query), qs, cache.data_ptr(),
-                             ctypes.byref(desc), key_scale, value_scale,
-                             _dev_ptr(block_tables, "block_tables", torch.int32),
-                             block_tables.shape[1], _dev_ptr(seq_lens, "seq_lens", torch.int32), s,
-                             hq, scale, _dev_ptr(workspace, "workspace"), workspace.nbytes,
-                             on), "pa_decode_fp4")
+    dev = _current_device(cache, "cache")
+    qp, qs = _rows(query, "query", hq, d, dev)
+    _check(lib.pa_decode_fp4(_arg(out, "out", query.dtype, dev), qp, _dtype_code(query), qs,
+                             cache.data_ptr(), ctypes.byref(desc), key_scale, value_scale,
+                             _arg(block_tables, "block_tables", torch.int32, dev),
+                             block_tables.shape[1], _arg(seq_lens, "seq_lens", torch.int32, dev), s,
+                             hq, scale, _arg(workspace, "workspace", workspace.dtype, dev),
+                             workspace.nbytes, _on(stream, dev)), "pa_decode_fp4")
 
 
 def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
@@ -647,21 +662,21 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
     if free_state is not None and (free_state.shape != (2,) or free_state_out.shape != (2,) or
                                    free_blocks.dim() != 1):
         raise ValueError("free_blocks must be [capacity], free_state [2]")
-    given = [t for t in (seq_lens, new_tokens, slot_mapping, positions, token_starts, seq_lens_out,
-                         free_blocks, free_state, free_state_out) if t is not None]
-    on = _launch_stream(stream, block_tables, *given)
-
-    def ptr(t, name, dtype=torch.int32):
-        return None if t is None else _dev_ptr(t, name, dtype)
-
+    dev = _current_device(block_tables, "block_tables")
+    i32 = torch.int32
     _check(lib.pa_extend_tables(
-        ptr(block_tables, "block_tables"), block_tables.shape[1], ptr(seq_lens, "seq_lens"),
-        ptr(new_tokens, "new_tokens"), n, block_size, num_blocks, ptr(free_blocks, "free_blocks"),
-        0 if free_blocks is None else free_blocks.shape[0], ptr(free_state, "free_state"),
-        ptr(seq_lens_out, "seq_lens_out"), ptr(free_state_out, "free_state_out"),
-        ptr(slot_mapping, "slot_mapping", torch.int64), ptr(positions, "positions"),
-        ptr(token_starts, "token_starts"), slot_mapping.shape[0], on),
-        "pa_extend_tables")
+        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+        _arg(seq_lens, "seq_lens", i32, dev), _arg(new_tokens, "new_tokens", i32, dev), n,
+        block_size, num_blocks,
+        None if free_blocks is None else _arg(free_blocks, "free_blocks", i32, dev),
+        0 if free_blocks is None else free_blocks.shape[0],
+        None if free_state is None else _arg(free_state, "free_state", i32, dev),
+        _arg(seq_lens_out, "seq_lens_out", i32, dev),
+        None if free_state is None else _arg(free_state_out, "free_state_out", i32, dev),
+        _arg(slot_mapping, "slot_mapping", torch.int64, dev),
+        None if positions is None else _arg(positions, "positions", i32, dev),
+        None if token_starts is None else _arg(token_starts, "token_starts", i32, dev),
+        slot_mapping.shape[0], _on(stream, dev)), "pa_extend_tables")
 
 
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20

@@ -13,7 +13,6 @@
 namespace {
 
 constexpr int kFp4MaxGroup = 16;
-constexpr int32_t kMaxTableTokens = 1 << 30;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -193,7 +192,7 @@ pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
                            void* stream) {
   if (num_seqs < 0 || num_seqs > PA_MAX_TABLE_REQUESTS || max_blocks_per_seq < 1 ||
       !is_pow2(block_size) || block_size > 256 || num_blocks < 1 || max_tokens < 0 ||
-      max_tokens > kMaxTableTokens)
+      max_tokens > PA_MAX_TABLE_TOKENS)
     return PA_ERR_INVALID_ARG;
   const bool ring = free_blocks || free_state || free_state_out || free_capacity != 0;
   if (ring && (!free_blocks || !free_state || !free_state_out || free_capacity < 1 ||
@@ -208,8 +207,10 @@ pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
       !aligned(token_starts, 4))
     return PA_ERR_INVALID_ARG;
   pa::TablesParams p = {};
-  pa_status st = pa::device_state(&p.err, nullptr);
+  int sms = 0;
+  pa_status st = pa::device_state(&p.err, &sms);
   if (st != PA_OK) return st;
+  p.in_place = seq_lens_out == seq_lens || (ring && free_state_out == free_state);
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
   p.new_tokens = new_tokens;
@@ -226,7 +227,7 @@ pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
   p.num_blocks = num_blocks;
   p.free_capacity = free_capacity;
   p.max_tokens = max_tokens;
-  return cuda_status(pa::launch_extend_tables(p, static_cast<cudaStream_t>(stream)));
+  return cuda_status(pa::launch_extend_tables(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

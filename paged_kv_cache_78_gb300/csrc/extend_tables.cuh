@@ -17,6 +17,7 @@ struct TablesParams {
   int32_t* positions;     // may be NULL
   int32_t* token_starts;  // may be NULL
   unsigned int* err;
+  bool in_place;  // an output is its input: the CTAs are one cluster
   int max_blocks_per_seq, num_seqs, log2_block_size, num_blocks, free_capacity, max_tokens;
 };
 

@@ -123,6 +123,6 @@ long long decode_wait_limit();
 
 // Block tables, slot map and positions from request lengths.
 struct TablesParams;
-cudaError_t launch_extend_tables(const TablesParams& params, cudaStream_t stream);
+cudaError_t launch_extend_tables(const TablesParams& params, int num_sms, cudaStream_t stream);
 
 }  // namespace pa

@@ -241,7 +241,7 @@ def tables_call(**kw):
 
 def test_table_refusals():
     bad = [dict(n=-1), dict(n=8193), dict(mb=0), dict(bs=12), dict(bs=512), dict(nb=0),
-           dict(most=-1), dict(most=(1 << 30) + 1), dict(tables=None), dict(lens=None),
+           dict(most=-1), dict(most=(1 << 30) + 1), dict(most=1 << 26), dict(tables=None), dict(lens=None),
            dict(new=None), dict(lens_out=None), dict(slots=None), dict(ring=None),
            dict(state=None), dict(state_out=None), dict(cap=0), dict(cap=-3),
            dict(cap=(1 << 30) + 1), dict(slots=ctypes.c_void_p(260)),
