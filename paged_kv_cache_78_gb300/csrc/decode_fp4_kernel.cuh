@@ -105,6 +105,37 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, const uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// c = a . b.
+__device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+
+// Products added to c: by the matrix unit, or (kShort) in a chain of their own that
+// done() adds with rounding.  The unit cuts its sums off towards zero, which makes a
+// sum over n products about n * 2^-25 too small: over a warp's 12600 tokens 1.3e-4.
+// That is less than bf16's half step of 2^-8 by far (short chains would cost 1% of the
+// time at four heads of 128, 9% at eight), but not fp32's, where chains end with
+// their stage of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.
+template <bool kShort>
+struct Fp4Sum {
+  float* c;
+  float own[4];
+  __device__ __forceinline__ Fp4Sum(float* to) : c(to) {}
+  __device__ __forceinline__ void operator()(const uint32_t* a, const uint32_t* b, bool first) {
+    if (!kShort) mma_f16(c, a, b);
+    else if (first) mma_f16_first(own, a, b);
+    else mma_f16(own, a, b);
+  }
+  __device__ __forceinline__ void done() {
+    if (kShort)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] += own[i];
+  }
+};
+
 // The 8 x 8 matrix of 16-bit elements that the warp holds, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -445,11 +476,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
       float sc[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[u][nt][c] = 0.f;
         constexpr int kWords = D / 32;  // of a thread's quarter row
+        constexpr int kSum = !kF32 ? kWords : D == 64 ? 1 : 2;  // words of one chain
+        float own[NT][4];
         uint32_t kw[2][kWords], ks[2][(D + 127) / 128];  // codes; scales, two to a word
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -489,13 +518,27 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
                               : half2_mul_by<false>(hi[b], ks[1][w / 4]);
           }
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint32_t a[4] = {lo[2 * b], hi[2 * b], lo[2 * b + 1], hi[2 * b + 1]};
+          for (int nt = 0; nt < NT; ++nt) {
+            // The matrix unit cuts its sums off towards zero.  For fp32 they are kept
+            // short, a quarter or half of a row, and added up with rounding: chains
+            // over the whole row made outputs up to 2.8e-6 wrong (D = 256, 30000
+            // tokens; now 9e-7, an unfused fp32 form 8e-7 to 3e-6).
+            float* sum = kF32 ? own[nt] : sc[u][nt];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t a[4] = {lo[2 * b], hi[2 * b], lo[2 * b + 1], hi[2 * b + 1]};
 #pragma unroll
-              for (int part = 0; part < kQParts; ++part)
-                mma_f16(sc[u][nt], a, q[part][nt][2 * w + b]);
+              for (int part = 0; part < kQParts; ++part) {
+                if (b == 0 && part == 0 && w % kSum == 0)
+                  mma_f16_first(sum, a, q[part][nt][2 * w + b]);
+                else
+                  mma_f16(sum, a, q[part][nt][2 * w + b]);
+              }
+            }
+            if (kF32 && w % kSum == kSum - 1)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                sc[u][nt][c] = w == kSum - 1 ? own[nt][c] : sc[u][nt][c] + own[nt][c];
           }
         }
       }
@@ -571,89 +614,106 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           }
 
       // ---- values ----
+      constexpr int kParts = D == 256 ? 2 : 1;  // groups of a thread's chunk of D / 8 elements
+      constexpr int kWords = D == 64 ? 1 : 2;   // words of a part, per token
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        constexpr int kParts = D == 256 ? 2 : 1;  // groups of a thread's chunk of D / 8 elements
-        constexpr int kWords = D == 64 ? 1 : 2;   // words of a part, per token
+      for (int part = 0; part < kParts; ++part) {
+        // Codes and scales of tokens 2t (wa) and 2t + 1 (wb) of the stage's tiles.
+        uint32_t wa[4][kWords], wb[4][kWords], vs[4];
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          // Codes and scales of tokens 2t (wa) and 2t + 1 (wb) of both tiles.
-          uint32_t wa[2][kWords], wb[2][kWords], vs[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t tile = stage + (2 * u + e) * C::kTileBytes;
-            const int group = D == 64 ? g >> 1 : g * kParts + part;
-            if constexpr (D == 64) {
-              const uint32_t at = tile + fp4_value_codes(D) + group * 64 + t * 16 + (g & 1) * 4;
-              wa[e][0] = lds_u32(at);
-              wb[e][0] = lds_u32(at + 8);
-            } else {
-              const uint4 v = lds128(tile + fp4_value_codes(D) + group * 64 + t * 16);
-              wa[e][0] = v.x;
-              wa[e][1] = v.y;
-              wb[e][0] = v.z;
-              wb[e][1] = v.w;
-            }
-            uint32_t two = lds_u16(tile + fp4_value_scales(D) + group * 8 + 2 * t);
-            if (ragged) {
-              // Rows past the sequence's end hold anything: a zero scale.
-              const int tok = u * 16 + e * 8 + 2 * t;
-              if (tok >= tokens) two = 0;
-              else if (tok + 1 >= tokens) two &= 0xffu;
-            }
-            vs[e] = e4m3x2_to_half2(two);
-          }
-          if constexpr (kNarrow) {
-            // Columns of even elements (g < 4) or of odd ones: the weight in that
-            // half, of token 2t, then of token 2t + 1.
-            const uint32_t first = g < 4 ? 0x4410u : 0x1044u;
-            const uint32_t second = g < 4 ? 0x4432u : 0x3244u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t b2[kQParts][2];
-#pragma unroll
-              for (int qp = 0; qp < kQParts; ++qp) {
-                b2[qp][0] = __byte_perm(pt[qp][u][0][e], 0, first);
-                b2[qp][1] = __byte_perm(pt[qp][u][0][e], 0, second);
-              }
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                uint32_t ha[4], hb[4];
-                e2m1x8_to_half2(wa[e][w], ha);
-                e2m1x8_to_half2(wb[e][w], hb);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const uint32_t a[4] = {half2_mul_by<false>(ha[2 * b], vs[e]),
-                                         half2_mul_by<false>(ha[2 * b + 1], vs[e]),
-                                         half2_mul_by<true>(hb[2 * b], vs[e]),
-                                         half2_mul_by<true>(hb[2 * b + 1], vs[e])};
-#pragma unroll
-                  for (int qp = 0; qp < kQParts; ++qp)
-                    mma_f16(o[0][part * 4 + w * 2 + b], a, b2[qp]);
-                }
-              }
-            }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t tile = stage + e * C::kTileBytes;
+          const int group = D == 64 ? g >> 1 : g * kParts + part;
+          if constexpr (D == 64) {
+            const uint32_t at = tile + fp4_value_codes(D) + group * 64 + t * 16 + (g & 1) * 4;
+            wa[e][0] = lds_u32(at);
+            wb[e][0] = lds_u32(at + 8);
           } else {
+            const uint4 v = lds128(tile + fp4_value_codes(D) + group * 64 + t * 16);
+            wa[e][0] = v.x;
+            wa[e][1] = v.y;
+            wb[e][0] = v.z;
+            wb[e][1] = v.w;
+          }
+          uint32_t two = lds_u16(tile + fp4_value_scales(D) + group * 8 + 2 * t);
+          if (ragged) {
+            // Rows past the sequence's end hold anything: a zero scale.
+            const int tok = e * 8 + 2 * t;
+            if (tok >= tokens) two = 0;
+            else if (tok + 1 >= tokens) two &= 0xffu;
+          }
+          vs[e] = e4m3x2_to_half2(two);
+        }
+        if constexpr (kNarrow) {
+          // Columns of even elements (g < 4) or of odd ones: the weight in that
+          // half, of token 2t, then of token 2t + 1.
+          const uint32_t first = g < 4 ? 0x4410u : 0x1044u;
+          const uint32_t second = g < 4 ? 0x4432u : 0x3244u;
+          uint32_t b2[4][kQParts][2];
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int qp = 0; qp < kQParts; ++qp) {
+              b2[e][qp][0] = __byte_perm(pt[qp][e / 2][0][e % 2], 0, first);
+              b2[e][qp][1] = __byte_perm(pt[qp][e / 2][0][e % 2], 0, second);
+            }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            Fp4Sum<kF32> add[2] = {o[0][part * 4 + w * 2], o[0][part * 4 + w * 2 + 1]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t ha[4], hb[4];
+              e2m1x8_to_half2(wa[e][w], ha);
+              e2m1x8_to_half2(wb[e][w], hb);
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const uint32_t a[4] = {half2_mul_by<false>(ha[2 * b], vs[e]),
+                                       half2_mul_by<false>(ha[2 * b + 1], vs[e]),
+                                       half2_mul_by<true>(hb[2 * b], vs[e]),
+                                       half2_mul_by<true>(hb[2 * b + 1], vs[e])};
+#pragma unroll
+                for (int qp = 0; qp < kQParts; ++qp) add[b](a, b2[e][qp], e == 0 && qp == 0);
+              }
+            }
+            add[0].done();
+            add[1].done();
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            float own[NT][4][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
               // Bytes of the two tokens' codes of one element: even, then odd ones.
               uint32_t even[2][4], odd[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                e2m1x8_to_half2((wa[e][w] & 0x0f0f0f0fu) | ((wb[e][w] << 4) & 0xf0f0f0f0u), even[e]);
-                e2m1x8_to_half2(((wa[e][w] >> 4) & 0x0f0f0f0fu) | (wb[e][w] & 0xf0f0f0f0u), odd[e]);
+                const uint32_t a2 = wa[2 * u + e][w], b2 = wb[2 * u + e][w];
+                e2m1x8_to_half2((a2 & 0x0f0f0f0fu) | ((b2 << 4) & 0xf0f0f0f0u), even[e]);
+                e2m1x8_to_half2(((a2 >> 4) & 0x0f0f0f0fu) | (b2 & 0xf0f0f0f0u), odd[e]);
               }
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
-                const uint32_t a[4] = {half2_mul(even[0][b], vs[0]), half2_mul(odd[0][b], vs[0]),
-                                       half2_mul(even[1][b], vs[1]), half2_mul(odd[1][b], vs[1])};
+                const uint32_t a[4] = {
+                    half2_mul(even[0][b], vs[2 * u]), half2_mul(odd[0][b], vs[2 * u]),
+                    half2_mul(even[1][b], vs[2 * u + 1]), half2_mul(odd[1][b], vs[2 * u + 1])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int qp = 0; qp < kQParts; ++qp)
-                    mma_f16(o[nt][part * 8 + w * 4 + b], a, pt[qp][u][nt]);
+                  for (int qp = 0; qp < kQParts; ++qp) {
+                    if (!kF32) mma_f16(o[nt][part * 8 + w * 4 + b], a, pt[qp][u][nt]);
+                    else if (u == 0 && qp == 0) mma_f16_first(own[nt][b], a, pt[qp][u][nt]);
+                    else mma_f16(own[nt][b], a, pt[qp][u][nt]);
+                  }
               }
             }
+            if constexpr (kF32)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) o[nt][part * 8 + w * 4 + b][c] += own[nt][b][c];
           }
         }
       }
