@@ -423,12 +423,15 @@ pa_status pa_decode_no_alloc(void* out, const void* query, const void* cache,
  *                 strides are multiples of 16 bytes.
  *   slot_mapping  as in pa_reshape_and_cache: negative slots are padding, a
  *                 slot past the pool is skipped and records PA_DEVERR_SLOT.
+ *                 Slots must be distinct (two tokens writing one slot may leave
+ *                 codes of one and scales of the other).
  *
  * pa_gather_cache_fp4 reads tokens back: key / value [num_tokens]
  * [num_kv_heads][head_size], contiguous, 16-byte aligned, receive the numbers
  * that the slots hold (a prompt chunk's attention over its cached prefix
  * needs them).  Rows of negative slots are left as they were, and so are rows
  * of slots past the pool, which record PA_DEVERR_SLOT.  A slot may repeat.
+ * key, value and the cache must not overlap (PA_ERR_INVALID_ARG).
  * num_tokens == 0 is a no-op for both.
  * ------------------------------------------------------------------------- */
 pa_status pa_reshape_and_cache_fp4(void* cache, const pa_cache_desc* desc, const void* key,
@@ -446,7 +449,8 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
  *   out    device, [num_seqs][num_heads][head_size] of `dtype`, contiguous.
  *   query  device, [num_seqs] rows of [num_heads][head_size] of `dtype`,
  *          query_stride elements apart; pointer and stride are multiples of
- *          16 bytes, and so is `out`.
+ *          16 bytes, and so is `out`, which must not overlap the queries
+ *          (PA_ERR_INVALID_ARG).
  * Tables, lengths, scale and their errors are pa_decode's: a length of 0
  * gives zero rows, a length past the table's row records PA_DEVERR_SEQ_LEN and
  * leaves its rows undefined, an id outside the pool records
@@ -459,8 +463,9 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
  * two fp16 parts for fp32 outputs; queries likewise (bf16 queries are exact).
  *   workspace  device scratch of pa_decode_fp4_workspace_size bytes, 256-byte
  *              aligned, zeroed once at allocation; every call leaves its
- *              counters zero.  Calls that overlap on the GPU need separate
- *              workspaces. */
+ *              counters zero.  It serves pa_decode_fp4 calls of any shape it is
+ *              large enough for, one after another, and no other call; calls
+ *              that overlap on the GPU need separate workspaces. */
 pa_status pa_decode_fp4_workspace_size(const pa_cache_desc* desc, int32_t num_heads,
                                        size_t* bytes);
 pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t query_stride,
@@ -505,7 +510,8 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
  * A block id outside [0, num_blocks) records PA_DEVERR_BLOCK_ID and gives its
  * tokens slot -1.  num_seqs is at most PA_MAX_TABLE_REQUESTS, max_tokens at
  * most PA_MAX_TABLE_TOKENS (else PA_ERR_INVALID_ARG); with num_seqs == 0 the
- * slots are all -1.  Buffers that are not the same must not overlap. */
+ * slots are all -1.  Two buffers of which one is written must not overlap,
+ * apart from the two that may be in place (PA_ERR_INVALID_ARG). */
 #define PA_MAX_TABLE_REQUESTS 8192
 #define PA_MAX_TABLE_TOKENS ((1 << 26) - 1)
 pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -30,6 +30,7 @@ bool tensor_scale_ok(float s) {
 }
 
 bool dtype_ok(int32_t t) { return t == PA_BF16 || t == PA_FP32; }
+int64_t elem_bytes(int32_t dtype) { return dtype == PA_BF16 ? 2 : 4; }
 
 pa_status check_call(const pa_cache_desc* desc, int32_t dtype, float key_scale, float value_scale) {
   const pa_status st = pa::check_fp4_desc(desc);
@@ -42,12 +43,24 @@ pa_status check_call(const pa_cache_desc* desc, int32_t dtype, float key_scale, 
 // Elements per row, and whether rows `stride` elements apart keep 16-byte
 // alignment without overlapping.
 bool stride_ok(int64_t stride, int64_t row, int32_t dtype) {
-  return stride >= row && stride * (dtype == PA_BF16 ? 2 : 4) % 16 == 0;
+  return stride >= row && stride * elem_bytes(dtype) % 16 == 0;
 }
 
 // One grid holds the call: a CTA per eight tokens and two heads, or more.
 bool grid_ok(const pa_cache_desc* d, int64_t num_tokens) {
   return (num_tokens + 7) / 8 * d->num_kv_heads < (1ll << 31);
+}
+
+// A buffer of a call, to tell whether two overlap.
+struct Range {
+  const void* p;
+  int64_t bytes;
+  bool written;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes &&
+         y < x + (uint64_t)a.bytes;
 }
 
 pa::Fp4Pool pool_of(const void* cache, const pa_cache_desc* d) {
@@ -115,6 +128,11 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
   if (!cache || !key || !value || !slot_mapping || !aligned(cache, 16) || !aligned(key, 16) ||
       !aligned(value, 16) || !aligned(slot_mapping, 8) || !grid_ok(desc, num_tokens))
     return PA_ERR_INVALID_ARG;
+  const Range out[2] = {{key, num_tokens * row * elem_bytes(dtype), true},
+                        {value, num_tokens * row * elem_bytes(dtype), true}};
+  const Range pool = {cache, desc->num_blocks * pa::fp4_block_bytes(desc), false};
+  if (overlap(out[0], out[1]) || overlap(out[0], pool) || overlap(out[1], pool))
+    return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = pa::device_state(&err, nullptr)) != PA_OK) return st;
   return cuda_status(pa::launch_fp4_gather(pool_of(cache, desc), key, value, dtype, slot_mapping,
@@ -154,6 +172,10 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
       !aligned(query, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
       !aligned(seq_lens, 4) ||
       !stride_ok(query_stride, (int64_t)num_heads * desc->head_size, dtype))
+    return PA_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)num_heads * desc->head_size;
+  if (overlap({out, num_seqs * row * elem_bytes(dtype), true},
+              {query, ((num_seqs - 1) * query_stride + row) * elem_bytes(dtype), false}))
     return PA_ERR_INVALID_ARG;
   pa::Fp4DecodeParams p = {};
   p.scale_log2 = (float)((double)scale * key_scale * 1.4426950408889634);
@@ -206,6 +228,26 @@ pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
   if ((max_tokens > 0 && !slot_mapping) || !aligned(slot_mapping, 8) || !aligned(positions, 4) ||
       !aligned(token_starts, 4))
     return PA_ERR_INVALID_ARG;
+  // Lengths and the ring's state may be written in place; nothing else may overlap
+  // what the step writes.
+  const int64_t n = num_seqs;
+  const Range buffers[] = {{block_tables, n * max_blocks_per_seq * 4, true},
+                           {seq_lens_out, n * 4, true},
+                           {free_state_out, 8, true},
+                           {slot_mapping, max_tokens * 8ll, true},
+                           {positions, max_tokens * 4ll, true},
+                           {token_starts, (n + 1) * 4, true},
+                           {seq_lens, n * 4, false},
+                           {free_state, 8, false},
+                           {new_tokens, n * 4, false},
+                           {free_blocks, free_capacity * 4ll, false}};
+  constexpr int kBuffers = sizeof buffers / sizeof buffers[0];
+  for (int i = 0; i < kBuffers && buffers[i].written; ++i)
+    for (int j = i + 1; j < kBuffers; ++j) {
+      const bool in_place = ((i == 1 && j == 6) || (i == 2 && j == 7)) &&
+                            buffers[i].p == buffers[j].p;
+      if (!in_place && overlap(buffers[i], buffers[j])) return PA_ERR_INVALID_ARG;
+    }
   pa::TablesParams p = {};
   int sms = 0;
   pa_status st = pa::device_state(&p.err, &sms);

@@ -133,6 +133,11 @@ def test_extend_tables_agrees_with_the_host_pool():
 P = ctypes.c_void_p(256)
 
 
+def far(i):
+    """A buffer's address, away from the others'."""
+    return ctypes.c_void_p(i << 24)
+
+
 def desc(**kw):
     d = dict(num_blocks=16, block_size=16, num_kv_heads=2, head_size=64, dtype=pa.PA_FP4)
     d.update(kw)
@@ -142,7 +147,7 @@ def desc(**kw):
 def write_call(d=None, **kw):
     d = desc() if d is None else d
     return pa.lib.pa_reshape_and_cache_fp4(
-        kw.get("cache", P), ctypes.byref(d), kw.get("key", P), kw.get("value", P),
+        kw.get("cache", far(1)), ctypes.byref(d), kw.get("key", far(2)), kw.get("value", far(3)),
         kw.get("dtype", pa.PA_BF16), kw.get("ks", 128), kw.get("vs", 128), kw.get("slots", P),
         kw.get("n", 4), kw.get("key_scale", 1.0), kw.get("value_scale", 1.0), None)
 
@@ -150,7 +155,8 @@ def write_call(d=None, **kw):
 def gather_call(d=None, **kw):
     d = desc() if d is None else d
     return pa.lib.pa_gather_cache_fp4(
-        kw.get("key", P), kw.get("value", P), kw.get("dtype", pa.PA_BF16), kw.get("cache", P),
+        kw.get("key", far(2)), kw.get("value", far(3)), kw.get("dtype", pa.PA_BF16),
+        kw.get("cache", far(1)),
         ctypes.byref(d), kw.get("slots", P), kw.get("n", 4), kw.get("key_scale", 1.0),
         kw.get("value_scale", 1.0), None)
 
@@ -158,8 +164,8 @@ def gather_call(d=None, **kw):
 def decode_call(d=None, **kw):
     d = desc() if d is None else d
     return pa.lib.pa_decode_fp4(
-        kw.get("out", P), kw.get("query", P), kw.get("dtype", pa.PA_BF16), kw.get("qs", 14 * 64),
-        kw.get("cache", P), ctypes.byref(d), kw.get("key_scale", 1.0), kw.get("value_scale", 1.0),
+        kw.get("out", far(2)), kw.get("query", far(3)), kw.get("dtype", pa.PA_BF16),
+        kw.get("qs", 14 * 64), kw.get("cache", far(1)), ctypes.byref(d), kw.get("key_scale", 1.0), kw.get("value_scale", 1.0),
         P, kw.get("mb", 4), P, kw.get("s", 2), kw.get("heads", 14), kw.get("scale", 0.125),
         kw.get("ws", P), kw.get("ws_bytes", 1 << 30), None)
 
@@ -234,9 +240,10 @@ def test_16_bit_calls_refuse_a_4_bit_pool():
 def tables_call(**kw):
     g = kw.get
     return pa.lib.pa_extend_tables(
-        g("tables", P), g("mb", 4), g("lens", P), g("new", P), g("n", 2), g("bs", 16), g("nb", 9),
-        g("ring", P), g("cap", 5), g("state", P), g("lens_out", P), g("state_out", P),
-        g("slots", P), g("pos", P), g("starts", P), g("most", 8), None)
+        g("tables", far(1)), g("mb", 4), g("lens", far(2)), g("new", far(3)), g("n", 2),
+        g("bs", 16), g("nb", 9), g("ring", far(4)), g("cap", 5), g("state", far(5)),
+        g("lens_out", far(6)), g("state_out", far(7)), g("slots", far(8)), g("pos", far(9)),
+        g("starts", far(10)), g("most", 8), None)
 
 
 def test_table_refusals():
@@ -249,6 +256,42 @@ def test_table_refusals():
            dict(ring=None, state=None, state_out=None)]  # a capacity without a ring
     for kw in bad:
         assert tables_call(**kw) == pa.PA_ERR_INVALID_ARG, kw
+
+
+def test_overlapping_buffers_are_refused():
+    # two requests: 8 bytes of lengths, counts and state, 12 of starts, 20 of the
+    # ring, 32 of the tables and of positions, 64 of slots
+    sizes = dict(tables=32, lens=8, new=8, ring=20, state=8, lens_out=8, state_out=8, slots=64,
+                 pos=32, starts=12)
+    where = dict(tables=1, lens=2, new=3, ring=4, state=5, lens_out=6, state_out=7, slots=8, pos=9,
+                 starts=10)
+    written = ("tables", "lens_out", "state_out", "slots", "pos", "starts")
+    for a in written:
+        for b in sizes:
+            if b == a:
+                continue
+            step = 8 if a == "slots" else 4
+            at = where[b] << 24
+            # a's last element on b's first, and a's first on b's last
+            first = at - sizes[a] + step
+            last = at + (sizes[b] - 4) // step * step
+            for x in (first, last):
+                assert tables_call(**{a: ctypes.c_void_p(x)}) == pa.PA_ERR_INVALID_ARG, (a, b)
+    assert tables_call(lens_out=far(3)) == pa.PA_ERR_INVALID_ARG   # in place of the counts
+    assert tables_call(state_out=far(2)) == pa.PA_ERR_INVALID_ARG
+    # four rows of 256 bytes; a pool of 16 blocks
+    row, pool = 4 * 256, 16 * 2 * 2 * 9 * 64
+    for x in (16, row - 16):
+        assert gather_call(key=ctypes.c_void_p((3 << 24) + x)) == pa.PA_ERR_INVALID_ARG
+        assert gather_call(key=ctypes.c_void_p((3 << 24) - x)) == pa.PA_ERR_INVALID_ARG
+    for name in ("key", "value"):
+        assert gather_call(**{name: ctypes.c_void_p((1 << 24) - row + 16)}) == pa.PA_ERR_INVALID_ARG
+        assert gather_call(**{name: ctypes.c_void_p((1 << 24) + pool - 16)}) == pa.PA_ERR_INVALID_ARG
+    # two rows of 14 heads, and rows 2000 elements apart
+    assert decode_call(out=far(3)) == pa.PA_ERR_INVALID_ARG
+    assert decode_call(out=ctypes.c_void_p((3 << 24) + 2 * 2 * 896 - 16)) == pa.PA_ERR_INVALID_ARG
+    assert decode_call(out=ctypes.c_void_p((3 << 24) - 2 * 2 * 896 + 16)) == pa.PA_ERR_INVALID_ARG
+    assert decode_call(qs=2000, out=ctypes.c_void_p((3 << 24) + 2 * 2896 - 16)) == pa.PA_ERR_INVALID_ARG
 
 
 def test_python_refusals():

@@ -2,6 +2,10 @@
 read-back (exact), block copies (exact), decode attention (within a bound
 derived from the roundings), the device-side tables (exact), and the three as
 a decode step, captured and replayed."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -368,6 +372,44 @@ def test_decode_many_sequences():
     assert_decode(r(), r.batch)
 
 
+def test_decode_most_sequences():
+    lens = [(i // 17) % 11 if i % 17 == 0 or i == 65534 else 0 for i in range(65535)]
+    r = Run(Batch(lens, 2, 2, 64, 8, seed=24))
+    assert_decode(r(), r.batch)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_decode_sequences_that_share_blocks_and_repeated_calls(dtype):
+    """Rows of one table several times over, and calls that agree bit for bit
+    however the parts of a sequence arrive."""
+    b = Batch([5000, 77], 12, 2, 128, 16, dtype, seed=25)
+    b.tables, b.lens = b.tables[[0, 1, 0, 0, 1]], b.lens[[0, 1, 0, 0, 1]]
+    b.lens[3] = 4000
+    b.query = rounded(np.random.default_rng(26).standard_normal((5, 12, 128)), dtype)
+    r = Run(b)
+    first = r().clone()
+    assert_decode(first, b)
+    for _ in range(20):
+        assert torch.equal(r(), first)
+
+
+def test_decode_fp32_sums_are_rounded_not_cut_off():
+    """512 sequences of 30000 tokens, so that a warp's share of one is over 10000
+    tokens, and values of one sign.  Additions to a running sum that round to
+    nearest are off by 2^-24 / sqrt(3) of it at most, in standard deviation, and
+    either way: n / 8 = 3750 of them (the sum of the weights has the most) by
+    2.1e-6, and the bound is ten of those.  Sums that are cut off lose 2^-24 to
+    2^-25 of it on average each time instead, always the same way: 5e-5 to 1e-4
+    for the n / 16 products of a value."""
+    b = Batch([30000], 8, 1, 128, 16, "fp32", seed=27)
+    fp4.write(b.cache, host(b.key), np.abs(host(b.value)), b.slots)
+    ref = b.reference()[0][0]
+    b.tables, b.lens = np.repeat(b.tables, 512, 0), np.repeat(b.lens, 512)
+    b.query = b.query.expand(512, 8, 128).contiguous()
+    got = host(Run(b)())
+    assert np.max(np.abs(got - ref) / np.abs(ref)) <= 2.1e-5
+
+
 def test_two_graphs_share_a_workspace_and_lengths_grow():
     a = Run(Batch([70, 1, 300], 8, 2, 128, 16, seed=17))
     b = Run(Batch([9, 2000], 4, 1, 128, 16, seed=18), workspace=None)
@@ -522,6 +564,30 @@ def test_tables_many_requests_and_tokens():
     Tables([3, 9], [70_000, 1], 16, most=90_000).check()
 
 
+def test_tables_most_tokens():
+    n, block = (1 << 26) - 1, 256
+    blocks = (1 << 18) + 3
+    ring = torch.randperm(blocks, device="cuda").int()
+    tables = torch.full((2, 1 << 18), -7, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    new = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    state = torch.tensor([1000, blocks], dtype=torch.int32, device="cuda")
+    slots = torch.empty(n, dtype=torch.int64, device="cuda")
+    pos = torch.empty(n, dtype=torch.int32, device="cuda")
+    for in_place in (False, True):
+        lo, so = (lens, state) if in_place else (torch.empty_like(lens), torch.empty_like(state))
+        slots.fill_(99), pos.fill_(99)
+        pa.pa_extend_tables(tables, lens, new, block, blocks, slots, pos, seq_lens_out=lo,
+                            free_blocks=ring, free_state=state, free_state_out=so)
+        at = torch.arange(n, device="cuda")
+        assert torch.equal(pos, at.int())
+        ids = torch.roll(ring, -1000)[:1 << 18]
+        assert torch.equal(tables[1], ids) and (tables[0] == -7).all()
+        assert torch.equal(slots, ids.long()[at >> 8] * 256 + (at & 255))
+        assert lo.tolist() == [0, n] and so.tolist() == [1000 - 3, 3]
+        assert pa.pa_get_device_error() == 0
+
+
 def test_tables_refuse_whole_steps():
     for kw in (dict(lens=[3, 5], new=[1, -1]), dict(lens=[3, -5], new=[1, 1]),
                dict(lens=[3, 30], new=[14, 3], width=2),
@@ -630,3 +696,34 @@ def test_captured_step_serves_growing_sequences(dtype, heads, hkv, head, block):
         assert np.array_equal(host(lens), b.lens)
         assert_decode(out, b, "step %d" % i)
     assert host(state)[1] == pool.num_free() and pa.pa_get_device_error() == 0
+
+
+FIRST_CALLS = """
+import torch
+import paged_kv_cache_78_gb300 as pa
+t = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+cache = pa.alloc_fp4_cache(6, 8, 1, 64)
+kv = torch.full((2, 1, 64), 6.0, device="cuda")
+out, back = torch.empty((2, 1, 64), device="cuda"), torch.empty((2, 2, 1, 64), device="cuda")
+tables, lens, new, state = t(1, 2, 3, 4).view(2, 2), t(0, 7), t(1, 1), t(0, 2)
+slots = torch.empty(2, dtype=torch.int64, device="cuda")
+ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(cache, 1), "cuda")
+ring = t(5, 0)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pa.pa_extend_tables(tables, lens, new, 8, 6, slots, free_blocks=ring, free_state=state)
+    pa.pa_reshape_and_cache_fp4(cache, kv, kv, slots)
+    pa.pa_gather_cache_fp4(back[0], back[1], cache, slots)
+    pa.pa_decode_fp4(out, kv, cache, tables, lens, 1.0, ws)
+g.replay()
+assert slots.tolist() == [40, 31] and (back == 6).all() and state.tolist() == [1, 1]
+assert (out - 6).abs().max() < 1e-5
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True,
+                       timeout=280)
+    assert r.returncode == 0 and r.stdout.split()[-1] == "captured", r.stderr
