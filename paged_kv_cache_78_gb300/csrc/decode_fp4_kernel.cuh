@@ -82,21 +82,6 @@ __device__ __forceinline__ uint2 lds_u64(uint32_t a) {
   return v;
 }
 
-// N floats of shared memory or of what other CTAs wrote, never from the L1 cache.
-template <int N>
-__device__ __forceinline__ void ld_past_l1(const float* p, float* v) {
-  if constexpr (N == 2) {
-    asm volatile("ld.volatile.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p) : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.volatile.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
-                   : "l"(p + i)
-                   : "memory");
-  }
-}
-
 // c += a . b: a 16 x 16, b 16 x 8, fp16 with fp32 sums.
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, const uint32_t* b) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -346,23 +331,27 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   // Where a CTA's share is at most four stages per warp, latency is what counts
   // and a merge over CTAs (3 to 4 us) costs more than four stages more per warp:
   // pairs of up to that many stages stay whole, with the CTA of their first unit.
-  if (share <= 4 * W) {
-    auto whole = [&](int unit) {
-      if (unit <= 0 || unit >= total) return unit;
-      const Fp4Place pl = locate(unit);
-      const int first = pl.at - pl.k - kFp4PairCost;  // the pair's first unit
-      return unit > first && pl.n <= 4 * W ? first + kFp4PairCost + pl.n : unit;
-    };
-    cta0 = whole(cta0);
-    cta1 = whole(cta1);
-  }
-
+  // The CTA's two ends, then the warp's first stage: a loop, as one-time code is
+  // paid by its length.
   bool ok = true;
-  const int share_w = (cta1 - cta0 + W - 1) / W;
-  const int my0 = cta0 + share_w * warp;
-  const int my1 = min(my0 + share_w, cta1);
+  int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
-  if (my0 < my1) pp = locate(my0);
+#pragma unroll 1
+  for (int i = share <= 4 * W ? 0 : 2; i < 3; ++i) {
+    int unit = i == 0 ? cta0 : cta1;
+    if (i == 2) {
+      share_w = (cta1 - cta0 + W - 1) / W;
+      my0 = unit = cta0 + share_w * warp;
+      my1 = min(my0 + share_w, cta1);
+      if (my0 >= my1) break;
+    }
+    if (i < 2 && (unit <= 0 || unit >= total)) continue;
+    pp = locate(unit);
+    if (i == 2) break;
+    const int first = pp.at - pp.k - kFp4PairCost;  // the pair's first unit
+    if (unit > first && pp.n <= 4 * W) unit = first + kFp4PairCost + pp.n;
+    (i == 0 ? cta0 : cta1) = unit;
+  }
   if (my0 < my1 && pp.at < my1) {
     const int per_block = min(kFp4Stage / kFp4Tile, 1 << (l2bs - 3));  // tiles of a copy
     const uint32_t lane_dst = (uint32_t)(lane * per_block) * C::kTileBytes;
@@ -935,7 +924,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
         };
         float mi = -INFINITY, li = 0.f, acc[kVec];
         if (lane < n) {
-          const volatile float* src = part(lane) + rows * D + unit;
+          const float* src = part(lane) + rows * D + unit;
           mi = src[0];
           li = src[per_run];
         }
@@ -950,8 +939,15 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
           const float wi = __shfl_sync(0xffffffffu, w, i);
-          float v[kVec];
-          ld_past_l1<kVec>(part(i) + col, v);
+          alignas(16) float v[kVec];
+          const float* src = part(i) + col;
+          if constexpr (kVec == 2) {
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kVec; e += 4)
+              *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(src + e);
+          }
 #pragma unroll
           for (int e = 0; e < kVec; ++e) acc[e] = fmaf(v[e], wi, acc[e]);
         }
@@ -969,7 +965,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           }
           break;
         }
-        // Hand the part on; whoever is last takes the next level.
+        // Hand the part on; whoever is last takes the next level.  Lane 0's atomic
+        // releases what the warp's lanes wrote before and acquires, for all of
+        // them, what the others' released.
         const int at = level == 0 ? (int)blockIdx.x : run.cta0 + group * kFp4Gather;
         float* to =
             p.cta_partials + ((size_t)at * 4 + 2 * level + (at == run.cta0)) * part_floats;
