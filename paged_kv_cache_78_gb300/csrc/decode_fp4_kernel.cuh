@@ -328,16 +328,19 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     return pl;
   };
 
-  // Where a CTA's share is at most four stages per warp, latency is what counts
-  // and a merge over CTAs (3 to 4 us) costs more than four stages more per warp:
-  // pairs of up to that many stages stay whole, with the CTA of their first unit.
+  // Where a CTA's share is at most a stage per warp, latency is what counts and a
+  // merge over CTAs costs more than the stages that it spares: pairs of up to that
+  // many stages stay whole, with the CTA of their first unit.  (64 sequences of up to
+  // 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 -> 8.3; with four stages per
+  // warp instead of one, 64 sequences of up to 2048 tokens took 16.5, not 14.5 us.
+  // One sequence of 8192 tokens, which gains nothing, looks in vain for 1.6 us.)
   // The CTA's two ends, then the warp's first stage: a loop, as one-time code is
   // paid by its length.
   bool ok = true;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
 #pragma unroll 1
-  for (int i = share <= 4 * W ? 0 : 2; i < 3; ++i) {
+  for (int i = share <= W ? 0 : 2; i < 3; ++i) {
     int unit = i == 0 ? cta0 : cta1;
     if (i == 2) {
       share_w = (cta1 - cta0 + W - 1) / W;
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     pp = locate(unit);
     if (i == 2) break;
     const int first = pp.at - pp.k - kFp4PairCost;  // the pair's first unit
-    if (unit > first && pp.n <= 4 * W) unit = first + kFp4PairCost + pp.n;
+    if (unit > first && pp.n <= W) unit = first + kFp4PairCost + pp.n;
     (i == 0 ? cta0 : cta1) = unit;
   }
   if (my0 < my1 && pp.at < my1) {
@@ -928,28 +931,40 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           mi = src[0];
           li = src[per_run];
         }
-        const float top = warp_max_redux(mi);
-        const float w = mi == top ? 1.f : fast_exp2(mi - top);
-        float sum = lane < n ? li * w : 0.f;
-#pragma unroll
-        for (int o = 1; o < kFp4Gather; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sum = __shfl_sync(0xffffffffu, sum, 0);
+        // Eight parts at a time (past the last, that one again, with no weight); the
+        // first ones are on their way with the maxima and sums.
+        constexpr int kBatch = 8;
+        float top = 0.f, w = 0.f, sum = 0.f;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);
-          alignas(16) float v[kVec];
-          const float* src = part(i) + col;
-          if constexpr (kVec == 2) {
-            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-          } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+          alignas(16) float v[kBatch][kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; e += 4)
-              *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(src + e);
+          for (int i = 0; i < kBatch; ++i) {
+            const float* src = part(min(i0 + i, n - 1)) + col;
+            if constexpr (kVec == 2) {
+              *reinterpret_cast<float2*>(v[i]) = *reinterpret_cast<const float2*>(src);
+            } else {
+#pragma unroll
+              for (int e = 0; e < kVec; e += 4)
+                *reinterpret_cast<float4*>(v[i] + e) = *reinterpret_cast<const float4*>(src + e);
+            }
+          }
+          if (i0 == 0) {
+            top = warp_max_redux(mi);
+            w = lane >= n ? 0.f : mi == top ? 1.f : fast_exp2(mi - top);
+            sum = lane < n ? li * w : 0.f;
+#pragma unroll
+            for (int o = 1; o < kFp4Gather; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
           }
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(v[e], wi, acc[e]);
+          for (int i = 0; i < kBatch; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) acc[e] = fmaf(v[i][e], wi, acc[e]);
+          }
         }
         const int group = ((int)blockIdx.x - run.cta0) / kFp4Gather;
         const int groups = (run.ctas + kFp4Gather - 1) / kFp4Gather;
