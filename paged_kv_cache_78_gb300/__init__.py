@@ -15,6 +15,7 @@ the block copies.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -199,17 +200,29 @@ def cache_desc(cache: torch.Tensor) -> CacheDesc:
     return CacheDesc(nb, bs, hkv, d, _dtype_code(cache))
 
 
-def fp4_cache_desc(cache: torch.Tensor) -> CacheDesc:
-    """Descriptor of a 4-bit pool [num_blocks, num_kv_heads, block_size / 8, 9 * head_size]."""
-    if cache.dtype != torch.uint8:
-        raise TypeError("a 4-bit cache must be uint8, got %s" % cache.dtype)
-    if cache.dim() != 4 or cache.shape[3] % 9:
+@functools.lru_cache(maxsize=64)
+def _fp4_geometry(shape):
+    """(descriptor, a reference to it, KV heads, head size) of a 4-bit pool's shape."""
+    if len(shape) != 4 or shape[3] % 9:
         raise ValueError("a 4-bit cache must be [num_blocks, num_kv_heads, block_size / 8, "
                          "9 * head_size]")
+    nb, hkv, tiles, size = shape
+    desc = CacheDesc(nb, 8 * tiles, hkv, size // 9, PA_FP4)
+    return desc, ctypes.byref(desc), hkv, size // 9
+
+
+def _fp4_pool(cache: torch.Tensor):
+    if cache.dtype is not torch.uint8:
+        raise TypeError("a 4-bit cache must be uint8, got %s" % cache.dtype)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
-    nb, hkv, tiles, size = cache.shape
-    return CacheDesc(nb, 8 * tiles, hkv, size // 9, PA_FP4)
+    return _fp4_geometry(cache.shape)
+
+
+def fp4_cache_desc(cache: torch.Tensor) -> CacheDesc:
+    """Descriptor of a 4-bit pool [num_blocks, num_kv_heads, block_size / 8, 9 * head_size]."""
+    d = _fp4_pool(cache)[0]
+    return CacheDesc(d.num_blocks, d.block_size, d.num_kv_heads, d.head_size, d.dtype)
 
 
 def alloc_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
@@ -237,8 +250,7 @@ def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        # the current stream's handle without a Stream object (2.9 -> 0.2 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _cuda_raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -506,12 +518,18 @@ def pa_decode_shared(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor
 # 4-bit pool and device-side tables
 # ---------------------------------------------------------------------------
 
+# The current device and the raw handle of a device's current stream, without the
+# objects around them (2.9 -> 0.2 us a call).
+_cuda_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_cuda_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current_device(t: torch.Tensor, name: str) -> int:
     """The device of t, which has to be the current one (launches go there)."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if dev != torch._C._cuda_getDevice():
+    if dev != _cuda_get_device():
         raise ValueError("%s is on device %d, which is not the current one" % (name, dev))
     return dev
 
@@ -542,7 +560,7 @@ def _rows(t: torch.Tensor, name: str, heads: int, head_size: int, dev: int):
 
 
 def _on(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _cuda_raw_stream(dev) if stream is None else _stream(stream)
 
 
 def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -552,7 +570,7 @@ def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torc
     head_size] (bf16 or fp32, rows may lie apart) are rounded to 4-bit codes
     with a scale per 16 elements; key_scale / value_scale are the pool's
     tensor scales (powers of two)."""
-    desc = fp4_cache_desc(cache)
+    _, desc, heads, size = _fp4_pool(cache)
     if key.shape != value.shape or key.dim() != 3:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
     if key.dtype is not value.dtype:
@@ -561,9 +579,9 @@ def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torc
     if slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be [num_tokens]")
     dev = _current_device(cache, "cache")
-    kp, ks = _rows(key, "key", desc.num_kv_heads, desc.head_size, dev)
-    vp, vs = _rows(value, "value", desc.num_kv_heads, desc.head_size, dev)
-    _check(lib.pa_reshape_and_cache_fp4(cache.data_ptr(), ctypes.byref(desc), kp, vp,
+    kp, ks = _rows(key, "key", heads, size, dev)
+    vp, vs = _rows(value, "value", heads, size, dev)
+    _check(lib.pa_reshape_and_cache_fp4(cache.data_ptr(), desc, kp, vp,
                                         _dtype_code(key), ks, vs,
                                         _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
                                         key_scale, value_scale, _on(stream, dev)),
@@ -576,18 +594,18 @@ def pa_gather_cache_fp4(key: torch.Tensor, value: torch.Tensor, cache: torch.Ten
     """Read tokens back from a 4-bit pool: key/value [n, num_kv_heads,
     head_size] (bf16 or fp32, contiguous) receive what the slots hold; rows of
     negative slots stay as they were."""
-    desc = fp4_cache_desc(cache)
+    _, desc, heads, size = _fp4_pool(cache)
     if key.dim() != 3 or key.shape != value.shape:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
     n, h, d = key.shape
-    if h != desc.num_kv_heads or d != desc.head_size:
+    if h != heads or d != size:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
     if slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be [num_tokens]")
     dev = _current_device(cache, "cache")
     _check(lib.pa_gather_cache_fp4(_arg(key, "key", key.dtype, dev),
                                    _arg(value, "value", key.dtype, dev), _dtype_code(key),
-                                   cache.data_ptr(), ctypes.byref(desc),
+                                   cache.data_ptr(), desc,
                                    _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
                                    key_scale, value_scale, _on(stream, dev)),
            "pa_gather_cache_fp4")
@@ -610,20 +628,21 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
     """pa_decode over a 4-bit pool; query (rows may lie apart) and out are
     bf16 or fp32.  The launch depends on the shapes alone, so that a captured
     call serves sequences as they grow."""
-    desc = fp4_cache_desc(cache)
+    _, desc, _, size = _fp4_pool(cache)
     s, hq, d = query.shape
-    if out.shape != query.shape or d != desc.head_size:
+    if out.shape != query.shape or d != size:
         raise ValueError("query/out must be [num_seqs, num_heads, head_size]")
     if query.dtype is not out.dtype:
         raise TypeError("query and out must have the same dtype")
-    if block_tables.dim() != 2 or block_tables.shape[0] != s or seq_lens.shape != (s,):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != s or seq_lens.shape != (s,):
         raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
     dev = _current_device(cache, "cache")
     qp, qs = _rows(query, "query", hq, d, dev)
     _check(lib.pa_decode_fp4(_arg(out, "out", query.dtype, dev), qp, _dtype_code(query), qs,
-                             cache.data_ptr(), ctypes.byref(desc), key_scale, value_scale,
+                             cache.data_ptr(), desc, key_scale, value_scale,
                              _arg(block_tables, "block_tables", torch.int32, dev),
-                             block_tables.shape[1], _arg(seq_lens, "seq_lens", torch.int32, dev), s,
+                             tables[1], _arg(seq_lens, "seq_lens", torch.int32, dev), s,
                              hq, scale, _arg(workspace, "workspace", workspace.dtype, dev),
                              workspace.nbytes, _on(stream, dev)), "pa_decode_fp4")
 
@@ -641,13 +660,14 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
     [front, blocks left]; without them the tables hold every block already),
     slots and positions of the new tokens, -1 behind them, lengths and ring
     state advanced (in place unless *_out are given)."""
-    n = seq_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != n or new_tokens.shape != (n,):
+    n, = seq_lens.shape
+    tables, most = block_tables.shape, slot_mapping.shape
+    if len(tables) != 2 or tables[0] != n or new_tokens.shape != (n,):
         raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens and new_tokens "
                          "[num_seqs]")
-    if slot_mapping.dim() != 1:
+    if len(most) != 1:
         raise ValueError("slot_mapping must be [max_tokens]")
-    if positions is not None and positions.shape != slot_mapping.shape:
+    if positions is not None and positions.shape != most:
         raise ValueError("positions must be [max_tokens]")
     if token_starts is not None and token_starts.shape != (n + 1,):
         raise ValueError("token_starts must be [num_seqs + 1]")
@@ -655,28 +675,31 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
         raise ValueError("free_blocks and free_state go together")
     if free_state_out is not None and free_state is None:
         raise ValueError("free_state_out needs free_state")
-    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
-    free_state_out = free_state if free_state_out is None else free_state_out
-    if seq_lens_out.shape != (n,):
-        raise ValueError("seq_lens_out must be [num_seqs]")
-    if free_state is not None and (free_state.shape != (2,) or free_state_out.shape != (2,) or
-                                   free_blocks.dim() != 1):
-        raise ValueError("free_blocks must be [capacity], free_state [2]")
     dev = _current_device(block_tables, "block_tables")
     i32 = torch.int32
+    lens = lens_out = _arg(seq_lens, "seq_lens", i32, dev)
+    if seq_lens_out is not None:
+        if seq_lens_out.shape != (n,):
+            raise ValueError("seq_lens_out must be [num_seqs]")
+        lens_out = _arg(seq_lens_out, "seq_lens_out", i32, dev)
+    ring = state = state_out = None
+    capacity = 0
+    if free_state is not None:
+        if free_state.shape != (2,) or free_blocks.dim() != 1:
+            raise ValueError("free_blocks must be [capacity], free_state [2]")
+        ring, capacity = _arg(free_blocks, "free_blocks", i32, dev), free_blocks.shape[0]
+        state = state_out = _arg(free_state, "free_state", i32, dev)
+        if free_state_out is not None:
+            if free_state_out.shape != (2,):
+                raise ValueError("free_state_out must be [2]")
+            state_out = _arg(free_state_out, "free_state_out", i32, dev)
     _check(lib.pa_extend_tables(
-        _arg(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-        _arg(seq_lens, "seq_lens", i32, dev), _arg(new_tokens, "new_tokens", i32, dev), n,
-        block_size, num_blocks,
-        None if free_blocks is None else _arg(free_blocks, "free_blocks", i32, dev),
-        0 if free_blocks is None else free_blocks.shape[0],
-        None if free_state is None else _arg(free_state, "free_state", i32, dev),
-        _arg(seq_lens_out, "seq_lens_out", i32, dev),
-        None if free_state is None else _arg(free_state_out, "free_state_out", i32, dev),
-        _arg(slot_mapping, "slot_mapping", torch.int64, dev),
+        _arg(block_tables, "block_tables", i32, dev), tables[1], lens,
+        _arg(new_tokens, "new_tokens", i32, dev), n, block_size, num_blocks, ring, capacity, state,
+        lens_out, state_out, _arg(slot_mapping, "slot_mapping", torch.int64, dev),
         None if positions is None else _arg(positions, "positions", i32, dev),
         None if token_starts is None else _arg(token_starts, "token_starts", i32, dev),
-        slot_mapping.shape[0], _on(stream, dev)), "pa_extend_tables")
+        most[0], _on(stream, dev)), "pa_extend_tables")
 
 
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20
