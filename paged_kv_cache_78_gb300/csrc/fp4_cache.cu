@@ -5,14 +5,16 @@
 // codes and one scale byte on the other, and are bound by memory; a thread takes
 // key and value so that addresses are worked out once for both (one of them per
 // thread spent 62% of the issue slots, most of it on addresses).  A CTA takes
-// eight consecutive tokens and some of their heads, lanes a group's tokens, then
-// the next group.  Tokens that follow one another usually lie in one tile, so
-// that a warp's codes and scales are whole sectors of 32 bytes, and the wide
-// side is anyway.
+// consecutive (eight tokens, head) units, the heads of a token next to each other,
+// lanes a group's tokens, then the next group.  Tokens that follow one another
+// usually lie in one tile, so that a warp's codes and scales are whole sectors of 32
+// bytes, and the wide side is anyway.  (Units of one token block only would leave
+// threads idle where heads are few: one head of 64, 150 MB, 59 us instead of 24.)
 //
 // Measured on 8 heads of 128, bf16, in a row of graph replays: the write of 65536
 // tokens 51.7 us (344 MB, 6.7 TB/s, 98% of the copy rate, part of it L2's), the
-// read-back 55.0 us (6.3 TB/s, 92%); of 16381 tokens 15.1 and 16.3 us (5.7 and 5.3
+// read-back 55.0 us (6.3 TB/s, 92%; fp32 75 to 89%, the lower where a token's row is
+// a power of two); of 16381 tokens 15.1 and 16.3 us (5.7 and 5.3
 // TB/s), where the L1 cache is at 72% (write) and 84% (read-back, its stores) of its
 // rate.  777 tokens of 4 heads of 64 take 5.2 us and 64 tokens of 2 heads 3.1 us a
 // call, which is the launch and two dependent reads.
@@ -30,13 +32,13 @@ template <int D>
 __device__ __forceinline__ bool fp4_unit(int num_tokens, int num_kv_heads, int* t, int* h, int* j) {
   constexpr int kUnits = kFp4Tile * D / kFp4Group;  // of one head of eight tokens
   constexpr int kHeads = kFp4Threads / kUnits;
-  const unsigned chunks = ((unsigned)num_kv_heads + kHeads - 1) / kHeads;
-  const unsigned block = blockIdx.x / chunks;
+  const unsigned head = blockIdx.x * kHeads + threadIdx.x / kUnits;  // of all tokens' heads
+  const unsigned block = head / (unsigned)num_kv_heads;
   const int i = threadIdx.x % kUnits;
-  *h = (int)(blockIdx.x - block * chunks) * kHeads + (int)threadIdx.x / kUnits;
-  *t = (int)block * kFp4Tile + i % kFp4Tile;
+  *h = (int)(head - block * num_kv_heads);
+  *t = (int)min((unsigned long long)block * kFp4Tile + i % kFp4Tile, 0x7fffffffull);
   *j = i / kFp4Tile;
-  return *h < num_kv_heads && *t < num_tokens;
+  return *t < num_tokens;
 }
 
 // Where group j of a tile's row has its codes and its scale.
@@ -80,10 +82,16 @@ __device__ __forceinline__ uint32_t quantise16(const uint4* w, float tensor_scal
   const uint32_t code = fp4_scale_code(largest(w, static_cast<const T*>(nullptr)) * inv_tensor);
   const float s = e4m3_to_float(code);
   const float r = s > 0.f ? fast_rcp(s) * inv_tensor : 0.f;
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    if constexpr (sizeof(T) == 2) q[e] = fp4_quotient_bf16(x[e], r);
-    else q[e] = fp4_quotient_f32(x[e], s * tensor_scale, r);
+    for (int e = 0; e < 16; ++e) q[e] = fp4_quotient_bf16(x[e], r);
+  } else {
+    bool sure = true;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q[e] = fp4_quotient_f32(x[e], r, &sure);
+    if (!sure)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) q[e] = fp4_exact_quotient_f32(x[e], s * tensor_scale, r);
   }
   *codes = make_uint2(e2m1_pack8(q), e2m1_pack8(q + 8));
   return code;
@@ -211,9 +219,9 @@ __global__ void __launch_bounds__(kFp4Threads)
 }
 
 unsigned fp4_grid(const Fp4Pool& pool, int num_tokens) {
-  const int heads = kFp4Threads / (kFp4Tile * pool.head_size / kFp4Group);
-  const unsigned chunks = ((unsigned)pool.num_kv_heads + heads - 1) / heads;
-  return (unsigned)((num_tokens + kFp4Tile - 1) / kFp4Tile) * chunks;
+  const unsigned heads = kFp4Threads / (kFp4Tile * pool.head_size / kFp4Group);
+  const unsigned all = ((unsigned)num_tokens + kFp4Tile - 1) / kFp4Tile * pool.num_kv_heads;
+  return (all + heads - 1) / heads;
 }
 
 template <typename T, int D>

@@ -37,7 +37,8 @@ def same(a, b):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("head,hkv,block,n", [(64, 1, 8, 1), (64, 3, 16, 77), (128, 8, 16, 130),
-                                              (128, 2, 256, 300), (256, 5, 32, 41)])
+                                              (128, 2, 256, 300), (256, 5, 32, 41), (64, 1, 8, 1001),
+                                              (64, 40, 16, 65), (128, 1, 16, 3), (256, 1, 8, 9)])
 def test_write_and_gather(dtype, head, hkv, block, n):
     rng = np.random.default_rng(head + n)
     nb = -(-n // block) + 3
@@ -88,6 +89,25 @@ def test_write_rounds_on_the_exact_quotients(dtype):
     gk, gv = fp4.read(cache.cpu().numpy(), np.arange(len(rows)))
     assert same(gk, fp4.dequantise(*fp4.quantise(host(key))))
     assert same(gv, fp4.dequantise(*fp4.quantise(host(value))))
+
+
+def test_write_rounds_fp32_numbers_near_borders():
+    """Numbers beside the borders of e2m1, nearer and nearer, in groups without any
+    whose quotient is a multiple of 1/4; then with one such in every other group."""
+    border = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    rows = []
+    for k in range(9, 24):
+        for m in range(8, 16):
+            s, d = m / 8 * 2.0 ** (m % 3 - 1), 2.0 ** -k
+            rows.append(np.concatenate([[6.01 * s], border * (1 + d) * s, -border * (1 - d) * s, [0.3 * s]]))
+            rows.append(np.concatenate([[6.01 * s], border * (1 - d) * s, -border * (1 + d) * s, [0.5 * s]]))
+    x = rounded(np.array(rows).reshape(-1, 1, 64), "fp32")
+    n = x.shape[0]
+    cache = torch.zeros((-(-n // 8), 1, 1, 9 * 64), dtype=torch.uint8, device="cuda")
+    pa.pa_reshape_and_cache_fp4(cache, dev(x), dev(-x), torch.arange(n, device="cuda"))
+    gk, gv = fp4.read(cache.cpu().numpy(), np.arange(n))
+    want = fp4.dequantise(*fp4.quantise(host(x)))
+    assert same(gk, want) and same(gv, -want)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
