@@ -584,7 +584,7 @@ def pa_reshape_and_cache_fp4(cache: torch.Tensor, key: torch.Tensor, value: torc
     _check(lib.pa_reshape_and_cache_fp4(cache.data_ptr(), desc, kp, vp,
                                         _dtype_code(key), ks, vs,
                                         _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
-                                        key_scale, value_scale, _on(stream, dev)),
+                                        float(key_scale), float(value_scale), _on(stream, dev)),
            "pa_reshape_and_cache_fp4")
 
 
@@ -607,7 +607,7 @@ def pa_gather_cache_fp4(key: torch.Tensor, value: torch.Tensor, cache: torch.Ten
                                    _arg(value, "value", key.dtype, dev), _dtype_code(key),
                                    cache.data_ptr(), desc,
                                    _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
-                                   key_scale, value_scale, _on(stream, dev)),
+                                   float(key_scale), float(value_scale), _on(stream, dev)),
            "pa_gather_cache_fp4")
 
 
@@ -616,7 +616,7 @@ def pa_decode_fp4_workspace_size(cache_or_desc, num_heads: int) -> int:
     desc = (cache_or_desc if isinstance(cache_or_desc, CacheDesc)
             else fp4_cache_desc(cache_or_desc))
     out = ctypes.c_size_t()
-    _check(lib.pa_decode_fp4_workspace_size(ctypes.byref(desc), num_heads, ctypes.byref(out)),
+    _check(lib.pa_decode_fp4_workspace_size(ctypes.byref(desc), int(num_heads), ctypes.byref(out)),
            "pa_decode_fp4_workspace_size")
     return out.value
 
@@ -640,10 +640,10 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
     dev = _current_device(cache, "cache")
     qp, qs = _rows(query, "query", hq, d, dev)
     _check(lib.pa_decode_fp4(_arg(out, "out", query.dtype, dev), qp, _dtype_code(query), qs,
-                             cache.data_ptr(), desc, key_scale, value_scale,
+                             cache.data_ptr(), desc, float(key_scale), float(value_scale),
                              _arg(block_tables, "block_tables", torch.int32, dev),
                              tables[1], _arg(seq_lens, "seq_lens", torch.int32, dev), s,
-                             hq, scale, _arg(workspace, "workspace", workspace.dtype, dev),
+                             hq, float(scale), _arg(workspace, "workspace", workspace.dtype, dev),
                              workspace.nbytes, _on(stream, dev)), "pa_decode_fp4")
 
 
@@ -695,8 +695,8 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
             state_out = _arg(free_state_out, "free_state_out", i32, dev)
     _check(lib.pa_extend_tables(
         _arg(block_tables, "block_tables", i32, dev), tables[1], lens,
-        _arg(new_tokens, "new_tokens", i32, dev), n, block_size, num_blocks, ring, capacity, state,
-        lens_out, state_out, _arg(slot_mapping, "slot_mapping", torch.int64, dev),
+        _arg(new_tokens, "new_tokens", i32, dev), n, int(block_size), int(num_blocks), ring, capacity,
+        state, lens_out, state_out, _arg(slot_mapping, "slot_mapping", torch.int64, dev),
         None if positions is None else _arg(positions, "positions", i32, dev),
         None if token_starts is None else _arg(token_starts, "token_starts", i32, dev),
         most[0], _on(stream, dev)), "pa_extend_tables")

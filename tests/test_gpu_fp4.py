@@ -608,6 +608,23 @@ def test_tables_most_tokens():
         assert pa.pa_get_device_error() == 0
 
 
+def test_calls_take_numpy_scalars():
+    b = Batch([20, 3], 4, 2, 64, 8, seed=28, key_scale=2.0, value_scale=0.5)
+    r = Run(b)
+    r.ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(r.cache, np.int64(4)), "cuda")
+    b.scale, b.key_scale, b.value_scale = np.float32(b.scale), np.float32(2), np.float32(0.5)
+    assert_decode(r(), b)
+    ko = torch.empty((1, 2, 64), device="cuda")
+    vo = torch.empty_like(ko)
+    one = torch.zeros(1, dtype=torch.int64, device="cuda")
+    pa.pa_reshape_and_cache_fp4(r.cache, ko.fill_(12), vo.fill_(3), one, np.float32(2), np.float32(0.5))
+    pa.pa_gather_cache_fp4(ko, vo, r.cache, one, np.float32(2), np.float32(0.5))
+    assert (ko == 12).all() and (vo == 3).all()
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_extend_tables(lens.view(1, 1).clone(), lens, lens + 1, np.int64(8), np.int64(5), one)
+    assert one.tolist() == [0] and lens.tolist() == [1]
+
+
 def test_tables_refuse_whole_steps():
     for kw in (dict(lens=[3, 5], new=[1, -1]), dict(lens=[3, -5], new=[1, 1]),
                dict(lens=[3, 30], new=[14, 3], width=2),
