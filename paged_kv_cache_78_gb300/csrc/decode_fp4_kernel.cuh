@@ -218,7 +218,7 @@ struct Fp4Config {
   static constexpr int kBars = kWarps * kWarpRing;
   static constexpr int kPieces = kBars + 8 * kWarps * kStages;
   static constexpr int kPre = (kPieces + kWarps * kFp4Pieces * (int)sizeof(Fp4Piece) + 15) / 16 * 16;
-  static constexpr int kRuns = (kPre + 4 * (kThreads + kWarps) + 15) / 16 * 16;
+  static constexpr int kRuns = (kPre + 4 * (kThreads + 2 * kWarps) + 15) / 16 * 16;
   static constexpr int kSmem = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
   static_assert(kStages >= 2 && kStages + 2 <= kFp4Pieces, "rings");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -266,9 +266,10 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     *heads = min(H, G - ht * H);
     return h * G + ht * H;
   };
-  // Units before each thread's sequences; the warps' sums.
+  // Units before each thread's sequences; the warps' sums and their sequences.
   int* warp_sums = reinterpret_cast<int*>(smem + C::kPre);
-  int* pre = warp_sums + W;
+  int* warp_seqs = warp_sums + W;
+  int* pre = warp_seqs + W;
   Fp4Run* runs = reinterpret_cast<Fp4Run*>(smem + C::kRuns);   // [warp][ended before, at its end]
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(bars + 8u * i, 1);
@@ -289,13 +290,14 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   // Sums stop at 2^27 units (600 GB of reads at 128 elements): lengths that
   // nobody meant, an error.
   const int chunk = (p.num_seqs + C::kThreads - 1) / C::kThreads;
-  int total;
+  int total, pairs;
   {
-    int mine = 0;
+    int mine = 0, seqs = 0;
     for (int s = tid * chunk; s < min((tid + 1) * chunk, p.num_seqs); ++s) {
       int len;
       const int n = stages_of(s, &len);
       if (n == 0 && len > 0 && blockIdx.x == 0) record_error(p.err, PA_DEVERR_SEQ_LEN);
+      seqs += n > 0;
       if (n > 0)
         mine = (int)min(mine + (long long)(n + kFp4PairCost) * per_seq, (long long)kFp4MaxWork);
     }
@@ -305,7 +307,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum = min(sum + v, kFp4MaxWork);
     }
-    if (lane == 31) warp_sums[warp] = sum;
+    seqs = __reduce_add_sync(0xffffffffu, seqs);
+    if (lane == 31) {
+      warp_sums[warp] = sum;
+      warp_seqs[warp] = seqs;
+    }
     __syncthreads();
     const unsigned other = lane < W ? (unsigned)warp_sums[lane] : 0u;
     const unsigned base = __reduce_add_sync(0xffffffffu, lane < warp ? other : 0u);
@@ -314,6 +320,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     if (all >= (unsigned)kFp4MaxWork && tid == 0 && blockIdx.x == 0)
       record_error(p.err, PA_DEVERR_SEQ_LEN);
     total = all >= (unsigned)kFp4MaxWork ? 0 : (int)all;
+    pairs = __reduce_add_sync(0xffffffffu, lane < W ? warp_seqs[lane] : 0) * per_seq;
     __syncthreads();
   }
   // Units of a CTA: an equal share, at least one per two warps (fewer parts to
@@ -348,19 +355,19 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     return pl;
   };
 
-  // Where a CTA's share is at most a stage per warp, latency is what counts and a
-  // merge over CTAs costs more than the stages that it spares: pairs of up to that
-  // many stages stay whole, with the CTA of their first unit.  (64 sequences of up to
-  // 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 -> 8.3; with four stages per
-  // warp instead of one, 64 sequences of up to 2048 tokens took 16.5, not 14.5 us.
-  // One sequence of 8192 tokens, which gains nothing, looks in vain for 1.6 us.)
+  // Where a CTA's share is at most a stage per warp, and so is the average pair,
+  // latency is what counts and a merge over CTAs costs more than the stages that it
+  // spares: pairs of up to that many stages stay whole, with the CTA of their first
+  // unit.  (64 sequences of up to 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 ->
+  // 8.3; with four stages per warp instead of one, 64 sequences of up to 2048 tokens
+  // took 16.5, not 14.5 us; one of 1024 tokens, all its pairs longer, 12.3, not 10.4.)
   // The CTA's two ends, then the warp's first stage: a loop, as one-time code is
   // paid by its length.
   bool ok = true;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
 #pragma unroll 1
-  for (int i = share <= W ? 0 : 2; i < 3; ++i) {
+  for (int i = share <= W && total / (W + kFp4PairCost) <= pairs ? 0 : 2; i < 3; ++i) {
     int unit = i == 0 ? cta0 : cta1;
     if (i == 2) {
       share_w = (cta1 - cta0 + W - 1) / W;
