@@ -8,7 +8,7 @@
 // each of which has to become fp16 before a product.  A conversion takes one
 // instruction per pair of codes and one multiplication per pair by the scales
 // (exact), on pipes that pass 16 lanes per clock and scheduler; with the matrix
-// instructions a stage of 32 tokens of 128 elements takes a warp about 400
+// instructions a step of 32 tokens of 128 elements takes a warp about 400
 // instructions and an SM 140 to 150 clocks (measured: 1.34 per instruction on such
 // a pipe and 4.6 per matrix instruction, per scheduler), 30 to 32 bytes per clock:
 // 1.3 times what the memory gives, so nothing more fits.  So the codes go
@@ -19,7 +19,7 @@
 // for this: a tile's key rows and value groups are the matrix instructions'
 // fragments.
 //
-// Every warp works for itself.  The stages of 32 tokens of all (sequence, KV
+// Every warp works for itself.  The stages of 32 or 64 tokens of all (sequence, KV
 // head) pairs, laid end to end, are cut into equal ranges, one per CTA, and
 // those into equal parts, one per warp; a warp streams its part through a ring
 // of its own (bulk copies that its lanes issue, one per block; no barrier with
@@ -30,15 +30,15 @@
 // Measured (graph replays in a row, data larger than L2, 6766 GB/s = 100%):
 //   8 x 32768 tokens, 32 heads on 8 of 128, bf16   59 us  302 MB  5.1 TB/s  75%
 //   the same with 64 heads on 8                    66 us                    68%
-//   the same with 64 heads on 8 of 64              47 us  151 MB            47%
+//   the same with 64 heads on 8 of 64              45 us  151 MB            50%
 //   8 x 32768 tokens, 64 heads on 8 of 128, fp32   90 us  302 MB            50%
 //   32 sequences of 1 .. 2048 tokens, 40 heads     43 us  181 MB            62%
 //   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  14.5 us
 //   four sequences of up to 100 tokens              8.3 us
 // Of the long batch reading alone takes 57 us and the arithmetic alone 55; the
 // launch, the lengths and the first copies take 5 to 6 us, and merges over CTAs 4,
-// and these are what is left of the short ones.  Heads of 64 pay a stage's fixed
-// part (exponents, copies, waits) for half the elements; fp32 doubles the matrix
+// and these are what is left of the short ones.  Heads of 64 pay a step's fixed
+// part (exponents, softmax) for half the elements; fp32 doubles the matrix
 // instructions.
 #pragma once
 
@@ -123,7 +123,7 @@ __device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, const
 // sum over n products about n * 2^-25 too small: over a warp's 12600 tokens 1.3e-4.
 // That is less than bf16's half step of 2^-8 by far (short chains would cost 1% of the
 // time at four heads of 128, 9% at eight), but not fp32's, where chains end with
-// their stage of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.
+// their step of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.
 template <bool kShort>
 struct Fp4Sum {
   float* c;
@@ -211,7 +211,9 @@ struct Fp4Config {
   static constexpr int kWarps = fp4_warps(D, H, kF32);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = fp4_tile_bytes(D);
-  static constexpr int kStageBytes = kFp4Stage / kFp4Tile * kTileBytes;
+  static constexpr int kStage = fp4_stage(D);
+  static constexpr int kStageBytes = kStage / kFp4Tile * kTileBytes;
+  static constexpr int kWholeStages = kWarps * kFp4Step / kStage;  // a step per warp
   static constexpr int kFit = kFp4RingBytes / kWarps / kStageBytes;
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kWarpRing = kStages * kStageBytes;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     *len_out = len;
     if (len <= 0) return 0;
     if (((len - 1) >> l2bs) >= p.max_blocks_per_seq) return 0;
-    return (int)((unsigned)(len - 1) / kFp4Stage) + 1;
+    return (int)((unsigned)(len - 1) / C::kStage) + 1;
   };
   // Sums stop at 2^27 units (600 GB of reads at 128 elements): lengths that
   // nobody meant, an error.
@@ -323,9 +325,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     pairs = __reduce_add_sync(0xffffffffu, lane < W ? warp_seqs[lane] : 0) * per_seq;
     __syncthreads();
   }
-  // Units of a CTA: an equal share, at least one per two warps (fewer parts to
+  // Units of a CTA: an equal share, at least a step per two warps (fewer parts to
   // merge where there is little work).
-  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, W / 2);
+  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, C::kWholeStages / 2);
   int cta0 = (int)min((long long)share * blockIdx.x, (long long)total);
   int cta1 = min(cta0 + share, total);
 
@@ -355,19 +357,20 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     return pl;
   };
 
-  // Where a CTA's share is at most a stage per warp, and so is the average pair,
+  // Where a CTA's share is at most a step per warp, and so is the average pair,
   // latency is what counts and a merge over CTAs costs more than the stages that it
   // spares: pairs of up to that many stages stay whole, with the CTA of their first
   // unit.  (64 sequences of up to 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 ->
-  // 8.3; with four stages per warp instead of one, 64 sequences of up to 2048 tokens
+  // 8.3; with four steps per warp instead of one, 64 sequences of up to 2048 tokens
   // took 16.5, not 14.5 us; one of 1024 tokens, all its pairs longer, 12.3, not 10.4.)
   // The CTA's two ends, then the warp's first stage: a loop, as one-time code is
   // paid by its length.
   bool ok = true;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
+  const bool short_pairs = total / (C::kWholeStages + kFp4PairCost) <= pairs;
 #pragma unroll 1
-  for (int i = share <= W && total / (W + kFp4PairCost) <= pairs ? 0 : 2; i < 3; ++i) {
+  for (int i = share <= C::kWholeStages && short_pairs ? 0 : 2; i < 3; ++i) {
     int unit = i == 0 ? cta0 : cta1;
     if (i == 2) {
       share_w = (cta1 - cta0 + W - 1) / W;
@@ -379,11 +382,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     pp = locate(unit);
     if (i == 2) break;
     const int first = pp.at - pp.k - kFp4PairCost;  // the pair's first unit
-    if (unit > first && pp.n <= W) unit = first + kFp4PairCost + pp.n;
+    if (unit > first && pp.n <= C::kWholeStages) unit = first + kFp4PairCost + pp.n;
     (i == 0 ? cta0 : cta1) = unit;
   }
   if (my0 < my1 && pp.at < my1) {
-    const int per_block = min(kFp4Stage / kFp4Tile, 1 << (l2bs - 3));  // tiles of a copy
+    const int per_block = min(C::kStage / kFp4Tile, 1 << (l2bs - 3));  // tiles of a copy
     const uint32_t lane_dst = (uint32_t)(lane * per_block) * C::kTileBytes;
     const uint32_t block_bytes = ((uint32_t)p.num_kv_heads << (l2bs - 3)) * C::kTileBytes;
 
@@ -407,9 +410,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
       const uint8_t* base;
     };
     auto fetch = [&]() -> Next {
-      const int tok0 = pp.k * kFp4Stage;
+      const int tok0 = pp.k * C::kStage;
       Next nx;
-      nx.tiles = min(kFp4Stage / kFp4Tile, (pp.len - tok0 + kFp4Tile - 1) >> 3);
+      nx.tiles = min(C::kStage / kFp4Tile, (pp.len - tok0 + kFp4Tile - 1) >> 3);
       nx.base = head_base + ((tok0 & ((1 << l2bs) - 1)) >> 3) * C::kTileBytes;
       nx.id = lane * per_block < nx.tiles ? __ldg(table + (tok0 >> l2bs)) : 0;
       // On to the next stage, if it is this warp's.
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     // and for ragged stages: the branches below are small and the same for the
     // warp, where a second body would be fetched anew at every sequence's end.
     auto attend = [&](const uint32_t stage, const int tokens) {
-      const bool ragged = tokens < kFp4Stage;
+      const bool ragged = tokens < kFp4Step;
       // ---- scores of 32 tokens: rows g (tile 2u) and g + 8 (tile 2u + 1) ----
       float sc[2][NT][4];
 #pragma unroll
@@ -794,7 +797,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           const bool w = wait_phase(bars + 8u * slot, parity, p.err, p.wait_limit);
           ok = __all_sync(0xffffffffu, w);
         }
-        if (ok) attend(ring + slot * C::kStageBytes, min(pc.len - k * kFp4Stage, kFp4Stage));
+        if (ok)
+#pragma unroll 1
+          for (int t0 = 0; t0 < C::kStage && k * C::kStage + t0 < pc.len; t0 += kFp4Step)
+            attend(ring + slot * C::kStageBytes + t0 / kFp4Tile * C::kTileBytes,
+                   min(pc.len - k * C::kStage - t0, kFp4Step));
         // The slot is free: the next stage.  After a wait that gave up nothing is
         // copied or computed any more, but the parts are still handed on, so that
         // the counters come out even.
