@@ -357,33 +357,53 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     return pl;
   };
 
-  // Where a CTA's share is at most a step per warp, and so is the average pair,
-  // latency is what counts and a merge over CTAs costs more than the stages that it
-  // spares: pairs of up to that many stages stay whole, with the CTA of their first
-  // unit.  (64 sequences of up to 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 ->
-  // 8.3; with four steps per warp instead of one, 64 sequences of up to 2048 tokens
-  // took 16.5, not 14.5 us; one of 1024 tokens, all its pairs longer, 12.3, not 10.4.)
-  // The CTA's two ends, then the warp's first stage: a loop, as one-time code is
-  // paid by its length.
+  // Ends of CTAs' and warps' parts that would cut a short pair move behind it: the
+  // pair stays whole with the warp (or, of several warps, the CTA) of its first unit,
+  // and nothing is left to merge, which takes a CTA 6 us where every warp cuts one.
+  // Short is a pair of no more stages than a warp's part has (256 sequences of 128
+  // tokens 29.2 -> 19.5 us, 1024 of up to 200, with parts less equal then, 48 -> 46).
+  // For a CTA whose share is at most a step per warp it is a pair of up to that: latency
+  // is what counts there, and a merge over CTAs costs more than the stages that it
+  // spares (64 sequences of up to 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 ->
+  // 8.3; with up to four steps per warp, 64 sequences of up to 2048 tokens took 16.5, not
+  // 14.5 us).  Both only where the average pair is short (one sequence of 1024 tokens
+  // looked in vain for 1.9 us).
+  // The CTA's two ends, then the warp's: a loop, as one-time code is paid by its length.
   bool ok = true;
+  const int per_warp = (share + W - 1) / W;
+  const bool few = share <= C::kWholeStages && total / (C::kWholeStages + kFp4PairCost) <= pairs;
+  const int whole_w = !few && total / (per_warp + kFp4PairCost) <= pairs ? per_warp : 0;
+  const int whole_cta = few ? C::kWholeStages : whole_w;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
-  const bool short_pairs = total / (C::kWholeStages + kFp4PairCost) <= pairs;
 #pragma unroll 1
-  for (int i = share <= C::kWholeStages && short_pairs ? 0 : 2; i < 3; ++i) {
-    int unit = i == 0 ? cta0 : cta1;
-    if (i == 2) {
+  for (int i = whole_cta ? 0 : 3; i < 4; ++i) {
+    if (i == 2 || (i == 3 && !whole_w)) {
       share_w = (cta1 - cta0 + W - 1) / W;
-      my0 = unit = cta0 + share_w * warp;
-      my1 = min(my0 + share_w, cta1);
-      if (my0 >= my1) break;
+      my1 = min(cta0 + share_w * (warp + 1), cta1);
+      if (!whole_w) i = 3;
     }
-    if (i < 2 && (unit <= 0 || unit >= total)) continue;
+    int unit = i == 0 ? cta0 : i == 1 ? cta1 : i == 2 ? my1 : cta0 + share_w * warp;
+    if (i == 3) my0 = unit;
+    if (i == 3 ? unit >= my1 : unit <= 0 || unit >= total) continue;
     pp = locate(unit);
-    if (i == 2) break;
     const int first = pp.at - pp.k - kFp4PairCost;  // the pair's first unit
-    if (unit > first && pp.n <= C::kWholeStages) unit = first + kFp4PairCost + pp.n;
-    (i == 0 ? cta0 : cta1) = unit;
+    if (unit > first && pp.n <= (i < 2 ? whole_cta : whole_w)) {
+      unit = first + kFp4PairCost + pp.n;
+      pp.k = 0;
+      pp.at = unit + kFp4PairCost;
+      if (i == 3 && unit < my1 && ++pp.hp == per_seq) {
+        pp.hp = 0;
+        do {
+          ++pp.s;
+          pp.n = stages_of(pp.s, &pp.len);
+        } while (pp.n == 0);
+      }
+    }
+    if (i == 0) cta0 = unit;
+    else if (i == 1) cta1 = unit;
+    else if (i == 2) my1 = unit;
+    else my0 = unit;
   }
   if (my0 < my1 && pp.at < my1) {
     const int per_block = min(C::kStage / kFp4Tile, 1 << (l2bs - 3));  // tiles of a copy
@@ -966,9 +986,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           mi = src[0];
           li = src[per_run];
         }
-        // Eight parts at a time (past the last, that one again, with no weight); the
+        // Four parts at a time (past the last, that one again, with no weight); the
         // first ones are on their way with the maxima and sums.
-        constexpr int kBatch = 8;
+        constexpr int kBatch = 4;
         float top = 0.f, w = 0.f, sum = 0.f;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) acc[e] = 0.f;

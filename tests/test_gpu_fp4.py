@@ -398,6 +398,19 @@ def test_decode_most_sequences():
     assert_decode(r(), r.batch)
 
 
+@pytest.mark.parametrize("head,heads,hkv", [(64, 4, 2), (128, 2, 2), (256, 3, 3)])
+@pytest.mark.parametrize("most,long", [(40, 0), (200, 0), (40, 9000), (300, 5000)])
+def test_decode_short_sequences_beside_long_ones(head, heads, hkv, most, long):
+    """Pairs that stay whole with a warp or a CTA, next to ones that are cut."""
+    rng = np.random.default_rng(most + long + head)
+    lens = rng.integers(0, most, 1500 if most < 100 else 300)
+    lens[7::31] = 0
+    if long:
+        lens[[0, 150, len(lens) - 1]] = long, long - 3, long // 2
+    r = Run(Batch(lens, heads, hkv, head, 16, seed=head + most))
+    assert_decode(r(), r.batch)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_decode_sequences_that_share_blocks_and_repeated_calls(dtype):
     """Rows of one table several times over, and calls that agree bit for bit
