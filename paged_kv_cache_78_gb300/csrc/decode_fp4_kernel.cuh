@@ -371,8 +371,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   // The CTA's two ends, then the warp's: a loop, as one-time code is paid by its length.
   bool ok = true;
   const int per_warp = (share + W - 1) / W;
-  const bool few = share <= C::kWholeStages && total / (C::kWholeStages + kFp4PairCost) <= pairs;
-  const int whole_w = !few && total / (per_warp + kFp4PairCost) <= pairs ? per_warp : 0;
+  auto short_of = [&](int stages) {  // the average pair has at most about so many
+    return total <= (long long)pairs * (stages + kFp4PairCost);
+  };
+  const bool few = share <= C::kWholeStages && short_of(C::kWholeStages);
+  const int whole_w = !few && short_of(per_warp) ? per_warp : 0;
   const int whole_cta = few ? C::kWholeStages : whole_w;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy
