@@ -123,7 +123,9 @@ __device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, const
 // sum over n products about n * 2^-25 too small: over a warp's 12600 tokens 1.3e-4.
 // That is less than bf16's half step of 2^-8 by far (short chains would cost 1% of the
 // time at four heads of 128, 9% at eight), but not fp32's, where chains end with
-// their step of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.
+// their step of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.  The
+// small parts of queries and weights go first, where they cut nothing off the large
+// ones' sum (errors a fifth smaller).
 template <bool kShort>
 struct Fp4Sum {
   float* c;
@@ -573,8 +575,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
             for (int b = 0; b < 2; ++b) {
               const uint32_t a[4] = {lo[2 * b], hi[2 * b], lo[2 * b + 1], hi[2 * b + 1]};
 #pragma unroll
-              for (int part = 0; part < kQParts; ++part) {
-                if (b == 0 && part == 0 && w % kSum == 0)
+              for (int part = kQParts - 1; part >= 0; --part) {  // small parts first
+                if (b == 0 && part == kQParts - 1 && w % kSum == 0)
                   mma_f16_first(sum, a, q[part][nt][2 * w + b]);
                 else
                   mma_f16(sum, a, q[part][nt][2 * w + b]);
@@ -717,7 +719,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
                                        half2_mul_by<true>(hb[2 * b], vs[e]),
                                        half2_mul_by<true>(hb[2 * b + 1], vs[e])};
 #pragma unroll
-                for (int qp = 0; qp < kQParts; ++qp) add[b](a, b2[e][qp], e == 0 && qp == 0);
+                for (int qp = kQParts - 1; qp >= 0; --qp)  // small parts first
+                  add[b](a, b2[e][qp], e == 0 && qp == kQParts - 1);
               }
             }
             add[0].done();
@@ -745,9 +748,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int qp = 0; qp < kQParts; ++qp) {
+                  for (int qp = kQParts - 1; qp >= 0; --qp) {
                     if (!kF32) mma_f16(o[nt][part * 8 + w * 4 + b], a, pt[qp][u][nt]);
-                    else if (u == 0 && qp == 0) mma_f16_first(own[nt][b], a, pt[qp][u][nt]);
+                    else if (u == 0 && qp == kQParts - 1) mma_f16_first(own[nt][b], a, pt[qp][u][nt]);
                     else mma_f16(own[nt][b], a, pt[qp][u][nt]);
                   }
               }
