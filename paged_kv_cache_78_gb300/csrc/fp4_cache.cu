@@ -48,8 +48,7 @@ __device__ __forceinline__ void fp4_places(int row, int j, int kv, int* codes, i
   *scale = kv ? fp4_value_scales(D) + j * 8 + row : fp4_key_scales(D) + row * (D / kFp4Group) + j;
 }
 
-// The group's largest magnitude; a NaN if there is one, and the largest number
-// for an infinity.
+// The group's largest magnitude; a NaN if there is one.
 __device__ __forceinline__ float largest(const uint4* w, const __nv_bfloat16*) {
   __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
@@ -59,8 +58,7 @@ __device__ __forceinline__ float largest(const uint4* w, const __nv_bfloat16*) {
     for (int e = 0; e < 4; ++e)
       top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[e])));
   }
-  const float x = __bfloat162float(__hmax_nan(top.x, top.y));
-  return x == INFINITY ? 3.0e38f : x;
+  return __bfloat162float(__hmax_nan(top.x, top.y));
 }
 __device__ __forceinline__ float largest(const uint4* w, const float*) {
   uint32_t top = 0;  // bits order NaNs above everything
@@ -68,7 +66,7 @@ __device__ __forceinline__ float largest(const uint4* w, const float*) {
   for (int c = 0; c < 4; ++c)
     top = max(max(top, max(w[c].x & 0x7fffffffu, w[c].y & 0x7fffffffu)),
               max(w[c].z & 0x7fffffffu, w[c].w & 0x7fffffffu));
-  return top == 0x7f800000u ? 3.0e38f : __uint_as_float(top);
+  return __uint_as_float(top);
 }
 
 // A group to its codes; returns the scale's code.

@@ -76,14 +76,16 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// e4m3 of max / 6 for a finite max or NaN (nearest, ties to even, at most 448;
-// NaN stays NaN).  The quotient is first rounded to fp32 (by one step of
+// e4m3 of max / 6 (nearest, ties to even, at most 448; NaN stays NaN).  A max past
+// 6 * 448, infinity among them (a number may become one in the division by a tensor
+// scale below 1), is as good as that.  The quotient is first rounded to fp32 (by one step of
 // Newton's iteration on the rounded product, which is enough for a correctly
 // rounded 1 / 6), which never moves it onto or past a border of e4m3: a border
 // times six has at most seven significant bits, so a max other than that is
 // off by one of its own last places, more than the rounding.
 __device__ __forceinline__ uint32_t fp4_scale_code(float max_abs) {
-  constexpr float kSixth = 1.f / 6.f;
+  constexpr float kSixth = 1.f / 6.f, kMost = 6.f * 448.f;
+  if (max_abs > kMost) max_abs = kMost;  // false for NaN
   const float p = max_abs * kSixth;
   const float q = fmaf(fmaf(-6.f, p, max_abs), kSixth, p);
   uint32_t r;

@@ -133,6 +133,28 @@ def test_write_special_values(dtype):
     assert same(host(ko), want) and same(host(vo), want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tensor_scale", [0.5, 0.25, 1.0, 2.0 ** -32, 2.0 ** 32])
+def test_write_saturates_under_every_tensor_scale(dtype, tensor_scale):
+    """Infinities, and finite numbers below and above what the largest scale holds and
+    what 32 bits hold once divided by the tensor scale."""
+    rng = np.random.default_rng(17)
+    big = np.array([2688.0, 2689.0, 2700.0, 3e4, 1e20, 1e38, 3.3e38, 3.5e38, 1e40, 1e47]) * tensor_scale
+    big = np.append(big[big < 3.38e38], [2.0 ** 127, 3.38e38, np.inf, np.nan])
+    x = rng.standard_normal((len(big), 2, 64)) * tensor_scale
+    x[:, 0, 5], x[:, 1, 20] = big, -big
+    x[-1, 0, 6] = np.inf                  # beside a NaN
+    t = rounded(x, dtype)
+    n = len(big)
+    cache = torch.randint(0, 256, (-(-n // 8), 2, 1, 9 * 64), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(n, device="cuda")
+    pa.pa_reshape_and_cache_fp4(cache, dev(t), dev(-t), slots, tensor_scale, tensor_scale)
+    want = fp4.dequantise(*fp4.quantise(host(t), tensor_scale), tensor_scale)
+    k, v = fp4.read(cache.cpu().numpy(), np.arange(n), tensor_scale, tensor_scale)
+    assert same(k, want) and same(v, -want)
+    assert np.isnan(want[-1, 0, :16]).all() and np.isfinite(want[:-1]).all()
+
+
 def test_padding_and_slots_outside_the_pool():
     rng = np.random.default_rng(8)
     cache = rng.integers(0, 256, (3, 2, 2, 9 * 64), dtype=np.uint8)
