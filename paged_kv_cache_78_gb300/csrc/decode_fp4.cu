@@ -20,9 +20,12 @@ size_t partial_floats(int head_size, int group) {
 
 }  // namespace
 
-// Header (the counters), a partial per warp (16 at most), four per CTA.
+// Header (the counters), a partial per warp (16 at most), four per CTA, the ended
+// chains of every warp.
 size_t decode_fp4_workspace_bytes(int head_size, int group, int num_sms) {
-  return kFp4HeaderBytes + (size_t)num_sms * (16 + 4) * partial_floats(head_size, group) * 4;
+  return kFp4HeaderBytes + (size_t)num_sms * 4 *
+                               ((16 + 4) * partial_floats(head_size, group) +
+                                16 * fp4_chain_floats(head_size, fp4_heads(head_size, group)));
 }
 
 cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, int dtype,
@@ -32,6 +35,7 @@ cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, in
   p.warp_partials =
       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFp4HeaderBytes);
   p.cta_partials = p.warp_partials + (size_t)num_sms * 16 * partial_floats(p.head_size, p.group);
+  p.chains = p.cta_partials + (size_t)num_sms * 4 * partial_floats(p.head_size, p.group);
   const bool half = dtype == PA_BF16;
   switch (p.head_size) {
     case 64:

@@ -57,6 +57,12 @@ __host__ __device__ constexpr int fp4_partial_floats(int rows, int head_size, in
   return (rows * (head_size + 2 * splits) + 3) / 4 * 4;
 }
 
+// Floats of a warp's ended chains of sums: for each of a lane's columns (two per tile of
+// eight, which four heads use twice) its maximum, its sum and its weighted values.
+__host__ __device__ constexpr int fp4_chain_floats(int head_size, int heads) {
+  return heads == 4 ? 32 * 2 * (head_size / 16 + 2) : 32 * 2 * (heads / 8) * (head_size / 8 + 2);
+}
+
 struct Fp4DecodeParams {
   void* out;
   const void* query;
@@ -67,6 +73,7 @@ struct Fp4DecodeParams {
   unsigned int* counters;  // [CTAs][3][kFp4Units], zero between calls
   float* warp_partials;    // [CTAs][warps][partial]
   float* cta_partials;     // [CTAs][4][partial]: of CTAs, then of groups of CTAs
+  float* chains;           // [CTAs][warps][fp4_chain_floats]
   long long wait_limit;
   int64_t query_stride;
   float scale_log2;   // scale * key_scale * log2(e)

@@ -56,6 +56,14 @@ constexpr float kFp4Lift = 7.f;   // weights are 2^(S - m + 7): fp16 keeps small
 constexpr float kFp4Slack = 8.f;  // scores may pass the running maximum by this before it moves
 constexpr int kFp4RingBytes = 216 * 1024;
 constexpr int kFp4MaxWork = 1 << 27;  // units of a launch
+// Tokens of a chain of sums.  Sums over more lose what is small beside them: the matrix
+// unit cuts off, and rounded additions drop whatever is below half a step (pairs of a
+// million tokens that a warp sees whole: bf16 1e-2 of the result, fp32 2.8e-4).  So a
+// chain's sums are added, with rounding, to the piece's in global memory: fp32 outputs are
+// then off by 1e-6 to 1.5e-6 up to 131072 tokens of a warp and 6e-6 at a million, bf16 ones
+// by 4e-5 before their rounding.  At one in 128 stages it costs nothing; its code costs
+// every call 0 to 0.7 us (four short sequences 9.7 -> 10.3).
+constexpr int kFp4Chain = 4096;
 // A pair's queries and its end count as this many stages (32 sequences of 40 pairs
 // each: 52 us at 0, 43 at 1, 44 at 2).
 constexpr int kFp4PairCost = 1;
@@ -120,12 +128,11 @@ __device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, const
 
 // Products added to c: by the matrix unit, or (kShort) in a chain of their own that
 // done() adds with rounding.  The unit cuts its sums off towards zero, which makes a
-// sum over n products about n * 2^-25 too small: over a warp's 12600 tokens 1.3e-4.
-// That is less than bf16's half step of 2^-8 by far (short chains would cost 1% of the
-// time at four heads of 128, 9% at eight), but not fp32's, where chains end with
-// their step of 32 tokens: 4e-7 to 2e-6 at any length, as an unfused fp32 form.  The
-// small parts of queries and weights go first, where they cut nothing off the large
-// ones' sum (errors a fifth smaller).
+// sum over n products about 1e-8 n too small: over kFp4Chain tokens 4e-5.  That is less
+// than bf16's half step of 2^-8 by far (short chains would cost 1% of the time at four
+// heads of 128, 9% at eight), but not fp32's, where the unit's chains end with their step
+// of 32 tokens.  The small parts of queries and weights go first, where they cut nothing off
+// the large ones' sum (errors a fifth smaller).
 template <bool kShort>
 struct Fp4Sum {
   float* c;
@@ -196,7 +203,6 @@ struct Fp4Piece {
   int n, len;      // stages and tokens of the sequence
   int at;          // the unit of its first stage
 };
-constexpr int kFp4Pieces = 8;  // ring of pieces, at least the stages in flight + 2
 
 // The parts of one pair in a CTA: warps `first` .. w, w the last of them,
 // whose run it is.  A part that reaches its warp's end lies in the warp's ring,
@@ -219,12 +225,15 @@ struct Fp4Config {
   static constexpr int kFit = kFp4RingBytes / kWarps / kStageBytes;
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kWarpRing = kStages * kStageBytes;
+  // Ring of a warp's pieces: when a piece ends, the stages in flight, the one that waits
+  // for a slot and the one after it may all have entered pieces of their own.
+  static constexpr int kPieceRing = kStages + 3 <= 8 ? 8 : 16;
   static constexpr int kBars = kWarps * kWarpRing;
   static constexpr int kPieces = kBars + 8 * kWarps * kStages;
-  static constexpr int kPre = (kPieces + kWarps * kFp4Pieces * (int)sizeof(Fp4Piece) + 15) / 16 * 16;
+  static constexpr int kPre = (kPieces + kWarps * kPieceRing * (int)sizeof(Fp4Piece) + 15) / 16 * 16;
   static constexpr int kRuns = (kPre + 4 * (kThreads + 2 * kWarps) + 15) / 16 * 16;
   static constexpr int kSmem = kRuns + (int)sizeof(Fp4Run) * 2 * kWarps;
-  static_assert(kStages >= 2 && kStages + 2 <= kFp4Pieces, "rings");
+  static_assert(kStages >= 2 && kStages + 3 <= kPieceRing, "rings");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(fp4_partial_floats(H, D, 2) * 4 <= kWarpRing, "a part fits its warp's ring");
 };
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * C::kWarpRing;
   const uint32_t bars = smem_u32(smem) + C::kBars + (uint32_t)warp * NS * 8;
-  Fp4Piece* pieces = reinterpret_cast<Fp4Piece*>(smem + C::kPieces) + warp * kFp4Pieces;
+  Fp4Piece* pieces = reinterpret_cast<Fp4Piece*>(smem + C::kPieces) + warp * C::kPieceRing;
   // First query head and heads of a pair.
   auto heads_of = [&](int hp, int* heads) -> int {
     const int h = hp / head_tiles, ht = hp - h * head_tiles;
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
       const int h = pp.hp / head_tiles;
       head_base = p.cache + ((size_t)h << (l2bs - 3)) * C::kTileBytes;
       if (lane == 0)
-        pieces[entered % kFp4Pieces] =
+        pieces[entered % C::kPieceRing] =
             Fp4Piece{pp.s, pp.hp, pp.k, min(pp.n - pp.k, my1 - pp.at), pp.n, pp.len, pp.at};
       ++entered;
     };
@@ -770,76 +779,116 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     bool last = false;
     for (int piece = 0; !last; ++piece) {
       __syncwarp();
-      const Fp4Piece pc = pieces[piece % kFp4Pieces];
-      int heads;
-      const int head0 = heads_of(pc.hp, &heads);
+      // What is needed of the record at the piece's end is read then, as registers are
+      // short between.
+      const Fp4Piece& rec = pieces[piece % C::kPieceRing];
+      const int len = rec.len;
       // ---- the pair's queries ----
-      // fp16 holds a row scaled by a power of two to a maximum in [2^13, 2^14)
-      // (bf16 exactly, unless an element is 2^-30 of the largest).
+      {
+        int heads;
+        const int head0 = heads_of(rec.hp, &heads);
+        // fp16 holds a row scaled by a power of two to a maximum in [2^13, 2^14)
+        // (bf16 exactly, unless an element is 2^-30 of the largest).
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int head = nt * 8 + (kNarrow ? g & 3 : g);
-        float x[D / 4];
-        if (head < heads) {
-          const T* src = static_cast<const T*>(p.query) + pc.s * p.query_stride +
-                         (size_t)(head0 + head) * D + t * (D / 4);
-          constexpr int kPer = ElemTraits<T>::kPerChunk;
+        for (int nt = 0; nt < NT; ++nt) {
+          const int head = nt * 8 + (kNarrow ? g & 3 : g);
+          float x[D / 4];
+          if (head < heads) {
+            const T* src = static_cast<const T*>(p.query) + rec.s * p.query_stride +
+                           (size_t)(head0 + head) * D + t * (D / 4);
+            constexpr int kPer = ElemTraits<T>::kPerChunk;
 #pragma unroll
-          for (int c = 0; c < D / 4 / kPer; ++c)
-            ElemTraits<T>::unpack(ldg_nc_v4(src + c * kPer), x + c * kPer);
-        } else {
+            for (int c = 0; c < D / 4 / kPer; ++c)
+              ElemTraits<T>::unpack(ldg_nc_v4(src + c * kPer), x + c * kPer);
+          } else {
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t ex = max(top >> 23, 14u);
-        const float up = __uint_as_float((267u - ex) << 23);
-        const float down = __uint_as_float((ex - 13u) << 23);
-        cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
-        cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float x0 = x[4 * j + 2 * b] * up, x1 = x[4 * j + 2 * b + 1] * up;
-            const uint32_t hi = pack_half2(x0, x1);
-            q[0][nt][j][b] = hi;
-            if constexpr (kF32) q[1][nt][j][b] = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+            for (int e = 0; e < D / 4; ++e) x[e] = 0.f;
           }
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
+          uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+          for (int e = 0; e < D / 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const uint32_t ex = max(top >> 23, 14u);
+          const float up = __uint_as_float((267u - ex) << 23);
+          const float down = __uint_as_float((ex - 13u) << 23);
+          cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale_log2;
+          cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale_log2;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
+          for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float x0 = x[4 * j + 2 * b] * up, x1 = x[4 * j + 2 * b + 1] * up;
+              const uint32_t hi = pack_half2(x0, x1);
+              q[0][nt][j][b] = hi;
+              if constexpr (kF32) q[1][nt][j][b] = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+            }
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
+        }
       }
       fresh = true;
-      for (int k = pc.k0; k < pc.k0 + pc.stages; ++k) {
-        if (ok) {
-          const bool w = wait_phase(bars + 8u * slot, parity, p.err, p.wait_limit);
-          ok = __all_sync(0xffffffffu, w);
-        }
-        if (ok)
+      constexpr int kChainStages = kFp4Chain / C::kStage;
+      for (int k = rec.k0; k < rec.k0 + rec.stages;) {
+        const int chain_end = min(k + kChainStages, rec.k0 + rec.stages);
+        for (; k < chain_end; ++k) {
+          if (ok) {
+            const bool w = wait_phase(bars + 8u * slot, parity, p.err, p.wait_limit);
+            ok = __all_sync(0xffffffffu, w);
+          }
+          if (ok)
 #pragma unroll 1
-          for (int t0 = 0; t0 < C::kStage && k * C::kStage + t0 < pc.len; t0 += kFp4Step)
-            attend(ring + slot * C::kStageBytes + t0 / kFp4Tile * C::kTileBytes,
-                   min(pc.len - k * C::kStage - t0, kFp4Step));
-        // The slot is free: the next stage.  After a wait that gave up nothing is
-        // copied or computed any more, but the parts are still handed on, so that
-        // the counters come out even.
-        if (have) {
-          if (ok) issue(next, slot);
-          if ((have = more)) next = fetch();
+            for (int t0 = 0; t0 < C::kStage && k * C::kStage + t0 < len; t0 += kFp4Step)
+              attend(ring + slot * C::kStageBytes + t0 / kFp4Tile * C::kTileBytes,
+                     min(len - k * C::kStage - t0, kFp4Step));
+          // The slot is free: the next stage.  After a wait that gave up nothing is
+          // copied or computed any more, but the parts are still handed on, so that
+          // the counters come out even.
+          if (have) {
+            if (ok) issue(next, slot);
+            if ((have = more)) next = fetch();
+          }
+          if (++slot == NS) {
+            slot = 0;
+            parity ^= 1;
+          }
         }
-        if (++slot == NS) {
-          slot = 0;
-          parity ^= 1;
+        if (__builtin_expect(rec.stages > kChainStages, 0)) {
+          // The sums of the piece's chains that ended before are added to this one's, at
+          // its maximum; then they are put away for the next.
+          const bool first = k - rec.k0 == kChainStages, final = k == rec.k0 + rec.stages;
+          float* past =
+              p.chains + ((size_t)blockIdx.x * W + warp) * fp4_chain_floats(D, H) + lane;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float* at = past + (nt * 2 + c) * (2 * kTiles + 2) * 32;
+              const float w = first ? 0.f : fast_exp2(at[0] - m[nt][c]);
+              auto join = [&](int i, float& sum) {
+                if (!first) sum = fmaf(at[32 * i], w, sum);
+                if (!final) {
+                  at[32 * i] = sum;
+                  sum = 0.f;
+                }
+              };
+              join(1, l[nt][c]);
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) {
+                join(2 * j + 2, o[nt][j][c]);
+                join(2 * j + 3, o[nt][j][c + 2]);
+              }
+              at[0] = m[nt][c];
+            }
         }
       }
+      const Fp4Piece pc = rec;
+      int heads;
+      const int head0 = heads_of(pc.hp, &heads);
       const bool ends = pc.k0 + pc.stages == pc.n;
       last = pc.at + pc.stages + (ends ? kFp4PairCost : 0) >= my1;
 

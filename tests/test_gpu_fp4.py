@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import paged_kv_cache_78_gb300 as pa
-from fp4_util import TORCH, Batch, assert_decode, host, rounded
+from fp4_util import TORCH, Batch, assert_decode, decode_bound, host, rounded
 from oracle import fp4
 
 pytestmark = pytest.mark.gpu
@@ -463,6 +463,60 @@ def test_decode_fp32_sums_are_rounded_not_cut_off():
     b.query = b.query.expand(512, 8, 128).contiguous()
     got = host(Run(b)())
     assert np.max(np.abs(got - ref) / np.abs(ref)) <= 2.1e-5
+
+
+@pytest.mark.parametrize("dtype,head,heads", [("bf16", 128, 4), ("bf16", 128, 8), ("bf16", 64, 16), ("bf16", 256, 8),
+                                              ("fp32", 128, 4), ("fp32", 64, 8), ("fp32", 256, 8)])
+def test_decode_sums_do_not_drift_with_the_length(dtype, head, heads):
+    """Pairs of a million tokens that a warp sees whole.  Every value of an element is
+    the same, so that the output is that value whatever the weights are.  Off are the
+    weights' roundings (bf16 2^-11, fp32 2^-22 at most), the output's (2^-8, 2^-24) and two
+    sums.  bf16: chains of 2^12 tokens, 2^9 additions that may cut off 2^-23 each.  fp32:
+    the same number rounded to nearest, 2^-24 / sqrt(3) in standard deviation each, of
+    which ten are allowed, and the four cut-offs of a step.  Then 2^8 chains' results
+    that are rounded to nearest."""
+    seqs, tokens, block = 2600, 1 << 20, 256
+    b = Batch([2048], heads, 1, head, block, dtype, seed=head + heads, query_std=2.0)
+    value = np.resize([0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -1.5], head) * (1 + np.arange(head) // 16 % 8)
+    fp4.write(b.cache, host(b.key), np.broadcast_to(value, (2048, 1, head)), b.slots)
+    held = fp4.read(b.cache, b.slots[:1])[1][0]
+    r = Run(b)
+    r.tables = r.tables.repeat(1, tokens // 2048).expand(seqs, -1).contiguous()
+    r.lens = torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")
+    r.query = dev(rounded(2.0 * np.random.default_rng(head).standard_normal((seqs, heads, head)), dtype))
+    r.out = torch.full_like(r.query, 77.0)
+    worst = np.max(np.abs(host(r()) / held - 1.0))
+    deviation = 10 * 2.0 ** -24 / np.sqrt(3)
+    if dtype == "bf16":
+        bound = 2.0 ** -11 + 2.0 ** -8 + 2 * (2.0 ** 9 * 2.0 ** -23 + 2.0 ** 4 * deviation)
+    else:
+        bound = 2.0 ** -22 + 2.0 ** -24 + 4 * 2.0 ** -23 + 2 * (2.0 ** 4.5 + 2.0 ** 4) * deviation
+    assert worst <= bound
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("head,heads", [(64, 4), (64, 16), (128, 3), (128, 8), (128, 16), (256, 4), (256, 11)])
+@pytest.mark.parametrize("rise", [0.0, 120.0, -120.0])
+def test_decode_long_sequences_in_a_warp(dtype, head, heads, rise):
+    """Pairs of several chains of 4096 tokens and a token, whole with a warp, whose scores
+    stay, rise (the maximum moves again and again) or fall."""
+    seqs, lens = 3000, [12289, 20001, 4096, 4097]
+    b = Batch([20001], heads, 1, head, 64, dtype, seed=head + heads)
+    key = host(b.key)
+    key[:, 0, 0] = np.linspace(0.0, 6.0, 20001)
+    fp4.write(b.cache, key, host(b.value), b.slots)
+    q = host(b.query).repeat(4, 0)
+    q[..., 0] = rise / (6.0 * b.scale)
+    b.query, b.tables, b.lens = rounded(q, dtype), b.tables.repeat(4, 0), np.array(lens, dtype=np.int32)
+    ref, mass, total, reach = b.reference()
+    bound = decode_bound(ref, mass, total, reach, b.lens, head, dtype)
+    r = Run(b)
+    r.tables, r.lens = r.tables.repeat(seqs // 4, 1), r.lens.repeat(seqs // 4)
+    r.query = r.query.repeat(seqs // 4, 1, 1)
+    r.out = torch.full_like(r.query, 77.0)
+    got = host(r()).reshape((-1,) + ref.shape)
+    assert (np.abs(got - ref) <= bound).all()
 
 
 def test_two_graphs_share_a_workspace_and_lengths_grow():
