@@ -43,6 +43,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -640,8 +641,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
               for (int e = c; e < 4; e += 2)
                 if (u * 16 + (e >> 1) * 8 + g < tokens) top = fmaxf(top, sc[u][nt][e] * cs[nt][c]);
             top = group_max<4>(top);
-            const float m_new = fmaxf(m[nt][c], top - kFp4Lift);
-            const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m[nt][c] - m_new);
+            // Never minus infinity: scores below the least number weigh nothing then.
+            const float m_new = fmaxf(fmaxf(m[nt][c], top - kFp4Lift), -FLT_MAX);
+            const float alpha = fast_exp2(m[nt][c] - m_new);
             m[nt][c] = m_new;
             l[nt][c] *= alpha;
 #pragma unroll

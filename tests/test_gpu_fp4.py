@@ -313,6 +313,27 @@ def test_decode_rising_scores():
     assert_decode(Run(b)(), b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("far,tokens,seqs", [(40, 100, 1), (3000, 5000, 1), (4999, 5000, 1), (70, 90, 400)])
+def test_decode_scores_below_the_least_number_weigh_nothing(dtype, far, tokens, seqs):
+    """The first `far` tokens' scores are beyond 32 bits, the others' are zero: the mean of
+    the others' values, whose weights are equal and exact.  Off are sums (2^-23 an addition
+    of 16 tokens) and the output's rounding."""
+    b = Batch([tokens], 4, 2, 64, 16, dtype, seed=far)
+    key = np.zeros((tokens, 2, 64))
+    key[:far] = 6 * 448.0
+    fp4.write(b.cache, key, host(b.value), b.slots)
+    b.query = rounded(np.full((1, 4, 64), -(2.0 ** 120)), dtype)
+    ref, mass = b.reference()[:2]
+    r = Run(b)
+    r.tables, r.lens = r.tables.expand(seqs, -1).contiguous(), r.lens.expand(seqs).contiguous()
+    r.query = r.query.expand(seqs, -1, -1).contiguous()
+    r.out = torch.full_like(r.query, 77.0)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    bound = half * (1 + 2.0 ** -6) * np.abs(ref) + (tokens / 16 + 16) * 2.0 ** -23 * mass
+    assert (np.abs(host(r()) - ref) <= bound).all()
+
+
 def test_decode_nan_and_infinity():
     b = Batch([40, 60, 50], 4, 2, 64, 16, "bf16", seed=10)
     q = b.query.clone()
