@@ -600,6 +600,17 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
         }
       }
 
+      // Rounded here, so that the largest less the maximum is exact: were the product
+      // part of that difference, it would be off by half a step of the maximum, and
+      // weights infinite or all zero where that is 8 or more (scores of 2^27 on).  (As one
+      // instruction it took the same time.)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[u][nt][c] = __fmul_rn(sc[u][nt][c], cs[nt][c & 1]);
+
       // ---- softmax: the maximum moves only when a score passes it by 2^8 ----
       float y[2][NT][4];
       auto weigh = [&]() {  // exponents; their maximum of this thread
@@ -610,7 +621,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              y[u][nt][c] = fmaf(sc[u][nt][c], cs[nt][c & 1], -m[nt][c & 1]);
+              y[u][nt][c] = __fsub_rn(sc[u][nt][c], m[nt][c & 1]);
         if (ragged) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int e = c; e < 4; e += 2)
-                if (u * 16 + (e >> 1) * 8 + g < tokens) top = fmaxf(top, sc[u][nt][e] * cs[nt][c]);
+                if (u * 16 + (e >> 1) * 8 + g < tokens) top = fmaxf(top, sc[u][nt][e]);
             top = group_max<4>(top);
             // Never minus infinity: scores below the least number weigh nothing then.
             const float m_new = fmaxf(fmaxf(m[nt][c], top - kFp4Lift), -FLT_MAX);

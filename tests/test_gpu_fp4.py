@@ -334,6 +334,28 @@ def test_decode_scores_below_the_least_number_weigh_nothing(dtype, far, tokens, 
     assert (np.abs(host(r()) - ref) <= bound).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 20, 2.0 ** 24, 2.0 ** 27, 2.0 ** 34, 2.0 ** 60, 2.0 ** 110])
+def test_decode_scores_with_steps_above_one(dtype, size):
+    """Scores so large that neighbouring fp32 numbers are units or more apart: the token with
+    the largest has all the weight (the next is further away than scores are off: a sum
+    of head / 16 + 5 parts, 2^-22 of its mass each, twice), which is rounded once to fp16."""
+    b = Batch([700, 33, 5000], 6, 2, 64, 16, dtype, seed=31, query_std=size)
+    ref, _, _, reach = b.reference()
+    sure = np.zeros(ref.shape[:2], dtype=bool)
+    for r, n in enumerate(b.lens):
+        at = np.arange(n)
+        k, v = fp4.read(b.cache, b.tables[r, at // 16].astype(np.int64) * 16 + at % 16)
+        for h in range(6):
+            x = np.sort(k[:, h // 3] @ host(b.query)[r, h]) * b.scale
+            sure[r, h] = x[-1] - x[-2] > 2 * 9 * 2.0 ** -22 * reach[r, h, 0] + 40
+    assert sure.sum() >= 12
+    got = host(Run(b)())
+    half = 2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref)[sure] <= half * np.abs(ref)[sure] + 1e-12).all()
+
+
 def test_decode_nan_and_infinity():
     b = Batch([40, 60, 50], 4, 2, 64, 16, "bf16", seed=10)
     q = b.query.clone()
