@@ -461,6 +461,7 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
  * serves sequences as they grow.  Weights of the values enter their product
  * rounded to fp16 for bf16 outputs (relative 2^-11; a bf16 output has 2^-8), in
  * two fp16 parts for fp32 outputs; queries likewise (bf16 queries are exact).
+ * A weight is off by up to 2^-32 (fp32 outputs: 2^-36) of the largest besides.
  * Sums over tokens are fp32, in chains of at most 4096 tokens whose results are
  * added with rounding: for bf16 outputs a chain may come out 4e-5 too small (the
  * matrix unit cuts off), fp32 outputs are off by about 1e-6 (6e-6 where a warp

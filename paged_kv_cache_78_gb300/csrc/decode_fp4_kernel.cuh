@@ -53,8 +53,13 @@
 
 namespace pa {
 
-constexpr float kFp4Lift = 7.f;   // weights are 2^(S - m + 7): fp16 keeps small ones
-constexpr float kFp4Slack = 8.f;  // scores may pass the running maximum by this before it moves
+// Weights are 2^(S - m + lift), and scores may pass the running maximum by the slack before
+// it moves: lift + slack = 15, the most that fp16 holds.  fp16 has steps of 2^-24, so a
+// weight is off by up to 2^-25 where the largest is 2^lift or more: 2^-32 of it for bf16,
+// whose half step that stays below for millions of them, and 2^-36 for fp32 (8 x 32768
+// tokens as with 2^-32 to 0.4%; 2^-39 would cost 1%, as the maximum moves more often).
+__host__ __device__ constexpr float fp4_lift(bool fp32) { return fp32 ? 11.f : 7.f; }
+constexpr float kFp4Top = 15.f;
 constexpr int kFp4RingBytes = 216 * 1024;
 constexpr int kFp4MaxWork = 1 << 27;  // units of a launch
 // Tokens of a chain of sums.  Sums over more lose what is small beside them: the matrix
@@ -256,6 +261,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   constexpr int kSteps = D / 16;                    // of QK
   constexpr int kTiles = kNarrow ? D / 32 : D / 16;  // of O^T
   constexpr int kQParts = kF32 ? 2 : 1;
+  constexpr float kLift = fp4_lift(kF32);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[u][nt][c] = __fmul_rn(sc[u][nt][c], cs[nt][c & 1]);
 
-      // ---- softmax: the maximum moves only when a score passes it by 2^8 ----
+      // ---- softmax: the maximum moves only when a score passes it by the slack ----
       float y[2][NT][4];
       auto weigh = [&]() {  // exponents; their maximum of this thread
         float over = -INFINITY;
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
             for (int c = 0; c < 4; ++c) over = fmaxf(over, y[u][nt][c]);
         return over;
       };
-      if (fresh || __any_sync(0xffffffffu, weigh() > kFp4Lift + kFp4Slack)) {
+      if (fresh || __any_sync(0xffffffffu, weigh() > kFp4Top)) {
         fresh = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -652,8 +658,9 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
               for (int e = c; e < 4; e += 2)
                 if (u * 16 + (e >> 1) * 8 + g < tokens) top = fmaxf(top, sc[u][nt][e]);
             top = group_max<4>(top);
-            // Never minus infinity: scores below the least number weigh nothing then.
-            const float m_new = fmaxf(fmaxf(m[nt][c], top - kFp4Lift), -FLT_MAX);
+            // Rounded up, so that no weight passes 2^lift where the steps are wide.  Never
+            // minus infinity: scores below the least number weigh nothing then.
+            const float m_new = fmaxf(fmaxf(m[nt][c], __fsub_ru(top, kLift)), -FLT_MAX);
             const float alpha = fast_exp2(m[nt][c] - m_new);
             m[nt][c] = m_new;
             l[nt][c] *= alpha;

@@ -562,6 +562,30 @@ def test_decode_long_sequences_in_a_warp(dtype, head, heads, rise):
     assert (np.abs(got - ref) <= bound).all()
 
 
+def test_decode_fp32_keeps_small_weights():
+    """One token far above all others, in a warp that sees the whole sequence: the others'
+    weights are 2^-34 to 2^-33 of its, and its value is zero.  Weights are kept in steps of
+    2^-24 where the largest is 2^11 at least, so each is off by half a step, 2^-36 of the
+    largest, at most; relative errors of what is kept are as in decode_bound."""
+    seqs, tokens, heads, head = 2600, 8193, 8, 128
+    b = Batch([tokens], heads, 1, head, 256, "fp32", seed=3)
+    key, value = np.full((tokens, 1, head), 0.0), np.full((tokens, 1, head), 6.0)
+    key[..., 0], key[0, 0, 0], value[0] = -6.0, 6.0, 0.0
+    fp4.write(b.cache, key, value, b.slots)
+    gap = np.linspace(33.0, 34.0, heads)                       # powers of two between the weights
+    q = np.zeros((1, heads, head))
+    q[0, :, 0] = gap * np.log(2.0) / (12.0 * b.scale)
+    b.query = rounded(q, "fp32")
+    ref, mass, total, reach = b.reference()
+    r = Run(b)
+    r.tables = r.tables.expand(seqs, -1).contiguous()
+    r.lens = torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")
+    r.query = r.query.expand(seqs, -1, -1).contiguous()
+    r.out = torch.full_like(r.query, 77.0)
+    bound = decode_bound(ref, mass, 0 * total, reach, [tokens], head, "fp32") + 2.0 ** -36 * total
+    assert (np.abs(host(r()) - ref) <= bound).all()
+
+
 def test_two_graphs_share_a_workspace_and_lengths_grow():
     a = Run(Batch([70, 1, 300], 8, 2, 128, 16, seed=17))
     b = Run(Batch([9, 2000], 4, 1, 128, 16, seed=18), workspace=None)
