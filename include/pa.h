@@ -458,7 +458,11 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
  * pool holds past a sequence's end (NaN scales among it) is never used.
  * Groups of num_heads / num_kv_heads <= 16.  No bound on the lengths is
  * needed: the launch depends on the shapes alone, so that a captured call
- * serves sequences as they grow.  Weights of the values enter their product
+ * serves sequences as they grow.  Its work, the sum of
+ * (seq_len / 32 + 2) * num_kv_heads (twice that for heads of 256 in groups past
+ * eight), has to stay below 10^9, half a second of reading at the least; a call
+ * with more records PA_DEVERR_SEQ_LEN and leaves the rows of all sequences that
+ * are not empty undefined.  Weights of the values enter their product
  * rounded to fp16 for bf16 outputs (relative 2^-11; a bf16 output has 2^-8), in
  * two fp16 parts for fp32 outputs; queries likewise (bf16 queries are exact).
  * A weight is off by up to 2^-32 (fp32 outputs: 2^-36) of the largest besides.

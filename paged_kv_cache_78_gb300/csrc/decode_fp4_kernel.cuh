@@ -61,7 +61,9 @@ namespace pa {
 __host__ __device__ constexpr float fp4_lift(bool fp32) { return fp32 ? 11.f : 7.f; }
 constexpr float kFp4Top = 15.f;
 constexpr int kFp4RingBytes = 216 * 1024;
-constexpr int kFp4MaxWork = 1 << 27;  // units of a launch
+// Units of a launch are at most about this many (5 TB of reads at 128 elements, half a
+// second and more; sequences may share blocks), so that two sums of them fit an int.
+constexpr int kFp4MaxWork = (1 << 30) - 1;
 // Tokens of a chain of sums.  Sums over more lose what is small beside them: the matrix
 // unit cuts off, and rounded additions drop whatever is below half a step (pairs of a
 // million tokens that a warp sees whole: bf16 1e-2 of the result, fp32 2.8e-4).  So a
@@ -307,8 +309,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     if (((len - 1) >> l2bs) >= p.max_blocks_per_seq) return 0;
     return (int)((unsigned)(len - 1) / C::kStage) + 1;
   };
-  // Sums stop at 2^27 units (600 GB of reads at 128 elements): lengths that
-  // nobody meant, an error.
+  // Sums stop at kFp4MaxWork: an error then, and nothing is computed.
   const int chunk = (p.num_seqs + C::kThreads - 1) / C::kThreads;
   int total, pairs;
   {
@@ -336,10 +337,11 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     const unsigned other = lane < W ? (unsigned)warp_sums[lane] : 0u;
     const unsigned base = __reduce_add_sync(0xffffffffu, lane < warp ? other : 0u);
     const unsigned all = __reduce_add_sync(0xffffffffu, other);
+    // The warps' sum may pass 32 bits, that of their upper halves does not.
+    const bool most = __reduce_add_sync(0xffffffffu, other >> 16) >= (kFp4MaxWork >> 16);
     pre[tid] = (int)base + sum - mine;
-    if (all >= (unsigned)kFp4MaxWork && tid == 0 && blockIdx.x == 0)
-      record_error(p.err, PA_DEVERR_SEQ_LEN);
-    total = all >= (unsigned)kFp4MaxWork ? 0 : (int)all;
+    if (most && tid == 0 && blockIdx.x == 0) record_error(p.err, PA_DEVERR_SEQ_LEN);
+    total = most ? 0 : (int)all;
     pairs = __reduce_add_sync(0xffffffffu, lane < W ? warp_seqs[lane] : 0) * per_seq;
     __syncthreads();
   }

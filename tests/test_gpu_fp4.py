@@ -586,6 +586,43 @@ def test_decode_fp32_keeps_small_weights():
     assert (np.abs(host(r()) - ref) <= bound).all()
 
 
+def test_decode_takes_a_long_batch_over_shared_blocks():
+    """4.3 billion tokens, as many sequences on one prefix have them (2^27 units of work and more)."""
+    seqs, tokens, kinds = 65535, 65536, 16
+    b = Batch([tokens], 4, 1, 128, 256, seed=29)
+    b.query = rounded(np.random.default_rng(30).standard_normal((kinds, 4, 128)), "bf16")
+    b.tables, b.lens = np.repeat(b.tables, kinds, 0), np.repeat(b.lens, kinds)
+    ref, mass, total, reach = b.reference()
+    bound = decode_bound(ref, mass, total, reach, b.lens, 128, "bf16")
+    r = Run(b)
+    r.tables = r.tables[:1].expand(seqs, -1).contiguous()
+    r.lens = r.lens[:1].expand(seqs).contiguous()
+    r.query = r.query.repeat(seqs // kinds + 1, 1, 1)[:seqs].contiguous()
+    r.out = torch.full_like(r.query, 77.0)
+    got = host(r())
+    assert pa.pa_get_device_error() == 0
+    at = np.arange(seqs) % kinds
+    assert (np.abs(got - ref[at]) <= bound[at]).all()
+
+
+def test_decode_refuses_more_work_than_it_can_count():
+    # 65535 KV heads that hold one block, read 255 times by each of 65 sequences
+    heads, seqs = 65535, 65
+    cache = torch.zeros((1, heads, 32, 9 * 64), dtype=torch.uint8, device="cuda")
+    tables = torch.zeros((seqs + 1, 64), dtype=torch.int32, device="cuda")
+    lens = torch.full((seqs + 1,), 255 * 64, dtype=torch.int32, device="cuda")
+    lens[seqs] = 0
+    q = torch.ones((seqs + 1, heads, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 77.0)
+    ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(cache, heads), "cuda")
+    pa.pa_decode_fp4(out, q, cache, tables, lens, 1.0, ws)
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SEQ_LEN
+    assert not out[seqs].any()
+    lens[1:] = 0                                         # the same workspace, less work
+    pa.pa_decode_fp4(out, q, cache, tables, lens, 1.0, ws)
+    assert pa.pa_get_device_error() == 0 and not out.any()
+
+
 def test_two_graphs_share_a_workspace_and_lengths_grow():
     a = Run(Batch([70, 1, 300], 8, 2, 128, 16, seed=17))
     b = Run(Batch([9, 2000], 4, 1, 128, 16, seed=18), workspace=None)
