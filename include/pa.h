@@ -425,13 +425,15 @@ pa_status pa_decode_no_alloc(void* out, const void* query, const void* cache,
  *                 slot past the pool is skipped and records PA_DEVERR_SLOT.
  *                 Slots must be distinct (two tokens writing one slot may leave
  *                 codes of one and scales of the other).
+ * The cache must not overlap key, value or slot_mapping (PA_ERR_INVALID_ARG).
  *
  * pa_gather_cache_fp4 reads tokens back: key / value [num_tokens]
  * [num_kv_heads][head_size], contiguous, 16-byte aligned, receive the numbers
  * that the slots hold (a prompt chunk's attention over its cached prefix
  * needs them).  Rows of negative slots are left as they were, and so are rows
  * of slots past the pool, which record PA_DEVERR_SLOT.  A slot may repeat.
- * key, value and the cache must not overlap (PA_ERR_INVALID_ARG).
+ * key and value must overlap neither each other nor the cache or slot_mapping
+ * (PA_ERR_INVALID_ARG).
  * num_tokens == 0 is a no-op for both.
  * ------------------------------------------------------------------------- */
 pa_status pa_reshape_and_cache_fp4(void* cache, const pa_cache_desc* desc, const void* key,
@@ -449,8 +451,8 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
  *   out    device, [num_seqs][num_heads][head_size] of `dtype`, contiguous.
  *   query  device, [num_seqs] rows of [num_heads][head_size] of `dtype`,
  *          query_stride elements apart; pointer and stride are multiples of
- *          16 bytes, and so is `out`, which must not overlap the queries
- *          (PA_ERR_INVALID_ARG).
+ *          16 bytes, and so is `out`.  out and the workspace must overlap neither
+ *          each other nor anything that the call reads (PA_ERR_INVALID_ARG).
  * Tables, lengths, scale and their errors are pa_decode's: a length of 0
  * gives zero rows, a length past the table's row records PA_DEVERR_SEQ_LEN and
  * leaves its rows undefined, an id outside the pool records

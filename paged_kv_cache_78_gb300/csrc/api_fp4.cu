@@ -63,6 +63,20 @@ bool overlap(const Range& a, const Range& b) {
          y < x + (uint64_t)a.bytes;
 }
 
+// Whether a buffer that the call writes (they come first) overlaps another.
+template <int N>
+bool conflict(const Range (&buffers)[N]) {
+  for (int i = 0; i < N && buffers[i].written; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (overlap(buffers[i], buffers[j])) return true;
+  return false;
+}
+int64_t pool_bytes(const pa_cache_desc* d) { return d->num_blocks * pa::fp4_block_bytes(d); }
+// `n` rows of `row` elements, `stride` apart.
+int64_t rows_bytes(int64_t n, int64_t stride, int64_t row, int32_t dtype) {
+  return ((n - 1) * stride + row) * elem_bytes(dtype);
+}
+
 pa::Fp4Pool pool_of(const void* cache, const pa_cache_desc* d) {
   pa::Fp4Pool p;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
@@ -109,6 +123,11 @@ pa_status pa_reshape_and_cache_fp4(void* cache, const pa_cache_desc* desc, const
       !aligned(value, 16) || !aligned(slot_mapping, 8) || !stride_ok(key_stride, row, dtype) ||
       !stride_ok(value_stride, row, dtype) || !grid_ok(desc, num_tokens))
     return PA_ERR_INVALID_ARG;
+  const Range buffers[] = {{cache, pool_bytes(desc), true},
+                           {key, rows_bytes(num_tokens, key_stride, row, dtype), false},
+                           {value, rows_bytes(num_tokens, value_stride, row, dtype), false},
+                           {slot_mapping, num_tokens * 8ll, false}};
+  if (conflict(buffers)) return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = pa::device_state(&err, nullptr)) != PA_OK) return st;
   return cuda_status(pa::launch_fp4_write(pool_of(cache, desc), key, value, dtype, key_stride,
@@ -128,11 +147,11 @@ pa_status pa_gather_cache_fp4(void* key, void* value, int32_t dtype, const void*
   if (!cache || !key || !value || !slot_mapping || !aligned(cache, 16) || !aligned(key, 16) ||
       !aligned(value, 16) || !aligned(slot_mapping, 8) || !grid_ok(desc, num_tokens))
     return PA_ERR_INVALID_ARG;
-  const Range out[2] = {{key, num_tokens * row * elem_bytes(dtype), true},
-                        {value, num_tokens * row * elem_bytes(dtype), true}};
-  const Range pool = {cache, desc->num_blocks * pa::fp4_block_bytes(desc), false};
-  if (overlap(out[0], out[1]) || overlap(out[0], pool) || overlap(out[1], pool))
-    return PA_ERR_INVALID_ARG;
+  const Range buffers[] = {{key, num_tokens * row * elem_bytes(dtype), true},
+                           {value, num_tokens * row * elem_bytes(dtype), true},
+                           {cache, pool_bytes(desc), false},
+                           {slot_mapping, num_tokens * 8ll, false}};
+  if (conflict(buffers)) return PA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = pa::device_state(&err, nullptr)) != PA_OK) return st;
   return cuda_status(pa::launch_fp4_gather(pool_of(cache, desc), key, value, dtype, slot_mapping,
@@ -174,9 +193,14 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
       !stride_ok(query_stride, (int64_t)num_heads * desc->head_size, dtype))
     return PA_ERR_INVALID_ARG;
   const int64_t row = (int64_t)num_heads * desc->head_size;
-  if (overlap({out, num_seqs * row * elem_bytes(dtype), true},
-              {query, ((num_seqs - 1) * query_stride + row) * elem_bytes(dtype), false}))
-    return PA_ERR_INVALID_ARG;
+  // The workspace, whose size needs the device, is looked at below.
+  Range buffers[] = {{out, num_seqs * row * elem_bytes(dtype), true},
+                     {workspace, 0, true},
+                     {query, rows_bytes(num_seqs, query_stride, row, dtype), false},
+                     {cache, pool_bytes(desc), false},
+                     {block_tables, (int64_t)num_seqs * max_blocks_per_seq * 4, false},
+                     {seq_lens, num_seqs * 4ll, false}};
+  if (conflict(buffers)) return PA_ERR_INVALID_ARG;
   pa::Fp4DecodeParams p = {};
   p.scale_log2 = (float)((double)scale * key_scale * 1.4426950408889634);
   if (!std::isfinite(p.scale_log2)) return PA_ERR_INVALID_ARG;
@@ -184,7 +208,8 @@ pa_status pa_decode_fp4(void* out, const void* query, int32_t dtype, int64_t que
   if ((st = pa::device_state(&p.err, &sms)) != PA_OK) return st;
   size_t need = 0;
   if ((st = pa_decode_fp4_workspace_size(desc, num_heads, &need)) != PA_OK) return st;
-  if (workspace_bytes < need) return PA_ERR_INVALID_ARG;
+  buffers[1].bytes = (int64_t)need;
+  if (workspace_bytes < need || conflict(buffers)) return PA_ERR_INVALID_ARG;
   p.out = out;
   p.query = query;
   p.cache = static_cast<const uint8_t*>(cache);

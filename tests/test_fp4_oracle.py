@@ -294,6 +294,33 @@ def test_overlapping_buffers_are_refused():
     assert decode_call(qs=2000, out=ctypes.c_void_p((3 << 24) + 2 * 2896 - 16)) == pa.PA_ERR_INVALID_ARG
 
 
+def test_writes_that_overlap_what_is_read_are_refused():
+    """First and last elements of one buffer on the last and first of another."""
+    row, pool, slots = 4 * 256, 16 * 2 * 2 * 9 * 64, 4 * 8
+    at = ctypes.c_void_p
+    for name, size, step in (("key", row, 16), ("value", row, 16), ("slots", slots, 8)):
+        for x in ((1 << 24) - size + step, 1 << 24, (1 << 24) + pool - 16):
+            assert write_call(**{name: at(x)}) == pa.PA_ERR_INVALID_ARG, name
+    # rows 2000 elements apart reach into the cache with their last one
+    assert write_call(ks=2000, key=at((1 << 24) - 2 * (3 * 2000 + 128) + 16)) == pa.PA_ERR_INVALID_ARG
+    for out in (2, 3):
+        for x in ((out << 24) - slots + 8, out << 24, (out << 24) + row - 8):
+            assert gather_call(slots=at(x)) == pa.PA_ERR_INVALID_ARG
+    # two rows of 14 heads of 64, tables of two rows of four, two lengths
+    def decode(**kw):
+        g = lambda name, i: kw.get(name, far(i))
+        return pa.lib.pa_decode_fp4(g("out", 2), g("query", 3), pa.PA_BF16, 14 * 64, g("cache", 1),
+                                    ctypes.byref(desc()), 1.0, 1.0, g("tables", 4), 4, g("lens", 5), 2,
+                                    14, 0.125, g("ws", 64), 1 << 30, None)
+    size = 2 * 14 * 64 * 2
+    for name, i, other, step in (("cache", 1, pool, 16), ("tables", 4, 32, 4), ("lens", 5, 8, 4)):
+        for x in ((2 << 24) - other + step, 2 << 24, (2 << 24) + size - step):
+            if name != "cache" or x % 16 == 0:
+                assert decode(**{name: at(x)}) == pa.PA_ERR_INVALID_ARG, name
+        for x in ((i << 24) - size + 16, (i << 24) + (other - 4) // 16 * 16):
+            assert decode(out=at(x)) == pa.PA_ERR_INVALID_ARG, name
+
+
 def test_python_refusals():
     c = torch.zeros((4, 2, 2, 9 * 64), dtype=torch.uint8)
     d = pa.fp4_cache_desc(c)

@@ -670,6 +670,24 @@ def test_decode_refuses_small_workspaces():
     assert e.value.status == pa.PA_ERR_INVALID_ARG
 
 
+def test_decode_refuses_buffers_in_its_workspace():
+    r = Run(Batch([40], 4, 2, 64, 16))
+    need = pa.pa_decode_fp4_workspace_size(r.cache, 4)
+    arena = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    r.ws = arena[:need]
+    at = (need + 15) // 16 * 16
+    for name in ("out", "query", "cache", "tables", "lens"):
+        was = getattr(r, name)
+        inside = arena[at - 16:at - 16 + was.nbytes] if name != "cache" else arena[:was.nbytes]
+        setattr(r, name, inside.view(was.dtype).view(was.shape))
+        with pytest.raises(pa.PAError) as e:
+            r()
+        assert e.value.status == pa.PA_ERR_INVALID_ARG, name
+        setattr(r, name, was)
+    r.out = arena[at:at + r.out.nbytes].view(r.out.dtype).view(r.out.shape)
+    assert_decode(r(), r.batch)
+
+
 def test_decode_waits_that_give_up_leave_the_workspace_usable():
     # A limit of one cycle, and more to read than L2 holds, so that most waits
     # for a copy find it not yet there and give up.
