@@ -192,6 +192,32 @@ def test_write_takes_rows_of_a_fused_projection():
         pa.pa_reshape_and_cache_fp4(a, qkv[:, 1:129].unflatten(1, (2, 64)), v, slots)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("head,hkv", [(64, 3), (128, 2), (256, 1)])
+def test_write_and_gather_rows_off_32_byte_boundaries(dtype, head, hkv):
+    """Rows that start 16 bytes into an allocation, and strides and outputs likewise."""
+    rng = np.random.default_rng(head)
+    n, half = 37, 8 if dtype == "bf16" else 4                  # elements of 16 bytes
+    slots = rng.permutation(48)[:n].astype(np.int64)
+    for off, odd in ((half, 0), (0, half), (half, half)):
+        stride = hkv * head + odd
+        kv = [dev(rounded(rng.standard_normal(n * stride + half), dtype)) for _ in range(2)]
+        key, value = (x.as_strided((n, hkv, head), (stride, head, 1), off) for x in kv)
+        cache = torch.zeros((3, hkv, 2, 9 * head), dtype=torch.uint8, device="cuda")
+        pa.pa_reshape_and_cache_fp4(cache, key, value, dev(slots), 0.5, 2.0)
+        k, v = fp4.read(cache.cpu().numpy(), slots, 0.5, 2.0)
+        assert same(k, fp4.dequantise(*fp4.quantise(host(key), 0.5), 0.5))
+        assert same(v, fp4.dequantise(*fp4.quantise(host(value), 2.0), 2.0))
+        size = n * hkv * head
+        for at, bt in ((half, half), (0, half), (half, 0)):    # one of the outputs, or both
+            flat = torch.full((2, size + 2 * half), 7.0, dtype=TORCH[dtype], device="cuda")
+            ko, vo = flat[0, at:at + size], flat[1, bt:bt + size]
+            pa.pa_gather_cache_fp4(ko.view(n, hkv, head), vo.view(n, hkv, head), cache, dev(slots), 0.5, 2.0)
+            assert same(host(ko).reshape(k.shape), k) and same(host(vo).reshape(v.shape), v)
+            for row, x in ((flat[0], at), (flat[1], bt)):
+                assert (row[:x] == 7).all() and (row[x + size:] == 7).all()
+
+
 def test_no_tokens():
     c = pa.alloc_fp4_cache(2, 8, 2, 64)
     k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
