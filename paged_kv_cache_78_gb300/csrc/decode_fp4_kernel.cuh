@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
                          : "memory");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        __syncwarp();  // other lanes read the zeros, which no barrier announces
       }
       ++issued;
     };

@@ -444,6 +444,23 @@ def test_decode_block_ids_outside_the_pool_count_as_zeros():
         assert np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("head,heads", [(64, 4), (128, 8)])
+def test_decode_bad_ids_among_the_last_stages(head, heads):
+    """Zeros that lanes write themselves, in stages that no later copy follows."""
+    tokens, shape = 500, dict(heads=heads, kv_heads=1, head=head, block=8, seed=32)
+    r = Run(Batch([tokens], **shape))
+    for bad in [(60,), (61, 62), (50, 56), tuple(range(40, 63)), tuple(range(0, 63, 3))]:
+        z = Batch([tokens], **shape)
+        for i in bad:
+            fp4.write(z.cache, np.zeros((8, 1, head)), np.zeros((8, 1, head)),
+                      z.tables[0, i].astype(np.int64) * 8 + np.arange(8))
+        r.tables = dev(z.tables)
+        r.tables[0, list(bad)] = -1
+        for _ in range(3):
+            assert_decode(r(), z, bad)
+        assert pa.pa_get_device_error() == pa.PA_DEVERR_BLOCK_ID
+
+
 def test_decode_rows_behind_the_batch_stay():
     b = Batch([30, 0, 70], 4, 2, 64, 16, seed=14)
     r = Run(b)
