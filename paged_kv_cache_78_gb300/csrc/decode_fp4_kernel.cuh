@@ -65,8 +65,8 @@ constexpr int kFp4RingBytes = 216 * 1024;
 // second and more; sequences may share blocks), so that two sums of them fit an int.
 constexpr int kFp4MaxWork = (1 << 30) - 1;
 // Tokens of a chain of sums.  Sums over more lose what is small beside them: the matrix
-// unit cuts off, and rounded additions drop whatever is below half a step (pairs of a
-// million tokens that a warp sees whole: bf16 1e-2 of the result, fp32 2.8e-4).  So a
+// unit cuts off, and rounded additions drop whatever is below half a step (a warp
+// that sees a million tokens of a pair: bf16 1e-2 of the result, fp32 2.8e-4).  So a
 // chain's sums are added, with rounding, to the piece's in global memory: fp32 outputs are
 // then off by 1e-6 to 1.5e-6 up to 131072 tokens of a warp and 6e-6 at a million, bf16 ones
 // by 4e-5 before their rounding.  At one in 128 stages it costs nothing; its code costs
@@ -75,6 +75,7 @@ constexpr int kFp4Chain = 4096;
 // A pair's queries and its end count as this many stages (32 sequences of 40 pairs
 // each: 52 us at 0, 43 at 1, 44 at 2).
 constexpr int kFp4PairCost = 1;
+constexpr int kFp4Whole = 512;  // tokens of a pair that may stay whole with a warp (see there)
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -380,8 +381,12 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   // Ends of CTAs' and warps' parts that would cut a short pair move behind it: the
   // pair stays whole with the warp (or, of several warps, the CTA) of its first unit,
   // and nothing is left to merge, which takes a CTA 6 us where every warp cuts one.
-  // Short is a pair of no more stages than a warp's part has (256 sequences of 128
-  // tokens 29.2 -> 19.5 us, 1024 of up to 200, with parts less equal then, 48 -> 46).
+  // Short is a pair of no more stages than a warp's part has, and of kFp4Whole tokens at
+  // most: whole pairs leave the warps less even, by up to a pair, which is little beside a
+  // merge only while pairs are short (32 heads on 8 of 128: 256 sequences of 128 tokens
+  // 29.4 -> 20.6 us, 512 of 300, 64 heads, 60.3 -> 52.3, 1024 of up to 300 60.3 -> 57.5; but
+  // 512 of up to 500 49.3 -> 53.4, of up to 1000 73.8 and 92.7 without the bound, 384 of
+  // 1500 125 and 169).
   // For a CTA whose share is at most a step per warp it is a pair of up to that: latency
   // is what counts there, and a merge over CTAs costs more than the stages that it
   // spares (64 sequences of up to 500 tokens 12.4 -> 10.4 us, four of up to 100 9.7 ->
@@ -395,7 +400,8 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
     return total <= (long long)pairs * (stages + kFp4PairCost);
   };
   const bool few = share <= C::kWholeStages && short_of(C::kWholeStages);
-  const int whole_w = !few && short_of(per_warp) ? per_warp : 0;
+  const int most_w = min(per_warp, kFp4Whole / C::kStage);
+  const int whole_w = !few && short_of(most_w) ? most_w : 0;
   const int whole_cta = few ? C::kWholeStages : whole_w;
   int share_w = 0, my0 = 0, my1 = 0;
   Fp4Place pp = {};  // the next stage to copy

@@ -519,6 +519,17 @@ def test_decode_short_sequences_beside_long_ones(head, heads, hkv, most, long):
     assert_decode(r(), r.batch)
 
 
+@pytest.mark.parametrize("head,heads,hkv", [(64, 8, 8), (128, 4, 4), (256, 5, 5)])
+@pytest.mark.parametrize("longest", [510, 530, 1100])
+def test_decode_pairs_about_as_long_as_may_stay_whole(head, heads, hkv, longest):
+    rng = np.random.default_rng(longest + head)
+    lens = rng.choice([1, 60, 480, 511, 512, 513, longest], 700, p=[.3, .3, .08, .08, .08, .08, .08])
+    b = Batch([max(lens)], heads, hkv, head, 16, seed=head + longest)
+    b.tables, b.lens = b.tables.repeat(len(lens), 0), lens.astype(np.int32)
+    b.query = rounded(rng.standard_normal((len(lens), heads, head)), "bf16")
+    assert_decode(Run(b)(), b)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_decode_sequences_that_share_blocks_and_repeated_calls(dtype):
     """Rows of one table several times over, and calls that agree bit for bit
@@ -554,7 +565,7 @@ def test_decode_fp32_sums_are_rounded_not_cut_off():
 @pytest.mark.parametrize("dtype,head,heads", [("bf16", 128, 4), ("bf16", 128, 8), ("bf16", 64, 16), ("bf16", 256, 8),
                                               ("fp32", 128, 4), ("fp32", 64, 8), ("fp32", 256, 8)])
 def test_decode_sums_do_not_drift_with_the_length(dtype, head, heads):
-    """Pairs of a million tokens that a warp sees whole.  Every value of an element is
+    """Pairs of a million tokens, as many as warps, so that each sees about as much of one.  Every value of an element is
     the same, so that the output is that value whatever the weights are.  Off are the
     weights' roundings (bf16 2^-11, fp32 2^-22 at most), the output's (2^-8, 2^-24) and two
     sums.  bf16: chains of 2^12 tokens, 2^9 additions that may cut off 2^-23 each.  fp32:
@@ -585,7 +596,7 @@ def test_decode_sums_do_not_drift_with_the_length(dtype, head, heads):
 @pytest.mark.parametrize("head,heads", [(64, 4), (64, 16), (128, 3), (128, 8), (128, 16), (256, 4), (256, 11)])
 @pytest.mark.parametrize("rise", [0.0, 120.0, -120.0])
 def test_decode_long_sequences_in_a_warp(dtype, head, heads, rise):
-    """Pairs of several chains of 4096 tokens and a token, whole with a warp, whose scores
+    """Pairs of several chains of 4096 tokens and a token, more than warps, whose scores
     stay, rise (the maximum moves again and again) or fall."""
     seqs, lens = 3000, [12289, 20001, 4096, 4097]
     b = Batch([20001], heads, 1, head, 64, dtype, seed=head + heads)
@@ -606,7 +617,7 @@ def test_decode_long_sequences_in_a_warp(dtype, head, heads, rise):
 
 
 def test_decode_fp32_keeps_small_weights():
-    """One token far above all others, in a warp that sees the whole sequence: the others'
+    """One token far above all others, in warps that see whole sequences: the others'
     weights are 2^-34 to 2^-33 of its, and its value is zero.  Weights are kept in steps of
     2^-24 where the largest is 2^11 at least, so each is off by half a step, 2^-36 of the
     largest, at most; relative errors of what is kept are as in decode_bound."""
