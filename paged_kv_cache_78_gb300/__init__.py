@@ -228,7 +228,7 @@ def fp4_cache_desc(cache: torch.Tensor) -> CacheDesc:
 def alloc_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
                     device="cuda") -> torch.Tensor:
     """A zeroed 4-bit pool (every key and value zero)."""
-    if block_size < 8 or block_size % 8:
+    if not 8 <= block_size <= 256 or block_size & (block_size - 1):
         raise ValueError("a 4-bit cache's block_size is a power of two in [8, 256]")
     return torch.zeros((num_blocks, num_kv_heads, block_size // 8, 9 * head_size),
                        dtype=torch.uint8, device=device)

@@ -358,6 +358,12 @@ def test_python_refusals():
         pa.pa_extend_tables(t, n, n, 16, 4, s)           # host tensors
 
 
+@pytest.mark.parametrize("block", [-16, 0, 7, 12, 24, 512])
+def test_pools_that_no_call_takes_are_not_allocated(block):
+    with pytest.raises(ValueError):
+        pa.alloc_fp4_cache(4, block, 2, 64, device="cpu")
+
+
 def test_workspace_size_refusals():
     out = ctypes.c_size_t()
     call = lambda d, h: pa.lib.pa_decode_fp4_workspace_size(ctypes.byref(d), h, ctypes.byref(out))
