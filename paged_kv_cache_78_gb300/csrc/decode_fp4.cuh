@@ -23,9 +23,9 @@ constexpr int kFp4HeaderBytes = kFp4MaxCtas * 3 * kFp4Units * 4;  // three count
 // Query heads of a unit of work (columns of the matrix instructions): 4, 8, or
 // 16 where the registers hold them; groups past eight heads of 256 elements read
 // the keys and values once per eight heads.  Up to four heads use the eight columns
-// twice (8 x 32768 tokens, heads of 128: 59 us, 64 us as eight heads; fp32 87 and 92;
-// a decode step of 128 sequences 74 and 78).  Sixteen heads of 128 take 98 us where
-// eight take 66, so twice eight would take 132 (fp32 136 and 180; of 64, 61 and 94).
+// twice (8 x 32768 tokens, heads of 128: 59 us, 63 us as eight heads; fp32 88 and 90;
+// a decode step of 128 sequences 74 and 78).  Sixteen heads of 128 take 99 us where
+// eight take 65, so twice eight would take 130 (fp32 142 and 185; of 64, 59 and 90).
 __host__ __device__ constexpr int fp4_heads(int head_size, int group) {
   return group <= 4 ? 4 : group <= 8 || head_size == 256 ? 8 : 16;
 }
@@ -34,9 +34,10 @@ __host__ __device__ constexpr int fp4_heads(int head_size, int group) {
 // weight fragments leave room in 128 registers, else 8.  Left of the bound 16 warps hide
 // each other's waits (8 x 32768 tokens, four heads of 128: 59 us, 74 us with 8 warps;
 // sixteen heads of 64: 58 and 67, although a few registers spill), right of it what
-// spills is read again in every step (four heads of 128, fp32: 87 us, 83 to 137 with 16,
-// by where the compiler spills; eight: 92 and 170; sixteen, bf16: 98 and 174; at 256 the
-// rings would not fit).
+// spills is read again in every step (four heads of 128, fp32: 88 us, 83 to 137 with 16,
+// by where the compiler spills; eight: 92 and 170; sixteen, bf16: 99 and 174; at 256 the
+// rings would not fit).  With 8 warps sixteen heads of 128 and eight of 256 spill in fp32,
+// 40 and 16 bytes a thread.
 __host__ __device__ constexpr int fp4_warps(int head_size, int heads, bool fp32) {
   const int parts = fp32 ? 2 : 1;
   const int accumulators = heads == 4 ? head_size / 8 : head_size / 32 * heads;

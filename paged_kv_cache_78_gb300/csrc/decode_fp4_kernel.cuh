@@ -29,12 +29,13 @@
 //
 // Measured (graph replays in a row, data larger than L2, 6766 GB/s = 100%):
 //   8 x 32768 tokens, 32 heads on 8 of 128, bf16   59 us  302 MB  5.1 TB/s  75%
-//   the same with 64 heads on 8                    66 us                    68%
+//   the same with 64 heads on 8                    65 us                    69%
 //   the same with 64 heads on 8 of 64              45 us  151 MB            50%
-//   8 x 32768 tokens, 64 heads on 8 of 128, fp32   90 us  302 MB            50%
-//   32 sequences of 1 .. 2048 tokens, 40 heads     43 us  181 MB            62%
+//   8 x 32768 tokens, 64 heads on 8 of 128, fp32   92 us  302 MB            48%
+//   32 sequences of 1 .. 2048 tokens, 40 heads     44 us  181 MB            61%
+//   384 sequences of 1500 tokens, 32 heads on 8   125 us  670 MB            79%
 //   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  14.5 us
-//   four sequences of up to 100 tokens              8.3 us
+//   four sequences of up to 100 tokens               10 us
 // Of the long batch reading alone takes 57 us and the arithmetic alone 55; the
 // launch, the lengths and the first copies take 5 to 6 us, and merges over CTAs 4,
 // and these are what is left of the short ones.  Heads of 64 pay a step's fixed
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(Fp4Config<T, D, H>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.group;
-  const int head_tiles = D == 256 ? (G + 7) / 8 : 1;  // of a KV head (see fp4_head_tiles)
+  const int head_tiles = D == 256 ? (G + 7) / 8 : 1;  // units of a KV head (see fp4_heads)
   const int rows = fp4_unit_rows(H, G);
   const int per_seq = p.num_kv_heads * head_tiles;  // pairs of a sequence
   const int l2bs = p.log2_block_size;
