@@ -559,6 +559,11 @@ def _rows(t: torch.Tensor, name: str, heads: int, head_size: int, dev: int):
     return t.data_ptr(), (row if n > 1 else heads * head_size)
 
 
+def _too_large(n) -> ValueError:
+    """For sizes that ctypes would cut to 32 bits."""
+    return ValueError("%d is past 2^31 - 1" % n)
+
+
 def _on(stream, dev: int) -> int:
     return _cuda_raw_stream(dev) if stream is None else _stream(stream)
 
@@ -637,6 +642,8 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
     tables = block_tables.shape
     if len(tables) != 2 or tables[0] != s or seq_lens.shape != (s,):
         raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
+    if tables[1] > 0x7FFFFFFF:
+        raise _too_large(tables[1])
     dev = _current_device(cache, "cache")
     qp, qs = _rows(query, "query", hq, d, dev)
     _check(lib.pa_decode_fp4(_arg(out, "out", query.dtype, dev), qp, _dtype_code(query), qs,
@@ -675,6 +682,10 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
         raise ValueError("free_blocks and free_state go together")
     if free_state_out is not None and free_state is None:
         raise ValueError("free_state_out needs free_state")
+    largest = max(tables[1], most[0], block_size, num_blocks,
+                  0 if free_blocks is None else free_blocks.shape[0])
+    if largest > 0x7FFFFFFF:
+        raise _too_large(largest)
     dev = _current_device(block_tables, "block_tables")
     i32 = torch.int32
     lens = lens_out = _arg(seq_lens, "seq_lens", i32, dev)

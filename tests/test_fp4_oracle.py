@@ -358,6 +358,23 @@ def test_python_refusals():
         pa.pa_extend_tables(t, n, n, 16, 4, s)           # host tensors
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Not cut to 32 bits, where they could pass for small ones."""
+    meta = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="meta")
+    big = (1 << 32) + 8
+    lens, slots = meta(1), meta(8, dtype=torch.int64)
+    for kw in (dict(tables=meta(1, big)), dict(slots=meta(big, dtype=torch.int64)), dict(blocks=big),
+               dict(size=big), dict(ring=meta(big))):
+        ring = kw.get("ring")
+        with pytest.raises(ValueError, match="past 2"):
+            pa.pa_extend_tables(kw.get("tables", meta(1, 4)), lens, lens, kw.get("size", 16),
+                                kw.get("blocks", 9), kw.get("slots", slots), free_blocks=ring,
+                                free_state=None if ring is None else meta(2))
+    q = meta(1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="past 2"):
+        pa.pa_decode_fp4(q, q, meta(4, 2, 2, 9 * 64, dtype=torch.uint8), meta(1, big), lens, 1.0, slots)
+
+
 @pytest.mark.parametrize("block", [-16, 0, 7, 12, 24, 512])
 def test_pools_that_no_call_takes_are_not_allocated(block):
     with pytest.raises(ValueError):
