@@ -1000,6 +1000,63 @@ def test_captured_step_serves_growing_sequences(dtype, heads, hkv, head, block):
     assert host(state)[1] == pool.num_free() and pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_prompt_steps_in_a_row_see_what_the_step_before_wrote(in_place):
+    """Steps of thousands of tokens (tables by several CTAs) captured one behind another, so
+    that each launch starts while the ones before still run; every step's tables, slots and
+    attention."""
+    rng = np.random.default_rng(33)
+    n, steps, most, block, blocks, width = 24, 6, 5000, 8, 4000, 320
+    heads, hkv, head = 4, 1, 64
+    i32 = lambda a: dev(np.asarray(a, dtype=np.int32))
+    new = rng.integers(0, 400, (steps, n))
+    new[:, ::5] = 1
+    ring = rng.permutation(blocks)
+    cache = torch.randint(0, 256, (blocks, hkv, 1, 9 * head), dtype=torch.uint8, device="cuda")
+    first = cache.cpu().numpy().copy()
+    k, v = (dev(rounded(rng.standard_normal((steps, most, hkv, head)), "bf16")) for _ in range(2))
+    q = dev(rounded(rng.standard_normal((steps, n, heads, head)), "bf16"))
+    out = torch.empty_like(q)
+    tables = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    lens = [torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(steps + 1)]
+    state = [i32([7, blocks]) for _ in range(steps + 1)]
+    slots = torch.empty((steps, most), dtype=torch.int64, device="cuda")
+    free, news = i32(ring), i32(new)
+    ws = pa.alloc_workspace(pa.pa_decode_fp4_workspace_size(cache, heads), "cuda")
+    at = lambda i: 0 if in_place else i
+
+    def run():
+        for i in range(steps):
+            pa.pa_extend_tables(tables, lens[at(i)], news[i], block, blocks, slots[i], free_blocks=free,
+                                free_state=state[at(i)], seq_lens_out=lens[at(i + 1)],
+                                free_state_out=state[at(i + 1)])
+            pa.pa_reshape_and_cache_fp4(cache, k[i], v[i], slots[i])
+            pa.pa_decode_fp4(out[i], q[i], cache, tables, lens[at(i + 1)], head ** -0.5, ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    ref, t, ln, st = first.copy(), np.full((n, width), -1), np.zeros(n, int), [7, blocks]
+    want = []
+    b = Batch([1], heads, hkv, head, block)  # a shell for the bound
+    for i in range(steps):
+        t, ln, st, sl, _, _, refused = fp4.extend_tables(t, ln, new[i], block, blocks, most, ring, st)
+        assert not refused
+        fp4.write(ref, host(k[i]), host(v[i]), sl)
+        r = fp4.decode(host(q[i]), ref, t, ln, b.scale)
+        want.append((sl, r[0], decode_bound(*r, ln, head, "bf16")))
+    for _ in range(5):
+        cache.copy_(dev(first)), tables.fill_(-1), lens[0].zero_(), state[0].copy_(i32([7, blocks]))
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (sl, r, bound) in enumerate(want):
+            assert np.array_equal(host(slots[i]), sl), i
+            assert (np.abs(host(out[i]) - r) <= bound).all(), i
+        assert np.array_equal(host(lens[at(steps)]), ln) and host(state[at(steps)]).tolist() == list(st)
+        assert np.array_equal(host(tables), t)
+    assert pa.pa_get_device_error() == 0
+
+
 FIRST_CALLS = """
 import torch
 import paged_kv_cache_78_gb300 as pa
