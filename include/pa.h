@@ -56,7 +56,8 @@ typedef enum pa_status {
 typedef enum pa_dtype {
   PA_BF16 = 0,
   PA_FP32 = 1,
-  PA_FP4 = 2 /* a 4-bit pool: only for the pa_*_fp4 calls and the block copies */
+  PA_FP4 = 2, /* a 4-bit pool: only for the pa_*_fp4 calls and the block copies */
+  PA_INT8 = 3 /* an 8-bit pool: only for the pa_*_int8 calls and the block copies */
 } pa_dtype;
 
 /* Bits of the device error word. */
@@ -64,7 +65,9 @@ typedef enum pa_dtype {
 #define PA_DEVERR_BLOCK_ID 0x2u    /* decode / copy_blocks: block id outside [0, num_blocks) */
 #define PA_DEVERR_SEQ_LEN 0x4u     /* decode: seq_len > max_seq_len or > table capacity */
 #define PA_DEVERR_TIMEOUT 0x8u     /* a pipeline wait exceeded its limit (about 2 s by default) */
-#define PA_DEVERR_BLOCKS 0x10u     /* extend_tables: the free list holds fewer blocks than needed */
+#define PA_DEVERR_BLOCKS 0x10u     /* extend_tables: the free list holds fewer blocks than needed;
+                                      evict_blocks: it has no room for the blocks that leave */
+#define PA_DEVERR_POSITION 0x20u   /* norm_rope: a position past the table */
 
 /* partition_size of pa_decode: the stage-balanced split (see pa_decode). */
 #define PA_PARTITION_BALANCED (-2)
@@ -76,7 +79,7 @@ typedef struct pa_cache_desc {
   int32_t num_kv_heads;  /* KV heads, >= 1 */
   int32_t head_size;     /* elements per head: 64, 128 or 256 */
   int32_t dtype;         /* pa_dtype */
-} pa_cache_desc;             /* PA_FP4: block_size a power of two in [8, 256] */
+} pa_cache_desc;             /* PA_FP4, PA_INT8: block_size a power of two in [8, 256] */
 
 /* ---------------------------------------------------------------------------
  * Cache write.  Each new token's key and value go to the physical slot that
@@ -532,6 +535,180 @@ pa_status pa_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
                            int32_t* seq_lens_out, int32_t* free_state_out, int64_t* slot_mapping,
                            int32_t* positions, int32_t* token_starts, int32_t max_tokens,
                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit pool (pa_cache_desc.dtype = PA_INT8): 1.98 times the tokens of a bf16
+ * pool of heads of 128 in the same memory (studying-code.tistory.com/16 sizes the pool
+ * by its bytes; the pages store 16-bit caches).
+ *
+ * A key or value is held as a code in [-127, 127], and the keys and the values of a
+ * block of tokens have, for every KV head, a scale each: x = code * scale.  The buffer is
+ *     cache[num_blocks][num_kv_heads][block_size / 8][16 * (head_size + 1)] bytes,
+ * 16-byte aligned; its last axis is a tile of eight tokens (D = head_size):
+ *     fp32, fp32, 8 bytes         key scale, value scale (of the block and head: every
+ *                                 tile of a block repeats them), zeros
+ *     [D / 16][8 tokens][16]      key codes plus 128, by groups of 16 elements
+ *     [D / 16][8 tokens][16]      value codes plus 128
+ * Zeroed bytes are a pool of zeros.  Slots, block tables and the host pool are those of
+ * the other pools; pa_copy_blocks and pa_swap_blocks take 8-bit pools as well.
+ * head_size is 64, 128 or 256 (else PA_ERR_UNSUPPORTED).  `dtype` of a call is the
+ * element type (PA_BF16 or PA_FP32) of its keys, values, queries and outputs.
+ *
+ * pa_reshape_and_cache_int8 writes new tokens, block by block.  Of the tokens that the
+ * call puts into a block, and for each head, keys and values by themselves:
+ *     most  = max |x| / 127, rounded to fp32,
+ *     scale = most, if a token goes to the block's first slot (the block begins: what it
+ *             held is dropped); else the larger of `most` and the block's scale,
+ *     code  = x / scale, the nearest whole number, ties to even (decided on the exact
+ *             quotient).
+ * Where the scale of a block that goes on grows, the codes that it holds are rounded
+ * again, code * old scale / scale, the same way.  A NaN or an infinity makes the scale
+ * NaN, and with it all of the block's keys (or values) of that head, until the block
+ * begins anew.  A maximum below 2^-143 may become zero.
+ *   key, value    device, [num_tokens] rows of [num_kv_heads][head_size] elements,
+ *                 key_stride / value_stride elements apart; pointers and strides are
+ *                 multiples of 16 bytes.
+ *   slot_mapping  as in pa_reshape_and_cache: negative slots are padding, a slot past
+ *                 the pool is skipped and records PA_DEVERR_SLOT.  Slots must be
+ *                 distinct, and a block's tokens neighbours in the call, with no
+ *                 padding between them (in any order), as pa_extend_tables, pa_pool_*
+ *                 and pa_slot_mapping give them: tokens of one block in two places of a
+ *                 call leave that block's numbers undefined.  Blocks fill from their first
+ *                 slot on, as the pool hands slots out.
+ * The cache must not overlap key, value or slot_mapping (PA_ERR_INVALID_ARG).
+ *
+ * pa_gather_cache_int8 reads tokens back: code * scale, rounded to `dtype`.  Its
+ * arguments and refusals are pa_gather_cache_fp4's.
+ * num_tokens == 0 is a no-op for both.
+ * ------------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_int8(void* cache, const pa_cache_desc* desc, const void* key,
+                                    const void* value, int32_t dtype, int64_t key_stride,
+                                    int64_t value_stride, const int64_t* slot_mapping,
+                                    int32_t num_tokens, void* stream);
+pa_status pa_gather_cache_int8(void* key, void* value, int32_t dtype, const void* cache,
+                               const pa_cache_desc* desc, const int64_t* slot_mapping,
+                               int32_t num_tokens, void* stream);
+
+/* Decode attention over an 8-bit pool: pa_decode's operation on the numbers that the
+ * pool holds.  out, query, tables, lengths, scale, groups (<= 16), the limit on the work
+ * and the errors are pa_decode_fp4's, and so is what a captured call may rely on: the
+ * launches depend on the shapes alone.  Queries and weights of the values enter their
+ * products as in pa_decode_fp4, codes exactly; a weight is off by up to 2^-32 (fp32
+ * outputs: 2^-36) of the largest, in units of the sequence's largest value scale.
+ *
+ * The attention that each block of a sequence gets can be added up over the steps, for
+ * pa_evict_blocks:
+ *     block_weights_out[s][b] = decay * block_weights[s][b]
+ *                               + sum over query heads and tokens j of block b of softmax_j
+ * for the blocks b of sequence s (b < ceil(seq_lens[s] / block_size)); what lies behind
+ * stays as it was.  Sums are fp32, in a fixed order.
+ *   block_weights_out  device fp32 [num_seqs][max_blocks_per_seq], laid out as the tables;
+ *                      NULL: no weights are kept.
+ *   block_weights      likewise, the weights before the step; the same buffer (in place) or
+ *                      other memory; NULL: zeros.
+ *   decay              finite.
+ *   workspace          as for pa_decode_fp4, of pa_decode_int8_workspace_size bytes:
+ *                      num_seqs and max_blocks_per_seq are those of the largest call that
+ *                      keeps weights (8 bytes for every 16 tokens, or block of 8, and query
+ *                      head of such a table), 0 if none does.
+ * out, block_weights_out and the workspace must overlap neither each other nor anything
+ * that the call reads, but for weights in place (PA_ERR_INVALID_ARG).  A sequence that
+ * is recorded as PA_DEVERR_SEQ_LEN keeps the weights that it has in block_weights_out. */
+pa_status pa_decode_int8_workspace_size(const pa_cache_desc* desc, int32_t num_heads,
+                                        int32_t num_seqs, int32_t max_blocks_per_seq,
+                                        size_t* bytes);
+pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t query_stride,
+                         const void* cache, const pa_cache_desc* desc,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* seq_lens, int32_t num_seqs, int32_t num_heads,
+                         float scale, const float* block_weights, float* block_weights_out,
+                         float decay, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: a sequence of more than max_blocks blocks
+ * gives up the blocks that got the least attention, whole (no key or value moves;
+ * studying-code.tistory.com/16, section "요청 완료 후 메모리 관리": blocks are what the pool
+ * takes back).  With n = ceil(seq_lens[s] / block_size), the n - max_blocks blocks of
+ * least block_weights[s][b] leave, ties the lowest b first, among keep_first <= b < n -
+ * keep_last.  Weights order as numbers, -0 with 0, NaNs above all.  Then
+ *     row s of the tables      the blocks that stay, in their order, then those that
+ *                              leave, in theirs (n entries; the others stay as they were)
+ *     row s of the weights     those of the blocks that stay, then zeros (n entries)
+ *     seq_lens[s]              less block_size for each block that left
+ *     evicted_tokens[s]        more by as much, so that a token's position is its place
+ *                              in the sequence plus evicted_tokens[s] (pa_norm_rope's
+ *                              position_offsets)
+ *     the ring of free blocks  (pa_extend_tables) at its end: the blocks that left,
+ *                              sequence after sequence
+ * The blocks must not be shared with other sequences.
+ *   block_tables, block_weights   device int32 / fp32 [num_seqs][max_blocks_per_seq].
+ *   max_blocks   >= keep_first + keep_last; keep_first >= 0; keep_last >= 1 (the last
+ *                block, which may be partly filled, always stays).
+ *   free_blocks, free_capacity, free_state   the ring; free_blocks is written.  All NULL / 0: the
+ *                host finds the blocks that left in the tables.
+ *   evicted_tokens   device int32 [num_seqs], or NULL with evicted_tokens_out.
+ *   ..._out      the state after the call; each may be its input (in place), or other
+ *                memory (of which the same entries are written).
+ * All or nothing: a negative length or one past its row records PA_DEVERR_SEQ_LEN, a ring
+ * without room (or a bad state) PA_DEVERR_BLOCKS, and the call then changes nothing: what
+ * it would write becomes what it read.  num_seqs is at most PA_MAX_TABLE_REQUESTS,
+ * max_blocks_per_seq at most PA_MAX_EVICT_BLOCKS (else PA_ERR_INVALID_ARG).  Two buffers of
+ * which one is written must not overlap, apart from those that may be in place
+ * (PA_ERR_INVALID_ARG).  Two launches, which depend on the shapes alone. */
+#define PA_MAX_EVICT_BLOCKS 49152
+pa_status pa_evict_blocks(const int32_t* block_tables, const float* block_weights,
+                          int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                          int32_t block_size, int32_t max_blocks, int32_t keep_first,
+                          int32_t keep_last, int32_t* free_blocks, int32_t free_capacity,
+                          const int32_t* free_state, const int32_t* evicted_tokens,
+                          int32_t* block_tables_out, float* block_weights_out,
+                          int32_t* seq_lens_out, int32_t* free_state_out,
+                          int32_t* evicted_tokens_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys for each head, and the rotation by position, in one pass: what
+ * comes between a model's projection and the cache write (the pages start from rotated
+ * keys; studying-code.tistory.com/16, section "디코딩 과정").  For every token's head x
+ * (head_size elements), its weight w and the token's position p,
+ *     y = x / sqrt(mean(x^2) + eps) * w,
+ *     out_i = y_i c_i - y_j s_i,  out_j = y_j c_i + y_i s_i   for the pairs (i, j),
+ * c_i = cos_sin[p][i], s_i = cos_sin[p][rotary_dim / 2 + i], i < rotary_dim / 2: with
+ * j = i + rotary_dim / 2, or, interleaved, the elements 2 i and 2 i + 1.  Elements from
+ * rotary_dim on are y.  Arithmetic is fp32, rounded once at the end.
+ *   query, key          device, [num_tokens] rows of [num_heads] (num_kv_heads) [head_size]
+ *                       elements of `dtype` (PA_BF16 or PA_FP32), query_stride / key_stride
+ *                       elements apart (slices of a fused projection's output, say).
+ *   query_out, key_out  likewise; each may be its input (in place, the same stride).
+ *                       Pointers and strides are multiples of 16 bytes.
+ *   query_weight, key_weight  device [head_size] of `dtype`, 16-byte aligned; NULL: ones.
+ *   eps                 finite, >= 0.
+ *   cos_sin             device fp32 [max_position][rotary_dim], 16-byte aligned: the cosines, then
+ *                       the sines, of a position's angles (of whatever scaling the model has).
+ *   rotary_dim          a multiple of 16 up to head_size; 0: no rotation (cos_sin NULL).
+ *   positions           device int32 [num_tokens] (pa_extend_tables gives them); a negative
+ *                       one is padding, whose rows are left as they were.
+ *   position_offsets    device int32 [num_tokens] or NULL: added to the positions (for one
+ *                       token a sequence, pa_evict_blocks' evicted_tokens).
+ * A position outside [0, max_position) after that records PA_DEVERR_POSITION and leaves its
+ * token's rows as they were (with rotary_dim 0 none is).  What is written must not overlap what is
+ * read, or each other, but for rows in place (PA_ERR_INVALID_ARG).  head_size is 64, 128 or 256
+ * (else PA_ERR_UNSUPPORTED).  num_tokens == 0 is a no-op. */
+typedef struct pa_norm_rope_args {
+  void* query_out;
+  void* key_out;
+  const void* query;
+  const void* key;
+  int64_t query_out_stride, key_out_stride, query_stride, key_stride;
+  const void* query_weight;
+  const void* key_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* position_offsets;
+  float eps;
+  int32_t dtype, num_tokens, num_heads, num_kv_heads, head_size, rotary_dim, max_position;
+  int32_t interleaved; /* 0 or 1 */
+} pa_norm_rope_args;
+pa_status pa_norm_rope(const pa_norm_rope_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Slot mapping from block tables (host).  slots[i] is the physical slot of

@@ -10,7 +10,9 @@ Cache layout (one layer): a contiguous tensor [2, num_blocks, block_size,
 num_kv_heads, head_size] of bf16 or fp32, index 0 = keys, 1 = values; or a
 4-bit pool, a contiguous uint8 tensor [num_blocks, num_kv_heads,
 block_size / 8, 9 * head_size] (alloc_fp4_cache) for the pa_*_fp4 calls and
-the block copies.
+the block copies; or an 8-bit pool, a contiguous int8 tensor [num_blocks,
+num_kv_heads, block_size / 8, 16 * (head_size + 1)] (alloc_int8_cache) for the
+pa_*_int8 calls and the block copies.
 """
 from __future__ import annotations
 
@@ -34,6 +36,7 @@ PA_ERR_TIMEOUT = 7
 PA_BF16 = 0
 PA_FP32 = 1
 PA_FP4 = 2
+PA_INT8 = 3
 PA_KERNEL_AUTO = 0
 PA_KERNEL_SIMT = 1
 PA_KERNEL_TENSOR = 2
@@ -42,6 +45,7 @@ PA_DEVERR_BLOCK_ID = 0x2
 PA_DEVERR_SEQ_LEN = 0x4
 PA_DEVERR_TIMEOUT = 0x8
 PA_DEVERR_BLOCKS = 0x10
+PA_DEVERR_POSITION = 0x20
 PA_PARTITION_BALANCED = -2
 
 # Every function include/pa.h declares.
@@ -58,7 +62,9 @@ EXPORTS = (
     "pa_pool_is_swapped", "pa_pool_num_free_cpu", "pa_decode_append", "pa_copy_bytes",
     "pa_set_decode_wait_limit", "pa_decode_shared_plan", "pa_decode_shared_workspace_size",
     "pa_decode_shared", "pa_reshape_and_cache_fp4", "pa_gather_cache_fp4", "pa_decode_fp4",
-    "pa_decode_fp4_workspace_size", "pa_extend_tables",
+    "pa_decode_fp4_workspace_size", "pa_extend_tables", "pa_reshape_and_cache_int8",
+    "pa_gather_cache_int8", "pa_decode_int8", "pa_decode_int8_workspace_size", "pa_evict_blocks",
+    "pa_norm_rope",
 )
 
 
@@ -82,6 +88,18 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_size", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("query_out", "key_out", "query", "key")]
+                + [(n, ctypes.c_int64) for n in ("query_out_stride", "key_out_stride", "query_stride",
+                                                 "key_stride")]
+                + [(n, ctypes.c_void_p) for n in ("query_weight", "key_weight", "cos_sin", "positions",
+                                                  "position_offsets")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("dtype", "num_tokens", "num_heads", "num_kv_heads",
+                                                 "head_size", "rotary_dim", "max_position",
+                                                 "interleaved")])
 
 
 def _load() -> ctypes.CDLL:
@@ -131,6 +149,14 @@ def _load() -> ctypes.CDLL:
                           vp],
         "pa_extend_tables": [vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32,
                              vp],
+        "pa_reshape_and_cache_int8": [vp, desc, vp, vp, i32, i64, i64, vp, i32, vp],
+        "pa_gather_cache_int8": [vp, vp, i32, vp, desc, vp, i32, vp],
+        "pa_decode_int8_workspace_size": [desc, i32, i32, i32, p_sz],
+        "pa_decode_int8": [vp, vp, i32, i64, vp, desc, vp, i32, vp, i32, i32, f32, vp, vp, f32, vp, sz,
+                           vp],
+        "pa_evict_blocks": [vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                            vp, vp],
+        "pa_norm_rope": [ctypes.POINTER(NormRopeArgs), vp],
         "pa_pool_add_seq_tokens": [vp, vp, i64, p_i64, p_i64],
         "pa_pool_append_token_id": [vp, i64, i32, p_i64, vp],
         "pa_pool_is_cached": [vp, i32, p_i32],
@@ -234,8 +260,44 @@ def alloc_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_si
                        dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=64)
+def _int8_geometry(shape):
+    """(descriptor, a reference to it, KV heads, head size) of an 8-bit pool's shape."""
+    if len(shape) != 4 or shape[3] % 16 or shape[3] < 32:
+        raise ValueError("an 8-bit cache must be [num_blocks, num_kv_heads, block_size / 8, "
+                         "16 * (head_size + 1)]")
+    nb, hkv, tiles, size = shape
+    desc = CacheDesc(nb, 8 * tiles, hkv, size // 16 - 1, PA_INT8)
+    return desc, ctypes.byref(desc), hkv, size // 16 - 1
+
+
+def _int8_pool(cache: torch.Tensor):
+    if cache.dtype is not torch.int8:
+        raise TypeError("an 8-bit cache must be int8, got %s" % cache.dtype)
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return _int8_geometry(cache.shape)
+
+
+def int8_cache_desc(cache: torch.Tensor) -> CacheDesc:
+    """Descriptor of an 8-bit pool [num_blocks, num_kv_heads, block_size / 8, 16 * (head_size + 1)]."""
+    d = _int8_pool(cache)[0]
+    return CacheDesc(d.num_blocks, d.block_size, d.num_kv_heads, d.head_size, d.dtype)
+
+
+def alloc_int8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
+                     device="cuda") -> torch.Tensor:
+    """A zeroed 8-bit pool (every key and value zero)."""
+    if not 8 <= block_size <= 256 or block_size & (block_size - 1):
+        raise ValueError("an 8-bit cache's block_size is a power of two in [8, 256]")
+    return torch.zeros((num_blocks, num_kv_heads, block_size // 8, 16 * (head_size + 1)),
+                       dtype=torch.int8, device=device)
+
+
 def _pool_desc(cache: torch.Tensor) -> CacheDesc:
-    return fp4_cache_desc(cache) if cache.dtype == torch.uint8 else cache_desc(cache)
+    if cache.dtype == torch.uint8:
+        return fp4_cache_desc(cache)
+    return int8_cache_desc(cache) if cache.dtype == torch.int8 else cache_desc(cache)
 
 
 def _dev_ptr(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -711,6 +773,223 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
         None if positions is None else _arg(positions, "positions", i32, dev),
         None if token_starts is None else _arg(token_starts, "token_starts", i32, dev),
         most[0], _on(stream, dev)), "pa_extend_tables")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit pool, eviction, norms with rotation
+# ---------------------------------------------------------------------------
+
+def pa_reshape_and_cache_int8(cache: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                              slot_mapping: torch.Tensor, stream=None) -> None:
+    """pa_reshape_and_cache into an 8-bit pool: key/value [n, num_kv_heads,
+    head_size] (bf16 or fp32, rows may lie apart) are rounded to 8-bit codes with a
+    scale per block and head.  A block's tokens are neighbours in the call."""
+    _, desc, heads, size = _int8_pool(cache)
+    if key.shape != value.shape or key.dim() != 3:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
+    if key.dtype is not value.dtype:
+        raise TypeError("key and value must have the same dtype")
+    n = key.shape[0]
+    if slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    if n > 0x7FFFFFFF:
+        raise _too_large(n)
+    dev = _current_device(cache, "cache")
+    kp, ks = _rows(key, "key", heads, size, dev)
+    vp, vs = _rows(value, "value", heads, size, dev)
+    _check(lib.pa_reshape_and_cache_int8(cache.data_ptr(), desc, kp, vp, _dtype_code(key), ks, vs,
+                                         _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
+                                         _on(stream, dev)), "pa_reshape_and_cache_int8")
+
+
+def pa_gather_cache_int8(key: torch.Tensor, value: torch.Tensor, cache: torch.Tensor,
+                         slot_mapping: torch.Tensor, stream=None) -> None:
+    """Read tokens back from an 8-bit pool: key/value [n, num_kv_heads,
+    head_size] (bf16 or fp32, contiguous) receive what the slots hold; rows of
+    negative slots stay as they were."""
+    _, desc, heads, size = _int8_pool(cache)
+    if key.dim() != 3 or key.shape != value.shape:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
+    n, h, d = key.shape
+    if h != heads or d != size:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_size]")
+    if slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    if n > 0x7FFFFFFF:
+        raise _too_large(n)
+    dev = _current_device(cache, "cache")
+    _check(lib.pa_gather_cache_int8(_arg(key, "key", key.dtype, dev),
+                                    _arg(value, "value", key.dtype, dev), _dtype_code(key),
+                                    cache.data_ptr(), desc,
+                                    _arg(slot_mapping, "slot_mapping", torch.int64, dev), n,
+                                    _on(stream, dev)), "pa_gather_cache_int8")
+
+
+def pa_decode_int8_workspace_size(cache_or_desc, num_heads: int,
+                                  block_tables: torch.Tensor | None = None) -> int:
+    """Workspace bytes of pa_decode_int8 (alloc_workspace), whatever the batch;
+    with block_tables, of calls over tables of that shape that keep weights."""
+    desc = (cache_or_desc if isinstance(cache_or_desc, CacheDesc)
+            else int8_cache_desc(cache_or_desc))
+    seqs, blocks = (0, 0) if block_tables is None else block_tables.shape
+    if max(seqs, blocks) > 0x7FFFFFFF:
+        raise _too_large(max(seqs, blocks))
+    out = ctypes.c_size_t()
+    _check(lib.pa_decode_int8_workspace_size(ctypes.byref(desc), int(num_heads), seqs, blocks,
+                                             ctypes.byref(out)), "pa_decode_int8_workspace_size")
+    return out.value
+
+
+def pa_decode_int8(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
+                   block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                   workspace: torch.Tensor, block_weights: torch.Tensor | None = None,
+                   block_weights_out: torch.Tensor | None = None, decay: float = 1.0,
+                   stream=None) -> None:
+    """pa_decode over an 8-bit pool; query (rows may lie apart) and out are bf16
+    or fp32.  With block_weights (fp32, the tables' shape) the attention that
+    each block gets is added to decay times what it holds (in place unless
+    block_weights_out is given; that alone starts from zeros).  The launches depend on the shapes
+    alone, so that a captured call serves sequences as they grow."""
+    _, desc, _, size = _int8_pool(cache)
+    s, hq, d = query.shape
+    if out.shape != query.shape or d != size:
+        raise ValueError("query/out must be [num_seqs, num_heads, head_size]")
+    if query.dtype is not out.dtype:
+        raise TypeError("query and out must have the same dtype")
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != s or seq_lens.shape != (s,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs]")
+    if tables[1] > 0x7FFFFFFF:
+        raise _too_large(tables[1])
+    dev = _current_device(cache, "cache")
+    qp, qs = _rows(query, "query", hq, d, dev)
+    before = after = None
+    if block_weights is not None:
+        if block_weights.shape != tables:
+            raise ValueError("block_weights must have the shape of block_tables")
+        before = after = _arg(block_weights, "block_weights", torch.float32, dev)
+    if block_weights_out is not None:
+        if block_weights_out.shape != tables:
+            raise ValueError("block_weights_out must have the shape of block_tables")
+        after = _arg(block_weights_out, "block_weights_out", torch.float32, dev)
+    _check(lib.pa_decode_int8(_arg(out, "out", query.dtype, dev), qp, _dtype_code(query), qs,
+                              cache.data_ptr(), desc,
+                              _arg(block_tables, "block_tables", torch.int32, dev), tables[1],
+                              _arg(seq_lens, "seq_lens", torch.int32, dev), s, hq, float(scale),
+                              before, after, float(decay),
+                              _arg(workspace, "workspace", workspace.dtype, dev), workspace.nbytes,
+                              _on(stream, dev)), "pa_decode_int8")
+
+
+def pa_evict_blocks(block_tables: torch.Tensor, block_weights: torch.Tensor,
+                    seq_lens: torch.Tensor, block_size: int, max_blocks: int, keep_first: int = 1,
+                    keep_last: int = 1, free_blocks: torch.Tensor | None = None,
+                    free_state: torch.Tensor | None = None,
+                    evicted_tokens: torch.Tensor | None = None,
+                    block_tables_out: torch.Tensor | None = None,
+                    block_weights_out: torch.Tensor | None = None,
+                    seq_lens_out: torch.Tensor | None = None,
+                    free_state_out: torch.Tensor | None = None,
+                    evicted_tokens_out: torch.Tensor | None = None, stream=None) -> None:
+    """Sequences of more than max_blocks blocks give up those of the least
+    block_weights, the first keep_first and the last keep_last aside: rows of the
+    tables and weights close up (what left follows in the table, zeros in the
+    weights), lengths shrink, the ring of free blocks (free_blocks, free_state = [front, blocks
+    left], as for pa_extend_tables) takes what left, evicted_tokens counts it.  All in place unless
+    *_out are given."""
+    n, = seq_lens.shape
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != n or block_weights.shape != tables:
+        raise ValueError("block_tables and block_weights must be [num_seqs, max_blocks], seq_lens "
+                         "[num_seqs]")
+    if (free_blocks is None) != (free_state is None):
+        raise ValueError("free_blocks and free_state go together")
+    if free_state is None and free_state_out is not None:
+        raise ValueError("free_state_out needs free_state")
+    if evicted_tokens is None and evicted_tokens_out is not None:
+        raise ValueError("evicted_tokens_out needs evicted_tokens")
+    largest = max(tables[1], block_size, max_blocks, keep_first, keep_last,
+                  0 if free_blocks is None else free_blocks.shape[0])
+    if largest > 0x7FFFFFFF:
+        raise _too_large(largest)
+    dev = _current_device(block_tables, "block_tables")
+    i32 = torch.int32
+
+    def pair(before, after, name, dtype, shape):
+        if before is None:
+            return None, None
+        if before.shape != shape or (after is not None and after.shape != shape):
+            raise ValueError("%s must be %s" % (name, list(shape)))
+        at = _arg(before, name, dtype, dev)
+        return at, at if after is None else _arg(after, name + "_out", dtype, dev)
+
+    t, t_out = pair(block_tables, block_tables_out, "block_tables", i32, tables)
+    w, w_out = pair(block_weights, block_weights_out, "block_weights", torch.float32, tables)
+    lens, lens_out = pair(seq_lens, seq_lens_out, "seq_lens", i32, (n,))
+    state, state_out = pair(free_state, free_state_out, "free_state", i32, (2,))
+    gone, gone_out = pair(evicted_tokens, evicted_tokens_out, "evicted_tokens", i32, (n,))
+    ring, capacity = None, 0
+    if free_blocks is not None:
+        if free_blocks.dim() != 1:
+            raise ValueError("free_blocks must be [capacity]")
+        ring, capacity = _arg(free_blocks, "free_blocks", i32, dev), free_blocks.shape[0]
+    _check(lib.pa_evict_blocks(t, w, tables[1], lens, n, int(block_size), int(max_blocks),
+                               int(keep_first), int(keep_last), ring, capacity, state, gone, t_out,
+                               w_out, lens_out, state_out, gone_out, _on(stream, dev)),
+           "pa_evict_blocks")
+
+
+def pa_norm_rope(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Tensor,
+                 key: torch.Tensor, query_weight: torch.Tensor | None,
+                 key_weight: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                 positions: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                 position_offsets: torch.Tensor | None = None, stream=None) -> None:
+    """RMS norm of every head of query [n, num_heads, head_size] and key [n,
+    num_kv_heads, head_size] (bf16 or fp32, rows may lie apart; the outputs may
+    be the inputs), its weight, and the rotation of the pairs (i, i + rotary / 2),
+    or (2 i, 2 i + 1) if interleaved, by cos_sin [max_position, rotary] (cosines,
+    then sines; fp32; None: no rotation) at positions (+ position_offsets).
+    Rows of negative positions stay as they were."""
+    n, heads, size = query.shape
+    if query_out.shape != query.shape or key_out.shape != key.shape or key.dim() != 3 \
+            or key.shape[0] != n or key.shape[2] != size:
+        raise ValueError("query/query_out must be [n, num_heads, head_size], key/key_out [n, "
+                         "num_kv_heads, head_size]")
+    dtype = query.dtype
+    for name, x in (("query_out", query_out), ("key", key), ("key_out", key_out)):
+        if x.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, x.dtype))
+    if positions.shape != (n,) or (position_offsets is not None and position_offsets.shape != (n,)):
+        raise ValueError("positions and position_offsets must be [num_tokens]")
+    kv_heads = key.shape[1]
+    if max(n, heads, kv_heads) > 0x7FFFFFFF:
+        raise _too_large(max(n, heads, kv_heads))
+    dev = _current_device(query, "query")
+    a = NormRopeArgs()
+    a.query_out, a.query_out_stride = _rows(query_out, "query_out", heads, size, dev)
+    a.key_out, a.key_out_stride = _rows(key_out, "key_out", kv_heads, size, dev)
+    a.query, a.query_stride = _rows(query, "query", heads, size, dev)
+    a.key, a.key_stride = _rows(key, "key", kv_heads, size, dev)
+    for name, w in (("query_weight", query_weight), ("key_weight", key_weight)):
+        if w is not None:
+            if w.shape != (size,):
+                raise ValueError("%s must be [head_size]" % name)
+            setattr(a, name, _arg(w, name, dtype, dev))
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        if max(cos_sin.shape) > 0x7FFFFFFF:
+            raise _too_large(max(cos_sin.shape))
+        a.cos_sin = _arg(cos_sin, "cos_sin", torch.float32, dev)
+        a.max_position, a.rotary_dim = cos_sin.shape
+        if a.rotary_dim == 0:
+            raise ValueError("cos_sin has no columns")
+    a.positions = _arg(positions, "positions", torch.int32, dev)
+    if position_offsets is not None:
+        a.position_offsets = _arg(position_offsets, "position_offsets", torch.int32, dev)
+    a.eps, a.dtype, a.num_tokens, a.num_heads = float(eps), _dtype_code(query), n, heads
+    a.num_kv_heads, a.head_size, a.interleaved = kv_heads, size, bool(interleaved)
+    _check(lib.pa_norm_rope(ctypes.byref(a), _on(stream, dev)), "pa_norm_rope")
 
 
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20

@@ -122,18 +122,28 @@ pa_status check_desc(const pa_cache_desc* d) {
   return PA_OK;
 }
 
-// The copies also take 4-bit pools (PA_FP4).
+// The copies also take 4-bit and 8-bit pools.
 pa_status check_pool_desc(const pa_cache_desc* d) {
-  return d && d->dtype == PA_FP4 ? pa::check_fp4_desc(d) : check_desc(d);
+  return d && d->dtype == PA_FP4    ? pa::check_fp4_desc(d)
+         : d && d->dtype == PA_INT8 ? pa::check_int8_desc(d)
+                                    : check_desc(d);
+}
+
+// Bytes of a block of a 4-bit or 8-bit pool (whose tiles hold keys and values
+// together); 0 for the other pools.
+int64_t tiled_block_bytes(const pa_cache_desc* d) {
+  return d->dtype == PA_FP4 ? pa::fp4_block_bytes(d)
+                            : d->dtype == PA_INT8 ? pa::int8_block_bytes(d) : 0;
 }
 
 // Half a block: one plane's rows of a bf16 or fp32 block, or half the bytes
-// of a 4-bit block (whose tiles hold keys and values together).
+// of a tiled block, rounded up to 16 (the halves then overlap by 16 bytes, which
+// both copy).
 pa::BlockGeometry block_geometry(const pa_cache_desc* d) {
   pa::BlockGeometry g;
-  if (d->dtype == PA_FP4) {
-    g.bytes = pa::fp4_block_bytes(d) / 2;
-    g.stride = 2 * g.bytes;
+  if (const int64_t bytes = tiled_block_bytes(d)) {
+    g.bytes = (bytes / 2 + 15) / 16 * 16;
+    g.stride = bytes;
   } else {
     g.bytes = (int64_t)d->block_size * d->num_kv_heads * d->head_size * elem_bytes(d->dtype);
     g.stride = g.bytes;
@@ -143,7 +153,7 @@ pa::BlockGeometry block_geometry(const pa_cache_desc* d) {
 
 // Distance between a block's halves.
 int64_t half_stride(const pa_cache_desc* d, const pa::BlockGeometry& g) {
-  return d->dtype == PA_FP4 ? g.bytes : d->num_blocks * g.bytes;
+  return tiled_block_bytes(d) ? g.stride - g.bytes : d->num_blocks * g.bytes;
 }
 
 bool head_size_supported(int d) { return d == 64 || d == 128 || d == 256; }

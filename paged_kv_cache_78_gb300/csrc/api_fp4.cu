@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "decode_fp4.cuh"
 #include "extend_tables.cuh"
 #include "pa.h"
@@ -12,25 +13,15 @@
 
 namespace {
 
-constexpr int kFp4MaxGroup = 16;
+using namespace pa;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-int ilog2(int x) {
-  int r = 0;
-  while ((1 << r) < x) ++r;
-  return r;
-}
-pa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
+constexpr int kFp4MaxGroup = 16;
 
 // A power of two in [2^-32, 2^32].
 bool tensor_scale_ok(float s) {
   int e = 0;
   return std::isfinite(s) && s > 0.f && std::frexp(s, &e) == 0.5f && e >= -31 && e <= 33;
 }
-
-bool dtype_ok(int32_t t) { return t == PA_BF16 || t == PA_FP32; }
-int64_t elem_bytes(int32_t dtype) { return dtype == PA_BF16 ? 2 : 4; }
 
 pa_status check_call(const pa_cache_desc* desc, int32_t dtype, float key_scale, float value_scale) {
   const pa_status st = pa::check_fp4_desc(desc);
@@ -40,43 +31,12 @@ pa_status check_call(const pa_cache_desc* desc, int32_t dtype, float key_scale, 
   return PA_OK;
 }
 
-// Elements per row, and whether rows `stride` elements apart keep 16-byte
-// alignment without overlapping.
-bool stride_ok(int64_t stride, int64_t row, int32_t dtype) {
-  return stride >= row && stride * elem_bytes(dtype) % 16 == 0;
-}
-
 // One grid holds the call: a CTA per eight tokens and two heads, or more.
 bool grid_ok(const pa_cache_desc* d, int64_t num_tokens) {
   return (num_tokens + 7) / 8 * d->num_kv_heads < (1ll << 31);
 }
 
-// A buffer of a call, to tell whether two overlap.
-struct Range {
-  const void* p;
-  int64_t bytes;
-  bool written;
-};
-bool overlap(const Range& a, const Range& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes &&
-         y < x + (uint64_t)a.bytes;
-}
-
-// Whether a buffer that the call writes (they come first) overlaps another.
-template <int N>
-bool conflict(const Range (&buffers)[N]) {
-  for (int i = 0; i < N && buffers[i].written; ++i)
-    for (int j = i + 1; j < N; ++j)
-      if (overlap(buffers[i], buffers[j])) return true;
-  return false;
-}
 int64_t pool_bytes(const pa_cache_desc* d) { return d->num_blocks * pa::fp4_block_bytes(d); }
-// `n` rows of `row` elements, `stride` apart.
-int64_t rows_bytes(int64_t n, int64_t stride, int64_t row, int32_t dtype) {
-  return ((n - 1) * stride + row) * elem_bytes(dtype);
-}
-
 pa::Fp4Pool pool_of(const void* cache, const pa_cache_desc* d) {
   pa::Fp4Pool p;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));

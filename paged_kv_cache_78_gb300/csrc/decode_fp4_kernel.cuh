@@ -51,6 +51,7 @@
 
 #include "decode_fp4.cuh"
 #include "pa_fp4.cuh"
+#include "warp_decode.cuh"
 
 namespace pa {
 
@@ -78,64 +79,6 @@ constexpr int kFp4Chain = 4096;
 constexpr int kFp4PairCost = 1;
 constexpr int kFp4Whole = 512;  // tokens of a pair that may stay whole with a warp (see there)
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Wait for a phase of `bar`, at most `limit` cycles from the first look on; a
-// wait that runs out records PA_DEVERR_TIMEOUT and returns false.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* err,
-                                           long long limit) {
-  if (mbar_test(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (clock64() - t0 < limit)
-    if (mbar_try_wait(bar, parity)) return true;
-  record_error(err, PA_DEVERR_TIMEOUT);
-  return false;
-}
-
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds_u64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-// c += a . b: a 16 x 16, b 16 x 8, fp16 with fp32 sums.
-__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, const uint32_t* b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
-// c = a . b.
-__device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, const uint32_t* b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
-}
-
 // Products added to c: by the matrix unit, or (kShort) in a chain of their own that
 // done() adds with rounding.  The unit cuts its sums off towards zero, which makes a
 // sum over n products about 1e-8 n too small: over kFp4Chain tokens 4e-5.  That is less
@@ -160,13 +103,6 @@ struct Fp4Sum {
   }
 };
 
-// The 8 x 8 matrix of 16-bit elements that the warp holds, transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
 // a times the low (kHigh: the high) half of s, which the multiplication takes
 // as an operand's half without an instruction of its own.
 template <bool kHigh>
@@ -183,19 +119,6 @@ __device__ __forceinline__ uint32_t half2_mul_by(uint32_t a, uint32_t s) {
         : "=r"(r)
         : "r"(a), "r"(s));
   return r;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <int S>
-__device__ __forceinline__ float group_max(float v) {  // over lanes that differ in bits >= S
-#pragma unroll
-  for (int o = S; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
 }
 
 // The work in units: every pair is kFp4PairCost units (its queries, its end),

@@ -1,0 +1,120 @@
+// Dispatch of the 8-bit decode over element types and head sizes, its workspace, and the
+// sums of the blocks' weights.
+#include "decode_int8.cuh"
+#include "pa_device.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+
+cudaError_t launch_decode_int8_bf16_d64(const Int8DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_int8_bf16_d128(const Int8DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_int8_bf16_d256(const Int8DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_int8_f32_d64(const Int8DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_int8_f32_d128(const Int8DecodeParams&, int num_sms, cudaStream_t);
+cudaError_t launch_decode_int8_f32_d256(const Int8DecodeParams&, int num_sms, cudaStream_t);
+
+namespace {
+
+// What follows the header, in floats, each part a multiple of 64 (256 bytes).
+struct Layout {
+  size_t warps, ctas, chains, rows, cells;
+};
+size_t up(size_t floats) { return (floats + 63) / 64 * 64; }
+Layout layout(int head_size, int num_heads, int group, int log2_block_size, size_t num_seqs,
+              size_t max_blocks, int num_sms) {
+  const int heads = int8_heads(head_size, group);
+  const size_t part = int8_partial_floats(int8_unit_rows(heads, group), head_size);
+  Layout l;
+  l.warps = up(num_sms * kInt8Warps * part);
+  l.ctas = up(num_sms * 4 * part);
+  l.chains = up((size_t)num_sms * kInt8Warps * int8_chain_floats(head_size, heads));
+  const size_t cells = (max_blocks << log2_block_size) >> int8_log2_cell(log2_block_size);
+  l.rows = max_blocks ? up(num_seqs * num_heads * 2) : 0;
+  l.cells = up(num_seqs * cells * num_heads * 2);
+  return l;
+}
+
+// A block's weight: the sum over heads and cells of weights / the row's sum, at the row's
+// maximum.  A warp takes a block, lanes the heads, so that a cell's are read in one piece;
+// 8 bytes per cell and head, written by the decode's kernel just before.
+__global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodeParams p) {
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (blockDim.x / 32);
+  const int l2bs = p.log2_block_size, l2cell = int8_log2_cell(l2bs);
+  const int per_block = 1 << (l2bs - l2cell);
+  const int64_t cells = (int64_t)p.max_blocks_per_seq * per_block;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (p.counters[kInt8HeaderBytes / 4 - 1]) return;  // a call that was refused as a whole
+  for (int64_t at = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+       at < (int64_t)p.num_seqs * p.max_blocks_per_seq; at += warps) {
+    const int s = (int)(at / p.max_blocks_per_seq), b = (int)(at % p.max_blocks_per_seq);
+    const int len = p.seq_lens[s];
+    if (len <= 0 || ((len - 1) >> l2bs) >= p.max_blocks_per_seq || b > (len - 1) >> l2bs) continue;
+    const int n = min(per_block, ((len - 1) >> l2cell) + 1 - b * per_block);
+    float sum = 0.f;
+    for (int h = lane; h < p.num_heads; h += 32) {
+      const float2 row = p.rows[(size_t)s * p.num_heads + h];
+      const float2* from = p.cells + (s * cells + (int64_t)b * per_block) * p.num_heads + h;
+      float mine = 0.f;
+      for (int c = 0; c < n; ++c) {
+        const float2 v = from[(size_t)c * p.num_heads];
+        mine = fmaf(v.x, fast_exp2(v.y - row.x), mine);
+      }
+      sum += __fdiv_rn(mine, row.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const float old = p.block_weights ? p.block_weights[at] : 0.f;
+      p.block_weights_out[at] = fmaf(p.decay, old, sum);
+    }
+  }
+}
+
+}  // namespace
+
+size_t decode_int8_workspace_bytes(int head_size, int num_heads, int group, int block_size,
+                                   int64_t num_seqs, int64_t max_blocks, int num_sms) {
+  int l2bs = 0;
+  while ((1 << l2bs) < block_size) ++l2bs;
+  const Layout l = layout(head_size, num_heads, group, l2bs, (size_t)num_seqs, (size_t)max_blocks,
+                          num_sms);
+  return kInt8HeaderBytes + 4 * (l.warps + l.ctas + l.chains + l.rows + l.cells);
+}
+
+cudaError_t launch_decode_int8(const Int8DecodeParams& params, void* workspace, int dtype,
+                               int num_sms, cudaStream_t stream) {
+  Int8DecodeParams p = params;
+  const Layout l = layout(p.head_size, p.num_heads, p.group, p.log2_block_size, p.num_seqs,
+                          p.block_weights_out ? p.max_blocks_per_seq : 0, num_sms);
+  p.counters = static_cast<unsigned int*>(workspace);
+  p.warp_partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kInt8HeaderBytes);
+  p.cta_partials = p.warp_partials + l.warps;
+  p.chains = p.cta_partials + l.ctas;
+  p.rows = reinterpret_cast<float2*>(p.chains + l.chains);
+  p.cells = reinterpret_cast<float2*>(p.chains + l.chains + l.rows);
+  const bool half = dtype == PA_BF16;
+  cudaError_t e;
+  switch (p.head_size) {
+    case 64:
+      e = half ? launch_decode_int8_bf16_d64(p, num_sms, stream)
+               : launch_decode_int8_f32_d64(p, num_sms, stream);
+      break;
+    case 128:
+      e = half ? launch_decode_int8_bf16_d128(p, num_sms, stream)
+               : launch_decode_int8_f32_d128(p, num_sms, stream);
+      break;
+    default:
+      e = half ? launch_decode_int8_bf16_d256(p, num_sms, stream)
+               : launch_decode_int8_f32_d256(p, num_sms, stream);
+  }
+  if (e != cudaSuccess || !p.block_weights_out) return e;
+  const int64_t blocks = (int64_t)p.num_seqs * p.max_blocks_per_seq;
+  const int64_t most = 8ll * num_sms, ctas = (blocks + 7) / 8;
+  void* args[] = {&p};
+  return launch_overlapped((const void*)block_weights_kernel,
+                           dim3((unsigned)(ctas < most ? ctas : most)), dim3(256), 0, stream, args);
+}
+
+}  // namespace pa

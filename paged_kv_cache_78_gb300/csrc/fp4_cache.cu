@@ -150,19 +150,6 @@ __global__ void __launch_bounds__(kFp4Threads)
   }
 }
 
-// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves (the
-// read-back of 65536 tokens 55.0 and 80.4 us).
-__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    stg_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
-    stg_v4(static_cast<uint8_t*>(p) + 16, make_uint4(w[4], w[5], w[6], w[7]));
-  }
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kFp4Threads)
     fp4_gather_kernel(Fp4Pool pool, T* __restrict__ key, T* __restrict__ value,

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "pa_device.cuh"
+#include "warp_decode.cuh"
 
 namespace pa {
 
@@ -54,17 +55,6 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-__device__ __forceinline__ float half_lo(uint32_t h) {
-  float f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(h));
-  return f;
-}
-__device__ __forceinline__ float half_hi(uint32_t h) {
-  float f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, b;\n\t}" : "=f"(f) : "r"(h));
-  return f;
 }
 
 // ---- numbers to codes ---------------------------------------------------------

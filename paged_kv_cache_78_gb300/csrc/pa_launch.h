@@ -20,6 +20,10 @@ pa_status device_state(unsigned int** err, int* num_sms);
 pa_status check_fp4_desc(const pa_cache_desc* desc);
 int64_t fp4_block_bytes(const pa_cache_desc* desc);
 
+// The same of an 8-bit pool (PA_INT8).
+pa_status check_int8_desc(const pa_cache_desc* desc);
+int64_t int8_block_bytes(const pa_cache_desc* desc);
+
 // Half of a block as the block copies see it: its bytes, and the distance
 // between the same halves of neighbouring blocks.
 struct BlockGeometry {
@@ -117,6 +121,38 @@ struct Fp4DecodeParams;
 size_t decode_fp4_workspace_bytes(int head_size, int group, int num_sms);
 cudaError_t launch_decode_fp4(const Fp4DecodeParams& params, void* workspace, int dtype,
                               int num_sms, cudaStream_t stream);
+
+// 8-bit cache: write and read-back of tokens by slot, as for the 4-bit cache.
+struct Int8Pool {
+  uint8_t* cache;
+  int64_t num_slots;
+  int num_kv_heads;
+  int head_size;
+  int log2_block_size;
+};
+cudaError_t launch_int8_write(const Int8Pool& pool, const void* key, const void* value, int dtype,
+                              int64_t key_stride, int64_t value_stride,
+                              const int64_t* slot_mapping, int num_tokens, int num_sms,
+                              unsigned int* err, cudaStream_t stream);
+cudaError_t launch_int8_gather(const Int8Pool& pool, void* key, void* value, int dtype,
+                               const int64_t* slot_mapping, int num_tokens, unsigned int* err,
+                               cudaStream_t stream);
+
+// Decode attention over an 8-bit cache; num_seqs and max_blocks of the calls that keep
+// weights (0: none).
+struct Int8DecodeParams;
+size_t decode_int8_workspace_bytes(int head_size, int num_heads, int group, int block_size,
+                                   int64_t num_seqs, int64_t max_blocks, int num_sms);
+cudaError_t launch_decode_int8(const Int8DecodeParams& params, void* workspace, int dtype,
+                               int num_sms, cudaStream_t stream);
+
+// Eviction of the blocks with the least weight.
+struct EvictParams;
+cudaError_t launch_evict_blocks(const EvictParams& params, int num_sms, cudaStream_t stream);
+
+// Norms of queries and keys, and rotation.
+cudaError_t launch_norm_rope(const pa_norm_rope_args& args, int num_sms, unsigned int* err,
+                             cudaStream_t stream);
 
 // Limit of the tensor-core decodes' pipeline waits (pa_set_decode_wait_limit).
 long long decode_wait_limit();

@@ -1,0 +1,176 @@
+"""Eviction by accumulated attention weight on the GPU (exact)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_78_gb300 as pa
+from oracle import int8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word():
+    pa.pa_get_device_error()
+    yield
+
+
+def dev(a, dtype=torch.int32):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda()
+
+
+class Evict:
+    """A call on the device and in the oracle."""
+
+    def __init__(self, lens, block=16, most=4, first=1, last=1, width=None, ring=True, gone=True, seed=0,
+                 weights=None, capacity=None, front=None, held=None):
+        rng = np.random.default_rng(seed)
+        self.lens = np.asarray(lens, dtype=np.int32)
+        n = -(-np.maximum(self.lens.astype(np.int64), 0) // block)
+        width = max(1, int(n.max(initial=1))) if width is None else width
+        self.rule = (block, most, first, last)
+        self.tables = rng.permutation(max(1, len(lens) * width)).reshape(-1, width)[:len(lens)].astype(np.int32)
+        self.weights = rng.random(self.tables.shape).astype(np.float32) if weights is None else weights
+        out = int(np.maximum(n - most, 0).sum())
+        self.ring = self.state = None
+        if ring:
+            capacity = out + 9 if capacity is None else capacity
+            held = min(4, capacity - out) if held is None else held
+            front = int(rng.integers(0, capacity)) if front is None else front
+            self.ring = rng.integers(1000, 2000, capacity).astype(np.int32)
+            self.state = np.array([front, held], dtype=np.int32)
+        self.gone = rng.integers(0, 1000, len(lens)).astype(np.int32) if gone else None
+
+    def check(self, in_place, what=""):
+        block, most, first, last = self.rule
+        put = lambda a, t=torch.int32: None if a is None else dev(a, t)
+        t, w, n = put(self.tables), put(self.weights, torch.float32), put(self.lens)
+        ring, state, gone = put(self.ring), put(self.state), put(self.gone)
+        outs = {}
+        if not in_place:
+            fill = lambda a, v: None if a is None else torch.full_like(a, v)
+            outs = dict(block_tables_out=fill(t, -7), block_weights_out=fill(w, -7.0), seq_lens_out=fill(n, -7),
+                        free_state_out=fill(state, -7), evicted_tokens_out=fill(gone, -7))
+            before = [x.clone() for x in (t, w, n)]
+        pa.pa_evict_blocks(t, w, n, block, most, first, last, ring, state, gone, **outs)
+        flags = pa.pa_get_device_error()
+        rt, rw, rn, rr, rs, rg, refused = int8.evict(self.tables, self.weights, self.lens, block, most, first, last,
+                                                     self.ring, self.state, self.gone)
+        got = [t, w, n, state, gone]
+        if not in_place:
+            for x, was in zip((t, w, n), before):
+                assert torch.equal(x.view(torch.int32), was.view(torch.int32))
+            got = [outs[k] for k in ("block_tables_out", "block_weights_out", "seq_lens_out", "free_state_out",
+                                     "evicted_tokens_out")]
+            used = np.minimum(-(-np.maximum(self.lens.astype(np.int64), 0) // block), t.shape[1])[:, None]
+            mine = np.arange(t.shape[1]) < used
+            rt, rw = np.where(mine, rt, -7), np.where(mine, rw, -7)
+        assert np.array_equal(got[0].cpu().numpy(), rt), what
+        assert np.array_equal(got[1].cpu().numpy(), rw, equal_nan=True), what
+        assert np.array_equal(got[2].cpu().numpy(), rn), what
+        if self.ring is not None:
+            assert np.array_equal(ring.cpu().numpy(), rr) and got[3].tolist() == [int(x) for x in rs], what
+        if self.gone is not None:
+            assert np.array_equal(got[4].cpu().numpy(), rg), what
+        return flags, refused
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("ring,gone", [(True, True), (False, False), (True, False)])
+@pytest.mark.parametrize("block,most,first,last", [(16, 4, 1, 1), (8, 7, 0, 1), (1, 5, 2, 3), (256, 1, 0, 1),
+                                                   (16, 40, 3, 37)])
+def test_ragged_sequences(block, most, first, last, ring, gone, in_place):
+    rng = np.random.default_rng(block + most)
+    lens = np.concatenate([[0, 1, block, block * most, block * most + 1, block * (most + 1)],
+                           rng.integers(0, 3 * block * most + 2, 40)])
+    e = Evict(lens, block, most, first, last, ring=ring, gone=gone, seed=block)
+    assert e.check(in_place) == (0, False)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,most", [([8192 * 16], 2048), ([1025 * 16, 1024 * 16, 1023 * 16 + 5], 2), ([49152 * 16 - 3], 100),
+                                       ([49152 * 16], 49151), ([131072, 5, 100_000] * 60, 3000), ([700] * 1000, 3)])
+def test_long_rows_and_many_sequences(lens, most, in_place):
+    assert Evict(lens, most=most, seed=most).check(in_place) == (0, False)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_most_sequences(in_place):
+    lens = np.random.default_rng(2).integers(0, 130, 8192)
+    assert Evict(lens, 8, most=5, seed=3).check(in_place) == (0, False)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_equal_and_special_weights(in_place):
+    rng = np.random.default_rng(4)
+    n, width = 12, 600
+    w = rng.choice([0.0, -0.0, 1.0, 2.0, -1.0, np.nan, np.inf, -np.inf, 1e-45, -1e-45], (n, width)).astype(np.float32)
+    w[0], w[1], w[2] = 0.0, np.nan, np.float32(0.1)
+    w[3] = rng.choice([0.0, -0.0], width)
+    w[4].view(np.int32)[:] = rng.integers(-(1 << 31), 1 << 31, width)     # any bits
+    w[5] = np.nextafter(np.float32(1), np.float32(rng.integers(0, 2, width) * 2))
+    for most in (2, 300, 599):
+        lens = [width * 16] * n
+        assert Evict(lens, most=most, weights=w, seed=most).check(in_place) == (0, False)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_refused_as_a_whole(in_place):
+    lens = [100, 200, 33]
+    bad = [(Evict([100, 209, 33], width=13, most=3), pa.PA_DEVERR_SEQ_LEN),
+           (Evict([100, -1, 33], most=3), pa.PA_DEVERR_SEQ_LEN),
+           (Evict([100, -(1 << 31), (1 << 31) - 1], most=3, width=8), pa.PA_DEVERR_SEQ_LEN),
+           (Evict(lens, most=3, capacity=15, held=2), pa.PA_DEVERR_BLOCKS),    # 14 leave
+           (Evict(lens, most=3, capacity=20, held=21), pa.PA_DEVERR_BLOCKS),
+           (Evict(lens, most=3, capacity=20, held=-1), pa.PA_DEVERR_BLOCKS),
+           (Evict(lens, most=3, capacity=20, front=20), pa.PA_DEVERR_BLOCKS),
+           (Evict(lens, most=3, capacity=20, front=-1), pa.PA_DEVERR_BLOCKS)]
+    for e, flag in bad:
+        assert e.check(in_place) == (flag, True)
+    assert Evict(lens, most=3, capacity=16, held=2).check(in_place) == (0, False)  # just room
+
+
+def test_no_sequences_and_nothing_to_do():
+    t = torch.zeros((0, 4), dtype=torch.int32, device="cuda")
+    n, w = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros((0, 4), device="cuda")
+    ring, state = torch.zeros(3, dtype=torch.int32, device="cuda"), dev(np.array([1, 2]))
+    after = torch.zeros_like(state)
+    pa.pa_evict_blocks(t, w, n, 16, 3, free_blocks=ring, free_state=state)
+    pa.pa_evict_blocks(t, w, n, 16, 3, free_blocks=ring, free_state=state, free_state_out=after)
+    assert after.tolist() == state.tolist() == [1, 2]
+    for in_place in (False, True):
+        assert Evict([0, 16, 64], most=4).check(in_place) == (0, False)
+
+
+def test_rows_behind_the_batch_stay_and_calls_repeat_in_a_graph():
+    e = Evict([3000, 17, 900, 2999], most=50, width=200, seed=7)
+    put = lambda a, t=torch.int32: dev(a, t)
+    big_t, big_w = torch.full((6, 200), -3, dtype=torch.int32, device="cuda"), torch.full((6, 200), -3.0, device="cuda")
+    big_n = torch.full((6,), -3, dtype=torch.int32, device="cuda")
+    ring, state, gone = put(e.ring), put(e.state), put(e.gone)
+    start = [put(e.tables), put(e.weights, torch.float32), put(e.lens), ring.clone(), state.clone(), gone.clone()]
+    live = [big_t[:4], big_w[:4], big_n[:4], ring, state, gone]
+
+    def reset():
+        for x, was in zip(live, start):
+            x.copy_(was)
+
+    def call():
+        pa.pa_evict_blocks(live[0], live[1], live[2], 16, 50, 1, 1, ring, state, gone)
+
+    reset()
+    call()
+    want = [x.clone() for x in live]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        call()                                            # nothing is left to do
+    for _ in range(20):
+        reset()
+        g.replay()
+        for x, y in zip(live, want):
+            assert torch.equal(x, y)
+    rt, rw, rn = int8.evict(e.tables, e.weights, e.lens, 16, 50, 1, 1)[:3]
+    assert np.array_equal(big_t[:4].cpu().numpy(), rt) and np.array_equal(big_w[:4].cpu().numpy(), rw)
+    assert big_n[:4].tolist() == rn.tolist()
+    assert (big_t[4:] == -3).all() and (big_w[4:] == -3).all() and (big_n[4:] == -3).all()
