@@ -38,15 +38,23 @@ __device__ __forceinline__ uint2 quantise_chunk(const uint4& w, float s, float i
   float x[kPer];
   ElemTraits<T>::unpack(w, x);
   uint32_t c[kPer];
-  // A scale of zero or NaN holds zeros; below 2^-100 the reciprocal and the products would
-  // leave fp32's normal numbers.
-  bool sure = s >= 0x1p-100f;
+  bool sure = true;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) c[e] = int8_near(x[e] * inv, &sure);
-  if (!sure) {
-    const bool zeros = !(s > 0.f);
+  if (s >= 0x1p-100f) {
+    if (!sure)
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) c[e] = zeros ? kInt8Bias : int8_exact((double)x[e], s);
+      for (int e = 0; e < kPer; ++e) c[e] = int8_exact(x[e] * inv, x[e], 0.f, s);
+  } else {
+    // A scale of zero or NaN holds zeros; other small ones leave fp32's normal numbers.
+    const bool zeros = !(s > 0.f);
+#pragma unroll 1
+    for (int e = 0; e < kPer; ++e) {
+      const uint32_t v = zeros ? kInt8Bias : int8_exact_small((double)x[e], s);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == e) c[i] = v;
+    }
   }
   uint2 r = make_uint2(0u, 0u);
   r.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
@@ -110,14 +118,22 @@ __device__ __forceinline__ void write_run(const Int8Pool& pool, const T* __restr
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t c[4];
-        bool sure = s >= 0x1p-100f && old >= 0x1p-100f;
+        bool sure = true;
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = int8_near((float)int8_code(words[k], e) * ratio, &sure);
-        if (!sure) {
-          const bool zeros = !(s > 0.f) || !(old > 0.f);
+        if (s >= 0x1p-100f) {
+          if (!sure)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = (float)int8_code(words[k], e), hi = x * old;
+              c[e] = int8_exact(x * ratio, hi, fmaf(x, old, -hi), s);
+            }
+        } else {
+          const bool zeros = !(s > 0.f);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            c[e] = zeros ? kInt8Bias : int8_exact((double)int8_code(words[k], e) * (double)old, s);
+            c[e] = zeros ? kInt8Bias
+                         : int8_exact_small((double)int8_code(words[k], e) * (double)old, s);
         }
         words[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040),
                                0x5410);

@@ -48,7 +48,9 @@ struct Eight {
   }
 };
 
-template <typename T, int D>
+// A thread has 16 elements of each of N heads of a token, all of which it asks for at
+// once, and before it knows the position.
+template <typename T, int D, int N>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;  // of a row
   const pa_norm_rope_args& a = p.a;
@@ -61,10 +63,26 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
   // The lane's two groups of eight.
   const int g0 = a.interleaved || !turns ? 2 * j : j;
   const int g1 = a.interleaved || !turns ? 2 * j + 1 : j + half;
+  const int heads = a.num_heads + a.num_kv_heads;
   grid_dependents_launch();
   grid_dependency_wait();
   // Lanes of other tokens share the warp: they come along to its shuffles.
   bool live = t < a.num_tokens;
+  Eight<T> w[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int h = first + i * p.groups;
+    if (live && h < heads) {
+      const T* src = h < a.num_heads
+                         ? static_cast<const T*>(a.query) + t * a.query_stride + h * D
+                         : static_cast<const T*>(a.key) + t * a.key_stride + (h - a.num_heads) * D;
+      w[i][0].load(src + 8 * g0);
+      w[i][1].load(src + 8 * g1);
+    } else {
+#pragma unroll
+      for (int e = 0; e < Eight<T>::kVecs; ++e) w[i][0].w[e] = w[i][1].w[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   int64_t at = -1;
   if (live) {
     at = __ldg(a.positions + t);
@@ -87,41 +105,30 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
     ElemTraits<float>::unpack(v[2], s);
     ElemTraits<float>::unpack(v[3], s + 4);
   }
-  const int heads = a.num_heads + a.num_kv_heads;
-#pragma unroll 2
-  for (int i = first; i - first < heads; i += p.groups) {  // the same count for the warp
-    const bool is_key = i >= a.num_heads;
-    const bool on = live && i < heads;
-    const int h = is_key ? i - a.num_heads : i;
-    const T* weight = static_cast<const T*>(is_key ? a.key_weight : a.query_weight);
-    float x[16];
-    Eight<T> w0, w1;
-    if (on) {
-      const T* src = static_cast<const T*>(is_key ? a.key : a.query) +
-                     t * (is_key ? a.key_stride : a.query_stride) + h * D;
-      w0.load(src + 8 * g0);
-      w1.load(src + 8 * g1);
-    } else {
 #pragma unroll
-      for (int e = 0; e < Eight<T>::kVecs; ++e) w0.w[e] = w1.w[e] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    w0.unpack(x);
-    w1.unpack(x + 8);
+  for (int i = 0; i < N; ++i) {
+    const int h = first + i * p.groups;
+    const bool is_key = h >= a.num_heads;
+    float x[16];
+    w[i][0].unpack(x);
+    w[i][1].unpack(x + 8);
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!on) continue;
+    if (!live || h >= heads) continue;
     const float inv = __frsqrt_rn(fmaf(sum, 1.f / D, a.eps));
+    const T* weight = static_cast<const T*>(is_key ? a.key_weight : a.query_weight);
     if (weight) {
-      float w[16];
+      float y[16];
+      Eight<T> w0, w1;
       w0.load(weight + 8 * g0);
       w1.load(weight + 8 * g1);
-      w0.unpack(w);
-      w1.unpack(w + 8);
+      w0.unpack(y);
+      w1.unpack(y + 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
+      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * y[e];
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] *= inv;
@@ -140,11 +147,21 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
         for (int e = 0; e < 8; ++e) turn(x[e], x[e + 8], e);
       }
     }
-    T* dst = static_cast<T*>(is_key ? a.key_out : a.query_out) +
-             t * (is_key ? a.key_out_stride : a.query_out_stride) + h * D;
+    T* dst = is_key ? static_cast<T*>(a.key_out) + t * a.key_out_stride + (h - a.num_heads) * D
+                    : static_cast<T*>(a.query_out) + t * a.query_out_stride + h * D;
     Eight<T>::store(dst + 8 * g0, x);
     Eight<T>::store(dst + 8 * g1, x + 8);
   }
+}
+
+template <typename T, int D, int N>
+cudaError_t launch_heads(RopeParams p, cudaStream_t stream) {
+  constexpr int kRows = kRopeThreads / (D / 16);  // of a CTA
+  p.groups = (p.a.num_heads + p.a.num_kv_heads + N - 1) / N;
+  const int64_t grid = ((int64_t)p.a.num_tokens * p.groups + kRows - 1) / kRows;
+  void* args[] = {&p};
+  return launch_overlapped((const void*)norm_rope_kernel<T, D, N>, dim3((unsigned)grid),
+                           dim3(kRopeThreads), 0, stream, args);
 }
 
 template <typename T, int D>
@@ -153,17 +170,11 @@ cudaError_t launch(const pa_norm_rope_args& args, int num_sms, unsigned int* err
   RopeParams p;
   p.a = args;
   p.err = err;
-  constexpr int kRows = kRopeThreads / (D / 16);  // of a CTA
-  const int heads = args.num_heads + args.num_kv_heads;
-  // A lane takes up to four heads where there are more rows than lanes (eight CTAs of 256
-  // an SM).
-  const int64_t rows = (int64_t)args.num_tokens * heads, most = 8ll * num_sms * kRows;
-  const int per = (int)(rows / most < 1 ? 1 : rows / most > 4 ? 4 : rows / most);
-  p.groups = (heads + per - 1) / per;
-  const int64_t grid = ((int64_t)args.num_tokens * p.groups + kRows - 1) / kRows;
-  void* kargs[] = {&p};
-  return launch_overlapped((const void*)norm_rope_kernel<T, D>, dim3((unsigned)grid),
-                           dim3(kRopeThreads), 0, stream, kargs);
+  constexpr int kMost = sizeof(T) == 2 ? 4 : 2;
+  // Several heads a thread where there are more rows than the GPU's lanes hold at once.
+  const int64_t rows = (int64_t)args.num_tokens * (args.num_heads + args.num_kv_heads);
+  if (rows * (D / 16) <= 2048ll * num_sms) return launch_heads<T, D, 1>(p, stream);
+  return launch_heads<T, D, kMost>(p, stream);
 }
 
 }  // namespace

@@ -48,10 +48,26 @@ __device__ __forceinline__ float int8_scale(uint32_t most) {
                              : __fdiv_rn(__uint_as_float(most), 127.f);
 }
 
-// x / s to the nearest whole number, ties to even, decided on the exact quotient, for
-// |x| <= 127.5 s; plus 128.  The quotient of fp64 numbers of 32 bits and 24 that is no tie
-// is 2^-33 (relative) away from one at the least, and fp64 keeps 2^-53.
-__device__ __forceinline__ uint32_t int8_exact(double x, float s) {
+// x / s to the nearest whole number, ties to even, decided on the exact quotient, plus 128;
+// x = hi + lo (lo at most half a step of hi), |x| <= 127.5 s, s >= 2^-100, from the
+// approximate quotient t, off by 2^-16 at the most.  hi - c s has no more bits than fp32
+// holds: for c = 0 it is hi, for c = 1 hi and s are within a factor of two, and from there on hi is a
+// multiple of s's last place and the difference below 2^24 of those.  Neither is |hi - c s| -
+// s / 2 rounded where it is near zero, and a sum's sign is not rounded ever.  (In fp64,
+// of which the GPU has little: the write of 16385 tokens 190 us, as one chunk in 60 has
+// a quotient beside a tie.)
+__device__ __forceinline__ uint32_t int8_exact(float t, float hi, float lo, float s) {
+  float c = rintf(t);
+  const float e = fmaf(-c, s, hi);
+  const float past = (fabsf(e) - 0.5f * s) + (e < 0.f ? -lo : lo);
+  const bool odd = (int)c & 1;
+  if (past > 0.f || (past == 0.f && odd)) c += e < 0.f ? -1.f : 1.f;
+  return (uint32_t)((int)c + kInt8Bias);
+}
+
+// The same in fp64 for scales below that.  A quotient of numbers of 32 bits and 24 that is no
+// tie is 2^-33 (relative) away from one at the least, and fp64 keeps 2^-53.
+static __device__ __noinline__ uint32_t int8_exact_small(double x, float s) {
   const double q = rint(x / (double)s);
   return (uint32_t)((int)fmin(fmax(q, -127.0), 127.0) + kInt8Bias);
 }
