@@ -25,9 +25,9 @@ Layout layout(int head_size, int num_heads, int group, int log2_block_size, size
   const int heads = int8_heads(head_size, group);
   const size_t part = int8_partial_floats(int8_unit_rows(heads, group), head_size);
   Layout l;
-  l.warps = up(num_sms * kInt8Warps * part);
+  l.warps = up(num_sms * kInt8MostWarps * part);
   l.ctas = up(num_sms * 4 * part);
-  l.chains = up((size_t)num_sms * kInt8Warps * int8_chain_floats(head_size, heads));
+  l.chains = up((size_t)num_sms * kInt8MostWarps * int8_chain_floats(head_size, heads));
   const size_t cells = (max_blocks << log2_block_size) >> int8_log2_cell(log2_block_size);
   l.rows = max_blocks ? up(num_seqs * num_heads * 2) : 0;
   l.cells = up(num_seqs * cells * num_heads * 2);

@@ -7,17 +7,27 @@
 
 namespace pa {
 
-constexpr int kInt8Warps = 8;           // of a CTA; one CTA per SM
+constexpr int kInt8MostWarps = 16;      // of a CTA; one CTA per SM
 constexpr int kInt8Gather = 16;         // parts that are merged at once
 constexpr int kInt8MaxCtas = kInt8Gather * kInt8Gather;
 constexpr int kInt8Rows = 16;           // heads of a unit at most, each merged by itself
 // Counters; the header's last word says that a call was refused on the device.
 constexpr int kInt8HeaderBytes = kInt8MaxCtas * 3 * kInt8Rows * 4 + 256;
 
-// Tokens of a stage, the unit of copies, waits and of the work's division: 8 KB of codes.
-__host__ __device__ constexpr int int8_stage(int head_size) { return 4096 / head_size; }
+// Warps of a CTA: 16 where a thread's accumulators and query fragments leave room in 128
+// registers, else 8.
+__host__ __device__ constexpr int int8_warps(int head_size, int heads, bool fp32) {
+  return head_size < 256 && head_size * heads / 32 + head_size / 8 * (heads / 8) * (fp32 ? 2 : 1) <= 64 ? 16 : 8;
+}
+// Tokens of a stage, the unit of copies, waits and of the work's division: 4 or 8 KB of codes,
+// so that a warp's ring has three.
+__host__ __device__ constexpr int int8_stage(int head_size, int warps) {
+  return (warps == 16 ? 2048 : 4096) / head_size;
+}
 // Tokens that a warp computes at a time.
-__host__ __device__ constexpr int int8_step(int head_size) { return head_size == 256 ? 16 : 32; }
+__host__ __device__ constexpr int int8_step(int head_size, int warps) {
+  return int8_stage(head_size, warps) < 32 ? 16 : 32;
+}
 
 // Query heads of a unit of work (columns of the matrix instructions): 8, or 16 where the
 // registers hold them; groups past eight heads of 256 elements read the keys and values

@@ -100,11 +100,11 @@ struct Int8Run {
 template <typename T, int D, int H>
 struct Int8Config {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWarps = kInt8Warps;
+  static constexpr int kWarps = int8_warps(D, H, kF32);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = int8_tile_bytes(D);
-  static constexpr int kStep = int8_step(D);
-  static constexpr int kStage = int8_stage(D);
+  static constexpr int kStep = int8_step(D, kWarps);
+  static constexpr int kStage = int8_stage(D, kWarps);
   static constexpr int kStageBytes = kStage / kInt8Tile * kTileBytes;
   static constexpr int kWholeStages = kWarps * kStep / kStage;  // a step per warp
   static constexpr int kFit = kInt8RingBytes / kWarps / kStageBytes;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Int8Config<T, D, H>::kThreads, 1)
     __syncthreads();
     const unsigned other = lane < W ? (unsigned)warp_sums[lane] : 0u;
     const unsigned base = __reduce_add_sync(0xffffffffu, lane < warp ? other : 0u);
-    // Eight sums may pass 32 bits, those of their upper halves do not.
+    // The warps' sum may pass 32 bits, that of their upper halves does not.
     const unsigned all = __reduce_add_sync(0xffffffffu, other);
     const bool most = __reduce_add_sync(0xffffffffu, other >> 16) >= (kInt8MaxWork >> 16);
     pre[tid] = (int)base + sum - mine;

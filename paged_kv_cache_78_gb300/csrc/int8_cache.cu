@@ -1,13 +1,23 @@
 // Quantising write into the 8-bit pool, and reading tokens back, for sm_103a.
 //
-// The scale of a block, head and side (keys or values) is that of all its tokens, so a
-// warp takes what a call puts into one block for one head and side: the block's tokens are
-// neighbours in the call, the first of them finds the others.  Their rows are read once
-// where they fit in registers (up to 4 KB: 16 tokens of a bf16 head of 128), the maximum goes
-// over the warp, and every 16 elements of a token are one 16-byte piece of the pool.  A
-// block that goes on has its scale read beside the rows, and its codes read and rounded
-// again only where the scale grows.
-// Reading back takes 16 elements of a token's key and of its value per thread.
+// The scale of a block, head and side (keys or values) is that of all its tokens, so what a
+// call puts into one block, a run, is found and written together: a block's tokens are
+// neighbours in the call.  A lane has 16 elements of a row, which are one 16-byte piece of the
+// pool.  A decode batch's runs are single tokens, whose latency counts: a row is a group of D / 16
+// lanes, a warp has several heads and sides.  A prompt's are blocks: a warp, or several for
+// large blocks and small prompts, holds a run's rows in registers from the one reading on, so
+// that each byte moves once.  One launch has CTAs for either kind.  A block that goes on has
+// its scale read beside the rows, and its codes read and rounded again only where it grows.
+//
+// Measured (graph replays in a row, data larger than L2), 8 heads of 128, bf16, blocks of 16: 16384
+// tokens of a prompt 30 us (3.4 TB/s, half of the copy rate: instructions, about 900 for 2048
+// elements, and three dependent trips a run at 24 warps per SM; fp32 37 us, 4.5 TB/s), 500
+// tokens 5.5 us; 128 tokens of as many sequences 2.8 us, 1024 7.3 us.
+// Each kind by itself, the other kind's kernel taking it: single tokens by the whole warp
+// 17 us (1024), prompts by groups 26 us (500 tokens; blocks of 256 tokens 330 us).
+//
+// Reading back takes 16 elements of a token's key and of its value per thread: 65536 tokens
+// 61.7 us, 96% of the copy rate.
 #include "pa_int8.cuh"
 #include "pa_launch.h"
 
@@ -19,200 +29,352 @@ constexpr int kInt8Threads = 256;
 
 // ---- write --------------------------------------------------------------------
 
-// The maximum of |x| over 16 bytes, as bits.
-__device__ __forceinline__ uint32_t largest_bits(const uint4& w, const __nv_bfloat16*) {
-  uint32_t top = 0;
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, v[e] & 0x7fff7fffu);
-  return max(top & 0xffff0000u, top << 16);
-}
-__device__ __forceinline__ uint32_t largest_bits(const uint4& w, const float*) {
-  return max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
-}
-
-// Codes of kPer numbers in a 16-byte chunk, packed from byte 0 on.
+// What a run does to its block's scale.
+struct Scale {
+  float s, inv;
+  float lean;  // int8_lean's, for bf16 rows with a maximum of their own; or 0
+  bool grows;  // and the codes are rounded again
+};
 template <typename T>
-__device__ __forceinline__ uint2 quantise_chunk(const uint4& w, float s, float inv) {
-  constexpr int kPer = ElemTraits<T>::kPerChunk;
-  float x[kPer];
-  ElemTraits<T>::unpack(w, x);
-  uint32_t c[kPer];
-  bool sure = true;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) c[e] = int8_near(x[e] * inv, &sure);
-  if (s >= 0x1p-100f) {
-    if (!sure)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) c[e] = int8_exact(x[e] * inv, x[e], 0.f, s);
-  } else {
-    // A scale of zero or NaN holds zeros; other small ones leave fp32's normal numbers.
-    const bool zeros = !(s > 0.f);
-#pragma unroll 1
-    for (int e = 0; e < kPer; ++e) {
-      const uint32_t v = zeros ? kInt8Bias : int8_exact_small((double)x[e], s);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == e) c[i] = v;
-    }
-  }
-  uint2 r = make_uint2(0u, 0u);
-  r.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-  if constexpr (kPer == 8)
-    r.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+__device__ __forceinline__ Scale scale_of(uint32_t top, float old, bool begins) {
+  Scale r;
+  r.s = int8_scale(top);
+  // Grown, or NaN now; a block whose scale is NaN keeps it.
+  r.grows = !begins && !(r.s <= old) && old == old;
+  const bool own = begins || r.grows;
+  if (!own) r.s = old;
+  r.inv = r.s >= kInt8Small ? 1.f / r.s : 0.f;
+  r.lean = sizeof(T) == 2 && own && r.s >= kInt8Small ? int8_lean(__uint_as_float(top), r.s, r.inv) : 0.f;
   return r;
 }
 
-// What a call puts into one block, for one head and side: tokens t0 .. t0 + n - 1, whose
-// slots lie in `block`.
-template <typename T, int D>
-__device__ __forceinline__ void write_run(const Int8Pool& pool, const T* __restrict__ src,
-                                          int64_t stride, const int64_t* __restrict__ slots,
-                                          int n, int64_t block, bool begins, int h, int kv) {
-  constexpr int kPer = ElemTraits<T>::kPerChunk;
-  constexpr int kChunks = D / kPer;                             // of a row
-  constexpr int kLanes = kChunks < 32 ? kChunks : 32;           // of a row at a time
-  constexpr int kRows = 32 / kLanes;                            // rows at a time
-  constexpr int kCols = kChunks / kLanes;                       // chunks of a lane in a row
-  constexpr int kHeld = 8;                                      // chunks of a lane in registers
-  constexpr int kSteps = kHeld / kCols;                         // steps of kRows rows
-  const int lane = threadIdx.x & 31;
-  const int row = lane / kLanes, col = lane % kLanes;
-  const int l2bs = pool.log2_block_size;
-  uint8_t* base = pool.cache + int8_block_offset(block, h, pool.num_kv_heads, l2bs, D);
-  float* head = reinterpret_cast<float*>(base) + kv;
-  const float old = begins ? 0.f : *head;
-  const T* from = src + row * stride + col * kPer;
-  // The rows, or the first of them.
-  uint4 w[kSteps][kCols];
-  uint32_t top = 0;
+// 16 elements of a row.
+template <typename T>
+struct Piece {
+  uint4 w[sizeof(T)];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const bool live = i * kRows + row < n;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      w[i][c] = live ? ldg_nc_v4(from + (int64_t)i * kRows * stride + c * kLanes * kPer)
-                     : make_uint4(0u, 0u, 0u, 0u);
-      top = max(top, largest_bits(w[i][c], static_cast<const T*>(nullptr)));
-    }
+    for (int i = 0; i < (int)sizeof(T); ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-#pragma unroll 1
-  for (int i = kSteps * kRows + row; i < n; i += kRows)
+  __device__ __forceinline__ void load(const T* p, bool wide) {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
-      top = max(top, largest_bits(ldg_nc_v4(src + i * stride + (c * kLanes + col) * kPer),
-                                  static_cast<const T*>(nullptr)));
-  top = __reduce_max_sync(0xffffffffu, top);
-  float s = int8_scale(top);
-  // Grown, or NaN now; a block whose scale is NaN keeps it.
-  const bool grows = !begins && !(s <= old) && !isnan(old);
-  if (!begins && !grows) s = old;
-  const int codes = kv ? int8_value_codes(D) : int8_key_codes();
-  if (grows) {
-    // All codes of the block, those that are written below among them.
-    const float ratio = old / s;
-    for (int i = lane; i < (D / 2) << (l2bs - 3); i += 32) {  // 16-byte pieces, D / 2 to a tile
-      uint8_t* at = base + i / (D / 2) * int8_tile_bytes(D) + codes + i % (D / 2) * 16;
-      uint4 v = *reinterpret_cast<const uint4*>(at);
-      uint32_t* words = &v.x;
+    for (int i = 0; i < (int)sizeof(T); i += 2)
+      load32(reinterpret_cast<const uint4*>(p) + i, &w[i], wide);
+  }
+  // The largest |x|, as bits (which order NaN above infinity above numbers).
+  __device__ __forceinline__ uint32_t largest() const {
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t c[4];
-        bool sure = true;
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = int8_near((float)int8_code(words[k], e) * ratio, &sure);
-        if (s >= 0x1p-100f) {
-          if (!sure)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = (float)int8_code(words[k], e), hi = x * old;
-              c[e] = int8_exact(x * ratio, hi, fmaf(x, old, -hi), s);
-            }
-        } else {
-          const bool zeros = !(s > 0.f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            c[e] = zeros ? kInt8Bias
-                         : int8_exact_small((double)int8_code(words[k], e) * (double)old, s);
-        }
-        words[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040),
-                               0x5410);
+        for (int e = 0; e < 4; ++e)
+          top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[e])));
       }
-      stg_v4(at, v);
+      return __float_as_uint(__bfloat162float(__hmax_nan(top.x, top.y)));
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = max(max(top, max(w[i].x & 0x7fffffffu, w[i].y & 0x7fffffffu)),
+                  max(w[i].z & 0x7fffffffu, w[i].w & 0x7fffffffu));
+      return top;
     }
-    __syncwarp();  // before other lanes' codes of the new tokens
   }
-  if (begins || grows)
-    for (int i = lane; i < 1 << (l2bs - 3); i += 32)
-      head[i * (int8_tile_bytes(D) / 4)] = s;
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  auto put = [&](int i, int c, const uint4& v) {  // row i, chunk c * kLanes + col
-    const int off = (int)(slots[i] & ((1 << l2bs) - 1));
-    const int chunk = c * kLanes + col;
-    uint8_t* at = base + (off >> 3) * int8_tile_bytes(D) + codes +
-                  chunk * kPer / kInt8Group * 128 + (off & 7) * 16 + chunk * kPer % kInt8Group;
-    const uint2 q = quantise_chunk<T>(v, s, inv);
-    if constexpr (kPer == 8) *reinterpret_cast<uint2*>(at) = q;
-    else *reinterpret_cast<uint32_t*>(at) = q.x;
-  };
+  __device__ __forceinline__ uint4 codes(const Scale& sc) const {
+    constexpr int kPer = ElemTraits<T>::kPerChunk;
+    const float s = sc.s;
+    float x[16];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i)
-    if (i * kRows + row < n)
+    for (int i = 0; i < (int)sizeof(T); ++i) ElemTraits<T>::unpack(w[i], x + i * kPer);
+    uint32_t c[16];
+    bool sure = s >= kInt8Small;
+    if constexpr (sizeof(T) == 2) {
+      if (sc.lean != 0.f) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) put(i * kRows + row, c, w[i][c]);
-#pragma unroll 1
-  for (int i = kSteps * kRows + row; i < n; i += kRows)
+        for (int e = 0; e < 16; ++e) c[e] = int8_plain(x[e], sc.lean);
+      } else {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
-      put(i, c, ldg_nc_v4(src + i * stride + (c * kLanes + col) * kPer));
+        for (int e = 0; e < 16; ++e) c[e] = int8_near_bf16(x[e], sc.inv, s);
+        sure = sure && !int8_few_bits(s);
+      }
+    } else {
+      float off = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) c[e] = int8_near(x[e], sc.inv, &off);
+      sure = sure && off < kInt8Sure;
+    }
+    if (!sure) {
+      // A tie or beside one (fp32: one piece in 1000); or a scale that is small, zero or NaN
+      // (zeros then).
+      const float lift = int8_lift_of(s), sl = s * lift, by = 1.f / sl;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float y = x[e] * lift;
+        c[e] = s > 0.f ? int8_exact(y * by, y, 0.f, sl) : kInt8Bias;
+      }
+    }
+    return make_uint4(low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7]),
+                      low_bytes(c[8], c[9], c[10], c[11]), low_bytes(c[12], c[13], c[14], c[15]));
+  }
+};
+
+// A piece of codes whose scale grows from old to s.
+__device__ __forceinline__ uint4 again(const uint4& v, float old, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
+  const float lift = int8_lift_of(s), was = old * lift, sl = s * lift, ratio = was / sl;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t c[4];
+    float off = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = int8_near((float)int8_code(w[k], e), ratio, &off);
+    if (!(off < kInt8Sure) || !(s > 0.f))
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = (float)int8_code(w[k], e), hi = x * was;
+        c[e] = s > 0.f ? int8_exact(x * ratio, hi, fmaf(x, was, -hi), sl) : kInt8Bias;
+      }
+    r[k] = low_bytes(c[0], c[1], c[2], c[3]);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Warps take (window of tokens, head, side); the window's tokens that are the first of
-// their block's in the call are the warp's work, one after another.
+// Codes of one side of a block, 16-byte piece i of D / 2 to a tile, in any order of lanes.
+template <int D>
+__device__ __forceinline__ void grow(uint8_t* base, int codes, int l2bs, float old, float s,
+                                     int first, int step) {
+  for (int i = first; i < (D / 2) << (l2bs - 3); i += step) {
+    uint4* at = reinterpret_cast<uint4*>(base + i / (D / 2) * int8_tile_bytes(D) + codes + i % (D / 2) * 16);
+    *at = again(*at, old, s);
+  }
+}
+
+// A piece of the token at `off` in the block whose tiles begin at base; j: its place in the row.
+template <int D>
+__device__ __forceinline__ uint8_t* piece_at(uint8_t* base, int codes, int off, int j) {
+  return base + (off >> 3) * int8_tile_bytes(D) + codes + j * 128 + (off & 7) * 16;
+}
+
+struct WriteParams {
+  Int8Pool pool;
+  const void* key;
+  const void* value;
+  int64_t key_stride, value_stride;
+  const int64_t* slots;
+  unsigned int* err;
+  int num_tokens;
+  bool wide;         // rows are on 32-byte boundaries
+  int single_ctas;   // the first CTAs of the grid, which take runs of one token
+  int single_window; // tokens of a warp of theirs
+  int window;        // tokens of a team of the others
+  int row_warps;     // warps of a team: they share a run's rows
+  int per;           // heads and sides of a team, one after another
+  __device__ __forceinline__ int block_of(int64_t slot) const {  // -1: padding, or no slot
+    return (uint64_t)slot < (uint64_t)pool.num_slots ? (int)(slot >> pool.log2_block_size) : -1;
+  }
+  __device__ __forceinline__ int block_at(int64_t t) const {
+    return t >= 0 && t < num_tokens ? block_of(__ldg(slots + t)) : -1;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const WriteParams& p, int side, int64_t t, int at) {
+  return (side & 1 ? static_cast<const T*>(p.value) + t * p.value_stride
+                   : static_cast<const T*>(p.key) + t * p.key_stride) + at;
+}
+
+// Runs of one token, as a decode batch has them: a warp takes some tokens and as many heads
+// and sides as it has groups of a row's D / 16 lanes.
 template <typename T, int D>
-__global__ void __launch_bounds__(kInt8Threads)
-    int8_write_kernel(Int8Pool pool, const T* __restrict__ key, const T* __restrict__ value,
-                      int64_t key_stride, int64_t value_stride,
-                      const int64_t* __restrict__ slot_mapping, int num_tokens, int window,
-                      unsigned int* err) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * (kInt8Threads / 32) + threadIdx.x / 32;
-  const int sides = 2 * pool.num_kv_heads;
-  const int64_t w0 = unit / sides * window;
-  const int side = (int)(unit % sides), h = side >> 1, kv = side & 1;
-  const int l2bs = pool.log2_block_size;
+__device__ __forceinline__ void write_singles(const WriteParams& p) {
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes;
+  const int lane = threadIdx.x & 31, j = lane % kLanes;
+  const int sides = 2 * p.pool.num_kv_heads;
+  const unsigned parts = (unsigned)((sides + kGroups - 1) / kGroups);
+  const unsigned unit = blockIdx.x * (kInt8Threads / 32) + threadIdx.x / 32;
+  const int side = (int)(unit % parts) * kGroups + lane / kLanes, h = side >> 1, kv = side & 1;
+  const bool on = side < sides;
+  const int64_t t0 = (int64_t)(unit / parts) * p.single_window;
+  if (t0 >= p.num_tokens) return;
+  const int l2bs = p.pool.log2_block_size, last = (1 << l2bs) - 1;
+  const int codes = kv ? int8_value_codes(D) : int8_key_codes();
+  // One token: its row is on its way before its slot is known.
+  Piece<T> x;
+  const bool early = p.single_window == 1;
+  if (early && on) x.load(row_of<T>(p, side, t0, h * D + j * 16), p.wide);
+  const int64_t t = t0 + lane;
+  const bool mine = lane < p.single_window && t < p.num_tokens;
+  const int64_t slot = mine ? __ldg(p.slots + t) : -1;
+  const int block = p.block_of(slot);
+  // Bad slots are recorded here, by the first heads and sides.
+  if (slot >= p.pool.num_slots && unit % parts == 0) record_error(p.err, PA_DEVERR_SLOT);
+  const bool alone = block >= 0 && p.block_at(t - 1) != block && p.block_at(t + 1) != block;
+  for (uint32_t singles = __ballot_sync(0xffffffffu, alone); singles; singles &= singles - 1) {
+    const int i = __ffs(singles) - 1;
+    const int off = __shfl_sync(0xffffffffu, (int)slot, i) & last;
+    const bool begins = off == 0;
+    uint8_t* base = p.pool.cache;
+    float held = 0.f;
+    uint32_t top = 0;
+    const int b = __shfl_sync(0xffffffffu, block, i);
+    if (on) {
+      base += int8_block_offset(b, h, p.pool.num_kv_heads, l2bs, D);
+      held = reinterpret_cast<const float*>(base)[kv];
+      if (!early) x.load(row_of<T>(p, side, t0 + i, h * D + j * 16), p.wide);
+      top = x.largest();
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const Scale sc = scale_of<T>(top, held, begins || !on);
+    // Blocks whose scale grows, each by the whole warp.
+    uint32_t growing = __ballot_sync(0xffffffffu, j == 0 && sc.grows);
+    for (; growing; growing &= growing - 1) {
+      const int g = __ffs(growing) - 1;
+      uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)base, g));
+      grow<D>(at, __shfl_sync(0xffffffffu, codes, g), l2bs, __shfl_sync(0xffffffffu, held, g),
+              __shfl_sync(0xffffffffu, sc.s, g), lane, 32);
+    }
+    __syncwarp();
+    if (on) {
+      if (begins || sc.grows)
+        for (int k = j; k < 1 << (l2bs - 3); k += kLanes)
+          (reinterpret_cast<float*>(base) + kv)[k * (int8_tile_bytes(D) / 4)] = sc.s;
+      stg_v4(piece_at<D>(base, codes, off, j), x.codes(sc));
+    }
+  }
+}
+
+// Longer runs, a prompt's blocks: teams of warps take (window of tokens, some heads and sides).
+// The runs that begin in the window are the team's work, one after another; a run's rows go
+// over the team's lanes, which hold them from the one reading on.
+template <typename T, int D>
+__device__ __forceinline__ void write_runs(const WriteParams& p, unsigned cta) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a step
+  constexpr int kSteps = 4, kWarps = kInt8Threads / 32;
+  __shared__ uint32_t tops[2][kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int team = warp / p.row_warps, rank = warp % p.row_warps;
+  const int j = lane % kLanes;
+  const int row0 = rank * kRows + lane / kLanes, step = p.row_warps * kRows;  // the lane's rows
+  const int sides = 2 * p.pool.num_kv_heads;
+  const unsigned unit = cta * (kWarps / p.row_warps) + team;
+  const unsigned parts = (unsigned)((sides + p.per - 1) / p.per);
+  const int side0 = (int)(unit % parts) * p.per, side1 = min(side0 + p.per, sides);
+  int64_t at = (int64_t)(unit / parts) * p.window;
+  const int64_t end = min(at + p.window, (int64_t)p.num_tokens);
+  const int l2bs = p.pool.log2_block_size, last = (1 << l2bs) - 1;
+  auto sync = [&]() {
+    if (p.row_warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * p.row_warps) : "memory");
+  };
+  if (at >= end) return;  // the whole team
+  // The window's rows of the first side are on their way to L2 while its slots are read.
+  constexpr int kLines = D * sizeof(T) / 128;
+  for (int r = rank * 32 + lane; r < (int)(end - at) * kLines; r += 32 * p.row_warps)
+    prefetch_l2(reinterpret_cast<const uint8_t*>(row_of<T>(p, side0, at + r / kLines, (side0 >> 1) * D)) +
+                r % kLines * 128);
+  int turn = 0;
+  while (at < end) {
+    // The slots from here on; the next run of two tokens or more that begins.
+    const int64_t slot = at + lane < p.num_tokens ? __ldg(p.slots + at + lane) : -1;
+    const int mine = p.block_of(slot);
+    int before = __shfl_up_sync(0xffffffffu, mine, 1), after = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (lane == 0) before = p.block_at(at - 1);
+    if (lane == 31) after = p.block_at(at + 32);
+    const uint32_t starts = __ballot_sync(
+        0xffffffffu, mine >= 0 && mine != before && mine == after && at + lane < end);
+    if (!starts) {
+      at += 32;
+      continue;
+    }
+    const int skip = __ffs(starts) - 1;
+    const int block = __shfl_sync(0xffffffffu, mine, skip);
+    const uint32_t other = ~__ballot_sync(0xffffffffu, mine == block) & (0xffffffffu << skip);
+    at += skip;
+    const int seen = 32 - skip;  // slots of the run that lanes may hold
+    int n = other ? __ffs(other) - 1 - skip : seen;
+    bool begins = __any_sync(0xffffffffu, lane >= skip && lane < skip + n && ((int)slot & last) == 0);
+    if (!other)
+      for (uint32_t same = 0xffffffffu; same == 0xffffffffu;) {
+        const int64_t i = at + n + lane;
+        const int64_t s = i < p.num_tokens ? __ldg(p.slots + i) : -1;
+        same = __ballot_sync(0xffffffffu, p.block_of(s) == block);
+        const int more = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+        begins |= __any_sync(0xffffffffu, lane < more && ((int)s & last) == 0);
+        n += more;
+      }
+    int offs[kSteps];  // of the lane's tokens in the block
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = row0 + i * step;
+      offs[i] = (int)__shfl_sync(0xffffffffu, (int)slot, skip + r) & last;
+      if (r >= seen && r < n) offs[i] = (int)__ldg(p.slots + at + r) & last;
+    }
+#pragma unroll 1
+    for (int side = side0; side < side1; ++side, turn ^= 1) {
+      const int kv = side & 1;
+      const int codes = kv ? int8_value_codes(D) : int8_key_codes();
+      const int64_t stride = kv ? p.value_stride : p.key_stride;
+      uint8_t* base = p.pool.cache + int8_block_offset(block, side >> 1, p.pool.num_kv_heads, l2bs, D);
+      float* head = reinterpret_cast<float*>(base) + kv;
+      const float held = *head;
+      const T* src = row_of<T>(p, side, at, (side >> 1) * D + j * 16);
+      Piece<T> x[kSteps];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = row0 + i * step;
+        if (r < n) x[i].load(src + r * stride, p.wide);
+        else x[i].clear();
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) top = max(top, x[i].largest());
+#pragma unroll 1
+      for (int r = row0 + kSteps * step; r < n; r += step) {  // rows past the team's registers
+        Piece<T> y;
+        y.load(src + r * stride, p.wide);
+        top = max(top, y.largest());
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (p.row_warps > 1) {
+        if (lane == 0) tops[turn][warp] = top;
+        sync();
+        for (int i = 0; i < p.row_warps; ++i) top = max(top, tops[turn][warp - rank + i]);
+      }
+      const Scale sc = scale_of<T>(top, held, begins);
+      if (sc.grows) {
+        // All codes of the block, those that are written below among them.
+        grow<D>(base, codes, l2bs, held, sc.s, rank * 32 + lane, p.row_warps * 32);
+        sync();  // before other lanes' codes of the new tokens
+      }
+      if (begins || sc.grows)
+        for (int i = rank * 32 + lane; i < 1 << (l2bs - 3); i += p.row_warps * 32)
+          head[i * (int8_tile_bytes(D) / 4)] = sc.s;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (row0 + i * step < n) stg_v4(piece_at<D>(base, codes, offs[i], j), x[i].codes(sc));
+#pragma unroll 1
+      for (int r = row0 + kSteps * step; r < n; r += step) {
+        Piece<T> y;
+        y.load(src + r * stride, p.wide);
+        stg_v4(piece_at<D>(base, codes, (int)__ldg(p.slots + at + r) & last, j), y.codes(sc));
+      }
+    }
+    at += n;
+  }
+}
+
+// One launch for both: CTAs that find no run of their kind are done at once.
+template <typename T, int D>
+__global__ void __launch_bounds__(kInt8Threads, sizeof(T) == 2 ? 3 : 2)
+    int8_write_kernel(const WriteParams p) {
   grid_dependents_launch();
   grid_dependency_wait();
-  if (w0 >= num_tokens) return;
-  const int64_t t = w0 + lane;
-  const bool mine = lane < window && t < num_tokens;
-  const int64_t slot = mine ? __ldg(slot_mapping + t) : -1;
-  const int64_t before = mine && t > 0 ? __ldg(slot_mapping + t - 1) : -1;
-  if (slot >= pool.num_slots && side == 0) record_error(err, PA_DEVERR_SLOT);
-  auto valid = [&](int64_t s) { return s >= 0 && s < pool.num_slots; };
-  const bool first = valid(slot) && !(valid(before) && (before >> l2bs) == (slot >> l2bs));
-  uint32_t firsts = __ballot_sync(0xffffffffu, first);
-  for (; firsts; firsts &= firsts - 1) {
-    const int at = __ffs(firsts) - 1;
-    const int64_t block = __shfl_sync(0xffffffffu, slot, at) >> l2bs;
-    const int64_t t0 = w0 + at;
-    // The run's length, and whether one of its tokens begins the block.
-    int n = 0;
-    bool begins = false;
-    for (uint32_t same = 0xffffffffu; same == 0xffffffffu;) {
-      const int64_t i = t0 + n + lane;
-      const int64_t s = i < num_tokens ? __ldg(slot_mapping + i) : -1;
-      const bool in = valid(s) && (s >> l2bs) == block;
-      same = __ballot_sync(0xffffffffu, in);
-      const int more = __ffs(~same) - 1;  // -1: all
-      const bool counted = more < 0 || lane < more;
-      begins |= __any_sync(0xffffffffu, counted && (s & ((1 << l2bs) - 1)) == 0);
-      n += more < 0 ? 32 : more;
-    }
-    const T* src = (kv ? value + t0 * value_stride : key + t0 * key_stride) + h * D;
-    write_run<T, D>(pool, src, kv ? value_stride : key_stride, slot_mapping + t0, n, block, begins,
-                    h, kv);
-  }
+  if (blockIdx.x < p.single_ctas) write_singles<T, D>(p);
+  else write_runs<T, D>(p, blockIdx.x - p.single_ctas);
 }
 
 // ---- read-back ----------------------------------------------------------------
@@ -270,22 +432,30 @@ __global__ void __launch_bounds__(kInt8Threads)
 }
 
 template <typename T, int D>
-cudaError_t launch_write(const Int8Pool& pool, const void* key, const void* value,
-                         int64_t key_stride, int64_t value_stride, const int64_t* slot_mapping,
-                         int num_tokens, int num_sms, unsigned int* err, cudaStream_t stream) {
-  // A token a warp while all warps are resident at once or nearly (64 warps an SM), so that
-  // a batch's tokens, each with a block of its own, do not wait for one another; else
-  // windows, so that a prompt's tokens do not each cost a warp.
-  const int64_t sides = 2ll * pool.num_kv_heads;
-  int window = 1;
-  while (window < 32 && (num_tokens + window - 1) / window * sides > 64ll * num_sms) window *= 2;
-  const int64_t warps = (num_tokens + window - 1) / window * sides;
-  constexpr int kPerCta = kInt8Threads / 32;
-  void* args[] = {const_cast<Int8Pool*>(&pool), &key, &value, &key_stride, &value_stride,
-                  &slot_mapping, &num_tokens, &window, &err};
-  return launch_overlapped((const void*)int8_write_kernel<T, D>,
-                           dim3((unsigned)((warps + kPerCta - 1) / kPerCta)), dim3(kInt8Threads),
-                           0, stream, args);
+cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
+  constexpr int kWarps = kInt8Threads / 32, kRows = 512 / D;
+  const int64_t n = p.num_tokens, sides = 2ll * p.pool.num_kv_heads;
+  const int64_t resident = 24ll * num_sms;  // warps
+  auto ctas = [](int64_t warps) { return (warps + kWarps - 1) / kWarps; };
+  const int64_t parts = (sides + kRows - 1) / kRows;
+  p.single_window = 1;
+  while (p.single_window < 32 && (n + p.single_window - 1) / p.single_window * parts > 2 * resident)
+    p.single_window *= 2;
+  p.single_ctas = (int)ctas((n + p.single_window - 1) / p.single_window * parts);
+  const int block = 1 << p.pool.log2_block_size;
+  p.window = block;
+  const int64_t windows = (n + block - 1) / block;
+  // Rows of a warp: four steps, fewer where there are few runs.
+  p.row_warps = 1;
+  while (p.row_warps < kWarps && (p.row_warps * 4 * kRows < block ||
+                                  (p.row_warps * kRows < block && windows * sides * p.row_warps * 2 <= resident)))
+    p.row_warps *= 2;
+  const int64_t per = windows * sides * p.row_warps / 8192;
+  p.per = (int)(per < 1 ? 1 : per > 4 ? 4 : per);
+  const int64_t grid = p.single_ctas + ctas(windows * ((sides + p.per - 1) / p.per) * p.row_warps);
+  void* args[] = {&p};
+  return launch_overlapped((const void*)int8_write_kernel<T, D>, dim3((unsigned)grid),
+                           dim3(kInt8Threads), 0, stream, args);
 }
 
 template <typename T, int D>
@@ -308,15 +478,28 @@ cudaError_t launch_int8_write(const Int8Pool& pool, const void* key, const void*
                               int64_t key_stride, int64_t value_stride,
                               const int64_t* slot_mapping, int num_tokens, int num_sms,
                               unsigned int* err, cudaStream_t stream) {
-  auto run = [&](auto* launch) {
-    return launch(pool, key, value, key_stride, value_stride, slot_mapping, num_tokens, num_sms,
-                  err, stream);
-  };
   const bool half = dtype == PA_BF16;
+  WriteParams p = {};
+  p.pool = pool;
+  p.key = key;
+  p.value = value;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.slots = slot_mapping;
+  p.err = err;
+  p.num_tokens = num_tokens;
+  p.wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31) == 0 &&
+           (key_stride | value_stride) * (half ? 2 : 4) % 32 == 0;
   switch (pool.head_size) {
-    case 64: return half ? run(launch_write<__nv_bfloat16, 64>) : run(launch_write<float, 64>);
-    case 128: return half ? run(launch_write<__nv_bfloat16, 128>) : run(launch_write<float, 128>);
-    default: return half ? run(launch_write<__nv_bfloat16, 256>) : run(launch_write<float, 256>);
+    case 64:
+      return half ? launch_write<__nv_bfloat16, 64>(p, num_sms, stream)
+                  : launch_write<float, 64>(p, num_sms, stream);
+    case 128:
+      return half ? launch_write<__nv_bfloat16, 128>(p, num_sms, stream)
+                  : launch_write<float, 128>(p, num_sms, stream);
+    default:
+      return half ? launch_write<__nv_bfloat16, 256>(p, num_sms, stream)
+                  : launch_write<float, 256>(p, num_sms, stream);
   }
 }
 

