@@ -654,7 +654,8 @@ pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t qu
  * it would write becomes what it read.  num_seqs is at most PA_MAX_TABLE_REQUESTS,
  * max_blocks_per_seq at most PA_MAX_EVICT_BLOCKS (else PA_ERR_INVALID_ARG).  Two buffers of
  * which one is written must not overlap, apart from those that may be in place
- * (PA_ERR_INVALID_ARG).  Two launches, which depend on the shapes alone. */
+ * (PA_ERR_INVALID_ARG).  One launch where seq_lens and free_state are not written in place,
+ * else two; they depend on the shapes alone. */
 #define PA_MAX_EVICT_BLOCKS 49152
 pa_status pa_evict_blocks(const int32_t* block_tables, const float* block_weights,
                           int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,

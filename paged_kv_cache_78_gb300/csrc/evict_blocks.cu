@@ -3,11 +3,11 @@
 //
 // How many blocks leave a sequence follows from its length alone, so every CTA finds by
 // itself, from all lengths, whether the call goes ahead and where its sequences' blocks go
-// in the ring; none waits for another.  The first launch only reads lengths and ring state,
-// the second, one CTA, writes them: they may be written in place.
+// in the ring; none waits for another.  Where lengths or ring state are written in place, that is
+// a second launch's work, one CTA, after all have read them.
 //
 // A sequence's weights become keys in shared memory whose unsigned order is theirs.  The
-// k-th smallest key is found bit by bit from the top, by counting; keys below it leave, and as many
+// k-th smallest key is found by counting, three bits at a time; keys below it leave, and as many
 // of those equal to it, from the lowest index on, as are left to go.  Then the row is
 // gone through once, a chunk of a thread per entry at a time: what stays moves down (so that a
 // row may be its own output: nothing is written before it was read), and what leaves
@@ -88,9 +88,17 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// Length and count of a sequence that k blocks leave.
+__device__ __forceinline__ void write_state(const EvictParams& p, int s, int len, int k) {
+  const int moved = k << p.log2_block_size;
+  p.seq_lens_out[s] = len - moved;
+  if (p.evicted_tokens) p.evicted_tokens_out[s] = p.evicted_tokens[s] + moved;
+}
+
 __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys[];
   __shared__ int counts[2][32];
+  __shared__ uint4 digits[2][32];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
   const int per = (p.num_seqs + gridDim.x - 1) / gridDim.x;
@@ -98,9 +106,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
   grid_dependents_launch();
   grid_dependency_wait();
   const EvictTotals totals = evict_totals(p, s0, blockIdx.x == 0);
-  int64_t ring = 0;  // where the next block that leaves goes
+  // Where the next block that leaves goes: below twice the capacity before it is brought back.
+  int ring = 0;
+  auto in_ring = [&](int i) { return i >= p.free_capacity ? i - p.free_capacity : i; };
+  if (p.alone && p.free_state && blockIdx.x == 0 && tid == 0) {
+    p.free_state_out[0] = p.free_state[0];
+    p.free_state_out[1] = p.free_state[1] + (totals.refused ? 0 : totals.all);
+  }
   if (p.free_state && !totals.refused)
-    ring = ((int64_t)p.free_state[0] + p.free_state[1] + totals.before) % p.free_capacity;
+    ring = in_ring(p.free_state[0] + p.free_state[1] + totals.before);
   // Exclusive count of a flag over the CTA's threads, and all of them.  One barrier a use:
   // `which` alternates between uses, so that a use's writers have passed the barrier that the
   // readers of the use before the last came to after they had read.
@@ -121,6 +135,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
     const float* weights = p.block_weights + row;
     int32_t* ids_out = p.block_tables_out + row;
     float* weights_out = p.block_weights_out + row;
+    if (p.alone && tid == 0) write_state(p, s, len, k);
     if (k == 0) {
       if (ids != ids_out)
         for (int i = tid; i < n; i += threads) ids_out[i] = ids[i];
@@ -129,52 +144,89 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
       continue;
     }
     const int first = p.keep_first, m = n - first - p.keep_last;  // candidates; k <= m
+    // A thread's own keys, several on their way at once.
+#pragma unroll 8
     for (int i = tid; i < m; i += threads) keys[i] = weight_key(weights[first + i]);
-    // The k-th smallest key: the largest value that fewer than k keys are below.
+    // The k-th smallest key: the largest value that fewer than k keys are below, three bits at
+    // a time from the top: seven values are tried at once, their counts two to a word (a
+    // warp's are at most 1536, all warps' 49152).
     uint32_t kth = 0;
     int below = 0;
 #pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t trial = kth | (1u << bit);
-      int c = 0;
-      for (int i = tid; i < m; i += threads) c += keys[i] < trial;  // a thread's own keys
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) counts[bit & 1][warp] = c;
-      __syncthreads();
-      c = __reduce_add_sync(0xffffffffu, lane < warps ? counts[bit & 1][lane] : 0);
-      if (c < k) {
-        kth = trial;
-        below = c;
+    for (int shift = 30, turn = 0; shift >= 0; shift -= 3, turn ^= 1) {
+      // A thread's keys (48 at most) by their next three bits, eight counts of a byte.  Keys
+      // below those with the bits so far count as 0, above them as 7: neither is ever below a value
+      // that it should not be below.
+      uint64_t by = 0;
+#pragma unroll 4
+      for (int i = tid; i < m; i += threads) {
+        const uint32_t key = keys[i];
+        by += 1ull << (8 * (key < kth ? 0u : min((key - kth) >> shift, 7u)));
       }
+      // Values 2 w and 2 w + 1 (keys below 0: none): running sums of counts.
+      uint32_t c[4], sum = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        c[w] = sum;
+        sum += (uint32_t)(by >> (16 * w)) & 0xff;
+        c[w] |= sum << 16;
+        sum += (uint32_t)(by >> (16 * w + 8)) & 0xff;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) c[w] = __reduce_add_sync(0xffffffffu, c[w]);
+      if (lane == 0) digits[turn][warp] = make_uint4(c[0], c[1], c[2], c[3]);
+      __syncthreads();
+      const uint4 all = lane < warps ? digits[turn][lane] : make_uint4(0u, 0u, 0u, 0u);
+      c[0] = __reduce_add_sync(0xffffffffu, all.x);
+      c[1] = __reduce_add_sync(0xffffffffu, all.y);
+      c[2] = __reduce_add_sync(0xffffffffu, all.z);
+      c[3] = __reduce_add_sync(0xffffffffu, all.w);
+      uint32_t digit = 0;
+#pragma unroll
+      for (int v = 1; v < 8; ++v) {
+        const int n_below = (c[v / 2] >> (16 * (v & 1))) & 0xffff;
+        if (n_below < k) {
+          digit = v;
+          below = n_below;
+        }
+      }
+      kth += digit << shift;
     }
     const int equal = k - below;  // of the keys equal to it, the first so many leave
     int gone = 0, ties = 0;       // so far
-    for (int i0 = 0; i0 < n; i0 += threads) {
-      const int i = i0 + tid;
-      int id = 0;
-      float w = 0.f;
-      bool less = false, tie = false;
-      if (i < n) {
-        id = ids[i];
-        w = weights[i];
+    constexpr int kBatch = 8;     // chunks whose entries are on their way at once
+    for (int b0 = 0; b0 < n; b0 += kBatch * threads) {
+      int id[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const int i = b0 + c * threads + tid;
+        id[c] = i < n ? ids[i] : 0;
+        w[c] = i < n ? weights[i] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        if (b0 + c * threads >= n) break;
+        const int i = b0 + c * threads + tid;
+        bool less = false, tie = false;
         if (i >= first && i < first + m) {
           const uint32_t key = keys[i - first];
           less = key < kth;
           tie = key == kth;
         }
-      }
-      int all;
-      const int tied = ties + count(tie, 1, &all);
-      ties += all;
-      const bool leaves = less || (tie && tied < equal);
-      const int before = gone + count(leaves, 0, &all);  // everything of the chunk is read
-      gone += all;
-      if (leaves) {
-        keys[before] = (uint32_t)id;  // before <= i - first: a key that was read
-        if (p.free_state) p.free_blocks[(ring + before) % p.free_capacity] = id;
-      } else if (i < n) {
-        ids_out[i - before] = id;
-        weights_out[i - before] = w;
+        int all;
+        const int tied = ties + count(tie, 1, &all);
+        ties += all;
+        const bool leaves = less || (tie && tied < equal);
+        const int before = gone + count(leaves, 0, &all);  // everything of the chunk is read
+        gone += all;
+        if (leaves) {
+          keys[before] = (uint32_t)id[c];  // before <= i - first: a key that was read
+          if (p.free_state) p.free_blocks[in_ring(ring + before)] = id[c];
+        } else if (i < n) {
+          ids_out[i - before] = id[c];
+          weights_out[i - before] = w[c];
+        }
       }
     }
     __syncthreads();
@@ -182,7 +234,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
       ids_out[n - k + i] = (int32_t)keys[i];
       weights_out[n - k + i] = 0.f;
     }
-    if (p.free_state) ring = (ring + k) % p.free_capacity;
+    if (p.free_state) ring = in_ring(ring + k);
     __syncthreads();  // keys and counts are free again
   }
 }
@@ -199,10 +251,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_state_kernel(const EvictP
   __syncthreads();  // every read of the lengths and the ring's state for the totals is done
   for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) {
     const int len = p.seq_lens[i];
-    const int moved = totals.refused ? 0 : leaving(p, len) << p.log2_block_size;
-    const int past = p.evicted_tokens ? p.evicted_tokens[i] : 0;
-    p.seq_lens_out[i] = len - moved;
-    if (p.evicted_tokens) p.evicted_tokens_out[i] = past + moved;
+    write_state(p, i, len, totals.refused ? 0 : leaving(p, len));
   }
   if (p.free_state && threadIdx.x == 0) {
     p.free_state_out[0] = front;
@@ -230,12 +279,14 @@ cudaError_t launch_evict_blocks(const EvictParams& params, int num_sms, cudaStre
   const int threads = params.max_blocks_per_seq <= 1024 ? 256 : kEvictThreads;
   int ctas = params.num_seqs < 2 * num_sms ? params.num_seqs : 2 * num_sms;
   if (ctas < 1) ctas = 1;
-  void* args[] = {const_cast<EvictParams*>(&params)};
+  EvictParams p = params;
+  p.alone = p.seq_lens_out != p.seq_lens && (!p.free_state || p.free_state_out != p.free_state);
+  void* args[] = {&p};
   cudaError_t e = launch_overlapped((const void*)evict_rows_kernel, dim3((unsigned)ctas),
                                     dim3(threads), smem, stream, args);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.alone) return e;
   return launch_overlapped((const void*)evict_state_kernel, dim3(1),
-                           dim3(params.num_seqs <= 256 ? 256 : kEvictThreads), 0, stream, args);
+                           dim3(p.num_seqs <= 256 ? 256 : kEvictThreads), 0, stream, args);
 }
 
 }  // namespace pa

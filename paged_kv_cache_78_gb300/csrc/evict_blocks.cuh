@@ -18,6 +18,7 @@ struct EvictParams {
   int32_t* free_state_out;
   int32_t* evicted_tokens_out;
   unsigned int* err;
+  bool alone;  // the rows' launch writes lengths and ring state, as nothing that is read is written
   int max_blocks_per_seq, num_seqs, log2_block_size, free_capacity;
   int max_blocks, keep_first, keep_last;
 };
