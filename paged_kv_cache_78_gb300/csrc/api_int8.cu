@@ -142,7 +142,8 @@ pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t qu
       !std::isfinite(decay) || (block_weights && !block_weights_out))
     return PA_ERR_INVALID_ARG;
   if (num_heads < 1 || num_heads % desc->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
-  if (num_heads / desc->num_kv_heads > kInt8MaxGroup || (int64_t)num_seqs * num_heads >= (1ll << 31))
+  if (num_heads / desc->num_kv_heads > kInt8MaxGroup || (int64_t)num_seqs * num_heads >= (1ll << 31) ||
+      (block_weights_out && (int64_t)num_seqs * max_blocks_per_seq >= (1ll << 32)))
     return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   const int64_t row = (int64_t)num_heads * desc->head_size;

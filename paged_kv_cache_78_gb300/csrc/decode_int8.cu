@@ -36,39 +36,53 @@ Layout layout(int head_size, int num_heads, int group, int log2_block_size, size
 
 // A block's weight: the sum over heads and cells of weights / the row's sum, at the row's
 // maximum.  A warp takes a block, lanes the heads, so that a cell's are read in one piece;
-// 8 bytes per cell and head, written by the decode's kernel just before.
+// 8 bytes per cell and head, written by the decode's kernel just before.  Everything is asked
+// for at once, whether the block is there or not: the addresses are in the workspace anyway.
 __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodeParams p) {
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * (blockDim.x / 32);
   const int l2bs = p.log2_block_size, l2cell = int8_log2_cell(l2bs);
   const int per_block = 1 << (l2bs - l2cell);
   const int64_t cells = (int64_t)p.max_blocks_per_seq * per_block;
+  const unsigned blocks = (unsigned)p.num_seqs * (unsigned)p.max_blocks_per_seq;  // below 2^32
   grid_dependents_launch();
   grid_dependency_wait();
-  if (p.counters[kInt8HeaderBytes / 4 - 1]) return;  // a call that was refused as a whole
-  for (int64_t at = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-       at < (int64_t)p.num_seqs * p.max_blocks_per_seq; at += warps) {
-    const int s = (int)(at / p.max_blocks_per_seq), b = (int)(at % p.max_blocks_per_seq);
+  for (unsigned at = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at < blocks;) {
+    const unsigned s = at / (unsigned)p.max_blocks_per_seq;
+    const int b = (int)(at - s * (unsigned)p.max_blocks_per_seq);
+    const bool refused = p.counters[kInt8HeaderBytes / 4 - 1];  // the call as a whole
     const int len = p.seq_lens[s];
-    if (len <= 0 || ((len - 1) >> l2bs) >= p.max_blocks_per_seq || b > (len - 1) >> l2bs) continue;
-    const int n = min(per_block, ((len - 1) >> l2cell) + 1 - b * per_block);
-    float sum = 0.f;
-    for (int h = lane; h < p.num_heads; h += 32) {
-      const float2 row = p.rows[(size_t)s * p.num_heads + h];
-      const float2* from = p.cells + (s * cells + (int64_t)b * per_block) * p.num_heads + h;
-      float mine = 0.f;
-      for (int c = 0; c < n; ++c) {
-        const float2 v = from[(size_t)c * p.num_heads];
-        mine = fmaf(v.x, fast_exp2(v.y - row.x), mine);
+    const float old = p.block_weights ? p.block_weights[at] : 0.f;
+    const float2* row = p.rows + (size_t)s * p.num_heads;
+    const float2* cell = p.cells + (s * cells + (int64_t)b * per_block) * p.num_heads;
+    float2 r = make_float2(0.f, 1.f), v = make_float2(0.f, 0.f);
+    if (lane < p.num_heads) {
+      r = row[lane];
+      v = cell[lane];
+    }
+    const bool there = !refused && len > 0 && (len - 1) >> l2bs < p.max_blocks_per_seq &&
+                       b <= (len - 1) >> l2bs;
+    if (there) {
+      const int n = min(per_block, ((len - 1) >> l2cell) + 1 - b * per_block);
+      float sum = 0.f;
+      for (int h = lane; h < p.num_heads; h += 32) {
+        if (h != lane) {
+          r = row[h];
+          v = cell[h];
+        }
+        float mine = v.x * fast_exp2(v.y - r.x);
+        for (int c = 1; c < n; ++c) {
+          const float2 u = cell[(size_t)c * p.num_heads + h];
+          mine = fmaf(u.x, fast_exp2(u.y - r.x), mine);
+        }
+        sum += __fdiv_rn(mine, r.y);
       }
-      sum += __fdiv_rn(mine, row.y);
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      const float old = p.block_weights ? p.block_weights[at] : 0.f;
-      p.block_weights_out[at] = fmaf(p.decay, old, sum);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) p.block_weights_out[at] = fmaf(p.decay, old, sum);
     }
+    if (blocks - at <= (unsigned)warps) break;
+    at += warps;
   }
 }
 

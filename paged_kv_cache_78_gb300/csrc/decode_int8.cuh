@@ -15,9 +15,11 @@ constexpr int kInt8Rows = 16;           // heads of a unit at most, each merged 
 constexpr int kInt8HeaderBytes = kInt8MaxCtas * 3 * kInt8Rows * 4 + 256;
 
 // Warps of a CTA: 16 where a thread's accumulators and query fragments leave room in 128
-// registers, else 8.
-__host__ __device__ constexpr int int8_warps(int head_size, int heads, bool fp32) {
-  return head_size < 256 && head_size * heads / 32 + head_size / 8 * (heads / 8) * (fp32 ? 2 : 1) <= 64 ? 16 : 8;
+// registers, else 8; but 8 for heads of 128 where no weights are kept, as the copies of 8 KB
+// that they make are read faster than those of 4 KB.
+__host__ __device__ constexpr int int8_warps(int head_size, int heads, bool fp32, bool weights) {
+  return head_size == 64 ? (heads == 16 && fp32 ? 8 : 16)
+                         : head_size == 128 && heads == 8 && !fp32 && weights ? 16 : 8;
 }
 // Tokens of a stage, the unit of copies, waits and of the work's division: 4 or 8 KB of codes,
 // so that a warp's ring has three.

@@ -12,7 +12,7 @@ namespace pa {
 template <typename T, int D, int H, bool kWeights>
 cudaError_t launch_decode_int8_one(const Int8DecodeParams& params, int num_sms,
                                    cudaStream_t stream) {
-  using C = Int8Config<T, D, H>;
+  using C = Int8Config<T, D, H, kWeights>;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

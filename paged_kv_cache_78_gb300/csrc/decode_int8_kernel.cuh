@@ -45,14 +45,13 @@ namespace pa {
 // weight is off by up to 2^-25 where the largest is 2^lift or more.
 __host__ __device__ constexpr float int8_lift(bool fp32) { return fp32 ? 11.f : 7.f; }
 constexpr float kInt8Top = 15.f;
-constexpr int kInt8RingBytes = 216 * 1024;
 // Units of a launch are at most about this many, so that two sums of them fit an int.
 constexpr int kInt8MaxWork = (1 << 30) - 1;
 // Tokens of a chain of sums: rounded additions drop whatever is below half a step of a sum, so
 // a chain's sums are added to the piece's in global memory.
 constexpr int kInt8Chain = 4096;
 // A pair's queries and its end count as this many stages.
-constexpr int kInt8PairCost = 1;
+constexpr int kInt8PairCost = 2;
 constexpr int kInt8Whole = 512;  // tokens of a pair that may stay whole with a warp
 
 // Four 8 x 8 matrices of 16-bit elements (rows of 16 bytes at the lanes' addresses), as they
@@ -97,18 +96,17 @@ struct Int8Run {
   int first, cta0, ctas;
 };
 
-template <typename T, int D, int H>
+template <typename T, int D, int H, bool kWeights>
 struct Int8Config {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kWarps = int8_warps(D, H, kF32);
+  static constexpr int kWarps = int8_warps(D, H, kF32, kWeights);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTileBytes = int8_tile_bytes(D);
   static constexpr int kStep = int8_step(D, kWarps);
   static constexpr int kStage = int8_stage(D, kWarps);
   static constexpr int kStageBytes = kStage / kInt8Tile * kTileBytes;
   static constexpr int kWholeStages = kWarps * kStep / kStage;  // a step per warp
-  static constexpr int kFit = kInt8RingBytes / kWarps / kStageBytes;
-  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  static constexpr int kStages = 2;
   static constexpr int kWarpRing = kStages * kStageBytes;
   // Ring of a warp's pieces: when a piece ends, the stages in flight, the one that waits
   // for a slot and the one after it may all have entered pieces of their own.
@@ -126,9 +124,9 @@ struct Int8Config {
 };
 
 template <typename T, int D, int H, bool kWeights>
-__global__ void __launch_bounds__(Int8Config<T, D, H>::kThreads, 1)
+__global__ void __launch_bounds__(Int8Config<T, D, H, kWeights>::kThreads, 1)
     decode_int8_kernel(const Int8DecodeParams p) {
-  using C = Int8Config<T, D, H>;
+  using C = Int8Config<T, D, H, kWeights>;
   constexpr bool kF32 = C::kF32;
   constexpr int W = C::kWarps;
   constexpr int NS = C::kStages;
@@ -359,13 +357,13 @@ __global__ void __launch_bounds__(Int8Config<T, D, H>::kThreads, 1)
       if (!__any_sync(0xffffffffu, bad)) {
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nx.tiles * TB);
         if (mine > 0)
-          bulk_load(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, (uint32_t)mine * TB, bar);
+          bulk_load_once(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, (uint32_t)mine * TB, bar);
       } else {
         // A block outside the pool: scales of zero.
         const uint32_t bytes = mine > 0 && !bad ? (uint32_t)mine * TB : 0u;
         const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
         if (lane == 0) mbar_arrive_expect_tx(bar, sum);
-        if (bytes) bulk_load(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, bytes, bar);
+        if (bytes) bulk_load_once(dst, nx.base + (uint64_t)(uint32_t)nx.id * block_bytes, bytes, bar);
         if (bad) {
           record_error(p.err, PA_DEVERR_BLOCK_ID);
           for (int i = 0; i < mine; ++i)

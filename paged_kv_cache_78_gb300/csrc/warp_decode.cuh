@@ -18,6 +18,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// The same of what is read once: lines that L2 may drop first.
+__device__ __forceinline__ void bulk_load_once(uint32_t dst, const void* src, uint32_t bytes,
+                                               uint32_t bar) {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // Wait for a phase of `bar`, at most `limit` cycles from the first look on; a
 // wait that runs out records PA_DEVERR_TIMEOUT and returns false.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* err,
