@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -102,6 +103,11 @@ class NormRopeArgs(ctypes.Structure):
                                                  "interleaved")])
 
 
+# The same, packed at once (attributes of a Structure, one by one, take 3 us a call).
+_norm_rope_bytes = struct.Struct("@4P4q5Pf8i4x").pack
+assert struct.calcsize("@4P4q5Pf8i4x") == ctypes.sizeof(NormRopeArgs)
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError("libpa.so is not built (%s); run python paged_kv_cache_78_gb300/_build.py"
@@ -156,7 +162,7 @@ def _load() -> ctypes.CDLL:
                            vp],
         "pa_evict_blocks": [vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp,
                             vp, vp],
-        "pa_norm_rope": [ctypes.POINTER(NormRopeArgs), vp],
+        "pa_norm_rope": [vp, vp],  # a NormRopeArgs, or its bytes
         "pa_pool_add_seq_tokens": [vp, vp, i64, p_i64, p_i64],
         "pa_pool_append_token_id": [vp, i64, i32, p_i64, vp],
         "pa_pool_is_cached": [vp, i32, p_i32],
@@ -965,31 +971,28 @@ def pa_norm_rope(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Te
     if max(n, heads, kv_heads) > 0x7FFFFFFF:
         raise _too_large(max(n, heads, kv_heads))
     dev = _current_device(query, "query")
-    a = NormRopeArgs()
-    a.query_out, a.query_out_stride = _rows(query_out, "query_out", heads, size, dev)
-    a.key_out, a.key_out_stride = _rows(key_out, "key_out", kv_heads, size, dev)
-    a.query, a.query_stride = _rows(query, "query", heads, size, dev)
-    a.key, a.key_stride = _rows(key, "key", kv_heads, size, dev)
+    qo, qos = _rows(query_out, "query_out", heads, size, dev)
+    ko, kos = _rows(key_out, "key_out", kv_heads, size, dev)
+    q, qs = _rows(query, "query", heads, size, dev)
+    k, ks = _rows(key, "key", kv_heads, size, dev)
+    weights = []
     for name, w in (("query_weight", query_weight), ("key_weight", key_weight)):
-        if w is not None:
-            if w.shape != (size,):
-                raise ValueError("%s must be [head_size]" % name)
-            setattr(a, name, _arg(w, name, dtype, dev))
+        if w is not None and w.shape != (size,):
+            raise ValueError("%s must be [head_size]" % name)
+        weights.append(0 if w is None else _arg(w, name, dtype, dev))
+    table = most = rotary = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_position, rotary_dim]")
-        if max(cos_sin.shape) > 0x7FFFFFFF:
-            raise _too_large(max(cos_sin.shape))
-        a.cos_sin = _arg(cos_sin, "cos_sin", torch.float32, dev)
-        a.max_position, a.rotary_dim = cos_sin.shape
-        if a.rotary_dim == 0:
+        most, rotary = cos_sin.shape
+        if most > 0x7FFFFFFF:
+            raise _too_large(most)
+        if rotary == 0:
             raise ValueError("cos_sin has no columns")
-    a.positions = _arg(positions, "positions", torch.int32, dev)
-    if position_offsets is not None:
-        a.position_offsets = _arg(position_offsets, "position_offsets", torch.int32, dev)
-    a.eps, a.dtype, a.num_tokens, a.num_heads = float(eps), _dtype_code(query), n, heads
-    a.num_kv_heads, a.head_size, a.interleaved = kv_heads, size, bool(interleaved)
-    _check(lib.pa_norm_rope(ctypes.byref(a), _on(stream, dev)), "pa_norm_rope")
+        table = _arg(cos_sin, "cos_sin", torch.float32, dev)
+    at = _arg(positions, "positions", torch.int32, dev)
+    off = 0 if position_offsets is None else _arg(position_offsets, "position_offsets", torch.int32, dev)
+    _check(lib.pa_norm_rope(_norm_rope_bytes(qo, ko, q, k, qos, kos, qs, ks, weights[0], weights[1], table, at,
+                                             off, eps, _dtype_code(query), n, heads, kv_heads, size, rotary,
+                                             most, bool(interleaved)), _on(stream, dev)), "pa_norm_rope")
 
 
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20

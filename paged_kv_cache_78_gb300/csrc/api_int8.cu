@@ -277,8 +277,8 @@ pa_status pa_norm_rope(const pa_norm_rope_args* args, void* stream) {
       (a.rotary_dim > 0 && (a.max_position < 1 || !a.cos_sin)))
     return PA_ERR_INVALID_ARG;
   const int64_t heads = (int64_t)a.num_heads + a.num_kv_heads;
-  // Rows of heads fit an int, and one grid holds them.
-  if (heads > (1 << 20) || a.num_tokens * heads >= (1ll << 33)) return PA_ERR_UNSUPPORTED;
+  // A token's heads fit an int, all tokens' 32 bits.
+  if (heads > (1 << 20) || a.num_tokens * heads >= (1ll << 32)) return PA_ERR_UNSUPPORTED;
   if (a.num_tokens == 0) return PA_OK;
   const int64_t n = a.num_tokens;
   const int64_t q_row = (int64_t)a.num_heads * a.head_size, k_row = (int64_t)a.num_kv_heads * a.head_size;

@@ -1,12 +1,17 @@
 // Norms of queries and keys for each head, and the rotation by position, in one pass for
 // sm_103a (pa_norm_rope).
 //
-// Every element is read once and written once; memory bounds it.  A head's row goes over
-// D / 16 lanes, 16 elements each, which are eight pairs: the lane's two groups of eight
-// neighbours are the pairs' first and second elements (halves), or the pairs lie inside the
-// groups (neighbours).  Either way the lane's cosines and sines are eight in a row of the
-// table, and no element leaves its lane.  A token's heads are shared out over lanes that go
-// through them with the same cosines.
+// Every element is read once and written once: memory, and for bf16 the instructions (about 12
+// an element).  A head's row goes over D / 16 lanes, 16 elements each, which are eight pairs: the lane's
+// two groups of eight neighbours are the pairs' first and second elements (halves), or the
+// pairs lie inside the groups (neighbours).  Either way the lane's cosines and sines are eight in a
+// row of the table, and no element leaves its lane.  A token's heads are shared out over lanes that
+// go through them with the same cosines; products go two to an instruction.
+//
+// Measured (graph replays in a row, data larger than L2): 16381 tokens, 32 + 8 heads of 128, bf16
+// 62 us (5.5 TB/s, 82% of the copy rate), fp32 101 us (6.7 TB/s, 99%); 128 tokens 2.3 us, 64 of 14 + 2
+// heads of 64 1.8 us.  (With the next heads on their way to shared memory, two stages a thread:
+// 60.6 us, fp32 149.)
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -22,7 +27,33 @@ struct RopeParams {
   int groups;  // rows of lanes that share a token's heads
 };
 
-// Eight elements as fp32, and back.
+// Two fp32 numbers in one instruction.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 parts(Two a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Two negative(Two a) { return Two{a.v ^ 0x8000000080000000ull}; }
+
+// Eight neighbours as four pairs of fp32, and back.
 template <typename T>
 struct Eight {
   static constexpr int kVecs = sizeof(T) / 2;
@@ -31,126 +62,182 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-  __device__ __forceinline__ void unpack(float* x) const {
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) ElemTraits<T>::unpack(w[i], x + i * ElemTraits<T>::kPerChunk);
+    for (int i = 0; i < kVecs; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  static __device__ __forceinline__ void store(T* p, const float* x) {
+  __device__ __forceinline__ void unpack(Two* x) const {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) ElemTraits<T>::unpack(w[i], f + i * ElemTraits<T>::kPerChunk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = two(f[2 * i], f[2 * i + 1]);
+  }
+  static __device__ __forceinline__ void store(T* p, const Two* x) {
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = parts(x[i]);
     if constexpr (sizeof(T) == 2) {
-      stg_v4(p, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+      stg_v4(p, make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                           pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y)));
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        stg_v4(p + 4 * i, make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
-                                     __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3])));
+        stg_v4(p + 4 * i, make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y),
+                                     __float_as_uint(f[2 * i + 1].x), __float_as_uint(f[2 * i + 1].y)));
     }
   }
 };
 
-// A thread has 16 elements of each of N heads of a token, all of which it asks for at
-// once, and before it knows the position.
-template <typename T, int D, int N>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p) {
-  constexpr int kLanes = D / 16;  // of a row
-  const pa_norm_rope_args& a = p.a;
-  const int64_t unit = (int64_t)blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
-  const int j = threadIdx.x % kLanes;
-  const int64_t t = unit / p.groups;
-  const int first = (int)(unit - t * p.groups);
+// Where a row of lanes stands: a token, and the first of its heads that are the row's (every
+// p.groups-th is).
+struct Place {
+  int64_t t;
+  int first;
+};
+__device__ __forceinline__ Place place_of(const RopeParams& p, unsigned unit) {
+  const unsigned token = unit / (unsigned)p.groups;
+  return Place{(int64_t)token, (int)(unit - token * p.groups)};
+}
+template <typename T>
+__device__ __forceinline__ const T* row_in(const pa_norm_rope_args& a, int64_t t, int h) {
+  return h < a.num_heads ? static_cast<const T*>(a.query) + t * a.query_stride + h * a.head_size
+                         : static_cast<const T*>(a.key) + t * a.key_stride +
+                               (h - a.num_heads) * a.head_size;
+}
+
+// What a lane knows of its part of a row.
+struct Lane {
+  int j, g0, g1;  // its number, and its two groups of eight
+  bool turns;
+};
+__device__ __forceinline__ Lane lane_of(const pa_norm_rope_args& a, int j) {
   const int half = a.rotary_dim / 16;  // lanes that rotate
-  const bool turns = j < half;
-  // The lane's two groups of eight.
-  const int g0 = a.interleaved || !turns ? 2 * j : j;
-  const int g1 = a.interleaved || !turns ? 2 * j + 1 : j + half;
+  Lane l;
+  l.j = j;
+  l.turns = j < half;
+  l.g0 = a.interleaved || !l.turns ? 2 * j : j;
+  l.g1 = a.interleaved || !l.turns ? 2 * j + 1 : j + half;
+  return l;
+}
+
+// The token's position; false for padding and for positions past the table, which `report`
+// records.
+__device__ __forceinline__ bool position_of(const RopeParams& p, int64_t t, int64_t* at, bool report) {
+  const pa_norm_rope_args& a = p.a;
+  *at = __ldg(a.positions + t);
+  if (*at < 0) return false;
+  if (a.position_offsets) *at += __ldg(a.position_offsets + t);
+  if (a.rotary_dim > 0 && (*at < 0 || *at >= a.max_position)) {
+    if (report) record_error(p.err, PA_DEVERR_POSITION);
+    return false;
+  }
+  return true;
+}
+
+// Cosines and sines of the lane's eight pairs, in a row of the table.
+__device__ __forceinline__ void angles_of(const pa_norm_rope_args& a, const Lane& l, int64_t at,
+                                          bool live, Two* c, Two* s) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] = two(1.f, 1.f), s[e] = two(0.f, 0.f);
+  if (live && l.turns) {
+    const float* row = a.cos_sin + at * a.rotary_dim + 8 * l.j;
+    Eight<float> v;
+    v.w[0] = ldg_nc_v4(row), v.w[1] = ldg_nc_v4(row + 4);
+    v.unpack(c);
+    v.w[0] = ldg_nc_v4(row + a.rotary_dim / 2), v.w[1] = ldg_nc_v4(row + a.rotary_dim / 2 + 4);
+    v.unpack(s);
+  }
+}
+
+// One head of a token, in the lanes of a row.  All of the warp's lanes come along.
+template <typename T, int D>
+__device__ __forceinline__ void turn_head(const pa_norm_rope_args& a, const Lane& l, int64_t t, int h,
+                                          bool on, const Eight<T>& w0, const Eight<T>& w1,
+                                          const Two* c, const Two* s) {
+  Two x[8];
+  w0.unpack(x);
+  w1.unpack(x + 4);
+  Two squares = x[0] * x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) squares = fma2(x[e], x[e], squares);
+  float sum = parts(squares).x + parts(squares).y;
+#pragma unroll
+  for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (!on) return;
+  const bool is_key = h >= a.num_heads;
+  const float inv = rsqrtf(fmaf(sum, 1.f / D, a.eps));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = x[e] * two(inv, inv);
+  const T* weight = static_cast<const T*>(is_key ? a.key_weight : a.query_weight);
+  if (weight) {
+    Two y[4];
+    Eight<T> g;
+    g.load(weight + 8 * l.g0);
+    g.unpack(y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = x[e] * y[e];
+    g.load(weight + 8 * l.g1);
+    g.unpack(y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e + 4] = x[e + 4] * y[e];
+  }
+  if (!a.interleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const Two u = x[e], v = x[e + 4];
+      x[e] = fma2(u, c[e], v * negative(s[e]));
+      x[e + 4] = fma2(u, s[e], v * c[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 uv = parts(x[e]);
+      const float ce = e % 2 ? parts(c[e / 2]).y : parts(c[e / 2]).x;
+      const float se = e % 2 ? parts(s[e / 2]).y : parts(s[e / 2]).x;
+      x[e] = two(uv.x * ce - uv.y * se, uv.y * ce + uv.x * se);
+    }
+  }
+  T* dst = is_key ? static_cast<T*>(a.key_out) + t * a.key_out_stride + (h - a.num_heads) * D
+                  : static_cast<T*>(a.query_out) + t * a.query_out_stride + h * D;
+  Eight<T>::store(dst + 8 * l.g0, x);
+  Eight<T>::store(dst + 8 * l.g1, x + 4);
+}
+
+// A row of lanes has N heads of a token, all of which it asks for at once and before it knows
+// the position.
+template <typename T, int D, int N>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 3 : 4)
+    norm_rope_kernel(const RopeParams p) {
+  constexpr int kLanes = D / 16;
+  const pa_norm_rope_args& a = p.a;
+  const Place at = place_of(p, blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes);
+  const Lane l = lane_of(a, threadIdx.x % kLanes);
   const int heads = a.num_heads + a.num_kv_heads;
   grid_dependents_launch();
   grid_dependency_wait();
-  // Lanes of other tokens share the warp: they come along to its shuffles.
-  bool live = t < a.num_tokens;
+  bool live = at.t < a.num_tokens;  // lanes of other tokens share the warp
   Eight<T> w[N][2];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int h = first + i * p.groups;
+    const int h = at.first + i * p.groups;
     if (live && h < heads) {
-      const T* src = h < a.num_heads
-                         ? static_cast<const T*>(a.query) + t * a.query_stride + h * D
-                         : static_cast<const T*>(a.key) + t * a.key_stride + (h - a.num_heads) * D;
-      w[i][0].load(src + 8 * g0);
-      w[i][1].load(src + 8 * g1);
+      const T* src = row_in<T>(a, at.t, h);
+      w[i][0].load(src + 8 * l.g0);
+      w[i][1].load(src + 8 * l.g1);
     } else {
-#pragma unroll
-      for (int e = 0; e < Eight<T>::kVecs; ++e) w[i][0].w[e] = w[i][1].w[e] = make_uint4(0u, 0u, 0u, 0u);
+      w[i][0].clear();
+      w[i][1].clear();
     }
   }
-  int64_t at = -1;
-  if (live) {
-    at = __ldg(a.positions + t);
-    live = at >= 0;
-    if (live && a.position_offsets) at += __ldg(a.position_offsets + t);
-    if (live && a.rotary_dim > 0 && (at < 0 || at >= a.max_position)) {
-      if (first == 0 && j == 0) record_error(p.err, PA_DEVERR_POSITION);
-      live = false;
-    }
-  }
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
-  if (live && turns) {
-    const float* row = a.cos_sin + at * a.rotary_dim + 8 * j;
-    const uint4 v[4] = {ldg_nc_v4(row), ldg_nc_v4(row + 4), ldg_nc_v4(row + a.rotary_dim / 2),
-                        ldg_nc_v4(row + a.rotary_dim / 2 + 4)};
-    ElemTraits<float>::unpack(v[0], c);
-    ElemTraits<float>::unpack(v[1], c + 4);
-    ElemTraits<float>::unpack(v[2], s);
-    ElemTraits<float>::unpack(v[3], s + 4);
-  }
+  int64_t pos = 0;
+  live = live && position_of(p, at.t, &pos, at.first == 0 && l.j == 0);
+  Two c[4], s[4];
+  angles_of(a, l, pos, live, c, s);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int h = first + i * p.groups;
-    const bool is_key = h >= a.num_heads;
-    float x[16];
-    w[i][0].unpack(x);
-    w[i][1].unpack(x + 8);
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!live || h >= heads) continue;
-    const float inv = __frsqrt_rn(fmaf(sum, 1.f / D, a.eps));
-    const T* weight = static_cast<const T*>(is_key ? a.key_weight : a.query_weight);
-    if (weight) {
-      float y[16];
-      Eight<T> w0, w1;
-      w0.load(weight + 8 * g0);
-      w1.load(weight + 8 * g1);
-      w0.unpack(y);
-      w1.unpack(y + 8);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * y[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= inv;
-    }
-    if (turns) {
-      auto turn = [&](float& u, float& v, int e) {
-        const float nu = u * c[e] - v * s[e];
-        v = v * c[e] + u * s[e];
-        u = nu;
-      };
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) turn(x[2 * e], x[2 * e + 1], e);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) turn(x[e], x[e + 8], e);
-      }
-    }
-    T* dst = is_key ? static_cast<T*>(a.key_out) + t * a.key_out_stride + (h - a.num_heads) * D
-                    : static_cast<T*>(a.query_out) + t * a.query_out_stride + h * D;
-    Eight<T>::store(dst + 8 * g0, x);
-    Eight<T>::store(dst + 8 * g1, x + 8);
+    const int h = at.first + i * p.groups;
+    turn_head<T, D>(a, l, at.t, h, live && h < heads, w[i][0], w[i][1], c, s);
   }
 }
 
@@ -170,11 +257,11 @@ cudaError_t launch(const pa_norm_rope_args& args, int num_sms, unsigned int* err
   RopeParams p;
   p.a = args;
   p.err = err;
-  constexpr int kMost = sizeof(T) == 2 ? 4 : 2;
-  // Several heads a thread where there are more rows than the GPU's lanes hold at once.
+  // 128 bytes of a thread on their way at once where there are more rows than the GPU's threads hold
+  // (16381 tokens of 40 heads of 128, bf16: 62 us, 77 with a head each; fp32 101 and 107).
   const int64_t rows = (int64_t)args.num_tokens * (args.num_heads + args.num_kv_heads);
   if (rows * (D / 16) <= 2048ll * num_sms) return launch_heads<T, D, 1>(p, stream);
-  return launch_heads<T, D, kMost>(p, stream);
+  return launch_heads<T, D, sizeof(T) == 2 ? 4 : 2>(p, stream);
 }
 
 }  // namespace
