@@ -186,6 +186,14 @@ __device__ __forceinline__ const T* row_of(const WriteParams& p, int side, int64
                    : static_cast<const T*>(p.key) + t * p.key_stride) + at;
 }
 
+// Steps of rows that a warp holds: bf16's 16 registers leave room for four CTAs an SM (1024
+// single tokens 5.7 us, 7.5 with twice the rows and three CTAs; blocks of 8 26.5 and 33.3; blocks of
+// 16 30 either way), while fp32 rather has its loads on their way at once (37.0 us, 41.0 with half).
+template <typename T>
+__host__ __device__ constexpr int write_steps() {
+  return sizeof(T) == 2 ? 2 : 4;
+}
+
 // Runs of one token, as a decode batch has them: a warp takes some tokens and as many heads
 // and sides as it has groups of a row's D / 16 lanes.
 template <typename T, int D>
@@ -253,7 +261,7 @@ __device__ __forceinline__ void write_singles(const WriteParams& p) {
 template <typename T, int D>
 __device__ __forceinline__ void write_runs(const WriteParams& p, unsigned cta) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a step
-  constexpr int kSteps = 4, kWarps = kInt8Threads / 32;
+  constexpr int kSteps = write_steps<T>(), kWarps = kInt8Threads / 32;
   __shared__ uint32_t tops[2][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int team = warp / p.row_warps, rank = warp % p.row_warps;
@@ -369,7 +377,7 @@ __device__ __forceinline__ void write_runs(const WriteParams& p, unsigned cta) {
 
 // One launch for both: CTAs that find no run of their kind are done at once.
 template <typename T, int D>
-__global__ void __launch_bounds__(kInt8Threads, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kInt8Threads, sizeof(T) == 2 ? 4 : 2)
     int8_write_kernel(const WriteParams p) {
   grid_dependents_launch();
   grid_dependency_wait();
@@ -435,7 +443,9 @@ template <typename T, int D>
 cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kInt8Threads / 32, kRows = 512 / D;
   const int64_t n = p.num_tokens, sides = 2ll * p.pool.num_kv_heads;
-  const int64_t resident = 24ll * num_sms;  // warps
+  // Warps of either kind that are worth having at once (32 an SM: 64 prompts of 37 tokens 13.3 us, not
+  // 11.4).
+  const int64_t resident = 24ll * num_sms;
   auto ctas = [](int64_t warps) { return (warps + kWarps - 1) / kWarps; };
   const int64_t parts = (sides + kRows - 1) / kRows;
   p.single_window = 1;
@@ -445,9 +455,9 @@ cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
   const int block = 1 << p.pool.log2_block_size;
   p.window = block;
   const int64_t windows = (n + block - 1) / block;
-  // Rows of a warp: four steps, fewer where there are few runs.
+  // Rows of a warp: as many as it holds, fewer where there are few runs.
   p.row_warps = 1;
-  while (p.row_warps < kWarps && (p.row_warps * 4 * kRows < block ||
+  while (p.row_warps < kWarps && (p.row_warps * write_steps<T>() * kRows < block ||
                                   (p.row_warps * kRows < block && windows * sides * p.row_warps * 2 <= resident)))
     p.row_warps *= 2;
   const int64_t per = windows * sides * p.row_warps / 8192;
