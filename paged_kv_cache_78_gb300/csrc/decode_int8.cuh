@@ -15,14 +15,16 @@ constexpr int kInt8Rows = 16;           // heads of a unit at most, each merged 
 constexpr int kInt8HeaderBytes = kInt8MaxCtas * 3 * kInt8Rows * 4 + 256;
 
 // Warps of a CTA: 16 where a thread's accumulators and query fragments leave room in 128
-// registers, else 8; but 8 for heads of 128 where no weights are kept, as the copies of 8 KB
-// that they make are read faster than those of 4 KB.
+// registers, which hide each other's waits (heads of 64: 64 sequences of up to 2048 tokens with
+// weights 16.2 us, 17.9 with 8; fp32 50.6 and 57.5; 8 x 32768 tokens of 128 with weights 91.0 and
+// 93.4), else 8.  But 8 for heads of 128 where no weights are kept: they copy 8 KB at a time,
+// not 4, which the memory gives faster (84.4 and 86.0 us, 384 x 1500 tokens 186 and 194), and for
+// fp32 of 128 (85 and 92), whose registers would spill.
 __host__ __device__ constexpr int int8_warps(int head_size, int heads, bool fp32, bool weights) {
   return head_size == 64 ? (heads == 16 && fp32 ? 8 : 16)
                          : head_size == 128 && heads == 8 && !fp32 && weights ? 16 : 8;
 }
-// Tokens of a stage, the unit of copies, waits and of the work's division: 4 or 8 KB of codes,
-// so that a warp's ring has three.
+// Tokens of a stage, the unit of copies, waits and of the work's division: 4 or 8 KB of codes.
 __host__ __device__ constexpr int int8_stage(int head_size, int warps) {
   return (warps == 16 ? 2048 : 4096) / head_size;
 }
@@ -32,8 +34,8 @@ __host__ __device__ constexpr int int8_step(int head_size, int warps) {
 }
 
 // Query heads of a unit of work (columns of the matrix instructions): 8, or 16 where the
-// registers hold them; groups past eight heads of 256 elements read the keys and values
-// once per eight heads.
+// registers hold them (16 heads of 128: 97 us where eight take 86, so twice eight would take 172);
+// groups past eight heads of 256 elements read the keys and values once per eight heads.
 __host__ __device__ constexpr int int8_heads(int head_size, int group) {
   return group <= 8 || head_size == 256 ? 8 : 16;
 }

@@ -6,12 +6,12 @@
 // P = 2^(S - m) with a running maximum m.  Reading the pool bounds it.  A code becomes fp16
 // (exactly) by a byte permutation and a subtraction per pair in the registers of the thread
 // that uses it as an operand of mma.sync; with the matrix instructions a step of 32 tokens
-// of 128 elements takes a warp about 450 instructions, and an SM, which gets the step's 8 KB in
+// of 128 elements takes a warp about 640 instructions, and an SM, which gets the step's 8 KB in
 // 370 clocks at HBM's rate, could issue 1480.  (tcgen05 would take its operands from shared or
-// tensor memory: the fp16 codes would have to be written there and read again.  e4m3 codes,
-// which it takes as they are, would round the queries and weights to four bits.)  The
-// pool's layout is made for this: ldmatrix gives a tile's keys, and with .trans its values, as
-// the matrix instructions' fragments.
+// tensor memory: the fp16 codes would have to be written there and read again, 4 bytes a code beside
+// the one that comes.  e4m3 codes, which it takes as they are, would round queries and weights to
+// four bits.)  The pool's layout is made for this: ldmatrix gives a tile's keys, and with .trans
+// its values, as the matrix instructions' fragments.
 //
 // Every warp works for itself.  The stages of 16 to 64 tokens of all (sequence, KV head)
 // pairs, laid end to end, are cut into equal ranges, one per CTA, and those into equal
@@ -21,13 +21,33 @@
 // the CTA's warps at the end, and over CTAs by whichever finishes last, always in the
 // same order.
 //
+// Two stages a warp, 132 KB on their way per SM: with three (198 KB) the memory gives less (8 x
+// 32768 tokens 84.4 us, 91 with three; 384 x 1500 186 and 204), and so it does without the
+// hint that L2 may drop the lines first (85.4; 128 sequences of up to 2100 tokens 50.2 and 53.3).
+//
 // Value scales: O is kept in units of the pair's largest value scale so far (rounded up
-// to a power of two, so that the ratios are exact in all but their rounding), which moves
-// with the maximum.
+// to a power of two, so that nothing but the ratios' own rounding is lost), which moves with the
+// maximum.
 //
 // kWeights: every cell (16 tokens, or a block of 8) hands on, for each head, the sum of its
 // weights and the maximum that they are relative to; a second launch adds them up when
 // the rows' maxima and sums are known.
+//
+// Measured (graph replays in a row, data larger than L2, 6776 GB/s = 100%):
+//   8 x 32768 tokens, 32 heads on 8 of 128, bf16     84.4 us  538 MB  94%  (with weights 91 us)
+//   the same with blocks of 256                      82.3 us          96%
+//   the same with 64 heads, with 128 heads on 8      86, 97 us        92%, 82%
+//   the same in fp32                                 85 us            93%
+//   16 x 32768 tokens, 32 heads on 8 of 64           87 us    539 MB  92%
+//   8 x 32768 tokens, 32 heads on 4 of 256           88 us    538 MB  90%
+//   384 x 1500 tokens, 32 heads on 8 of 128         186 us   1.19 GB  94%
+//   128 sequences of 0 .. 2100 tokens                50 us    273 MB  80%  (56 us)
+//   32 sequences of 1 .. 2048 tokens, 40 heads       53 us    311 MB  86%
+//   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  13.0 us               (16.2 us)
+//   four sequences of up to 100 tokens                6.1 us
+// What is left of the short ones is the launch (2.5 us), lengths, tables and first copies one
+// after another (4 us), steps of a lone warp (1.5 us each) and merges over CTAs (3 to 4 us);
+// 16 heads of 128 are bound by instructions (8 warps, two column tiles).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -50,9 +70,10 @@ constexpr int kInt8MaxWork = (1 << 30) - 1;
 // Tokens of a chain of sums: rounded additions drop whatever is below half a step of a sum, so
 // a chain's sums are added to the piece's in global memory.
 constexpr int kInt8Chain = 4096;
-// A pair's queries and its end count as this many stages.
+// A pair's queries and its end count as this many stages (128 sequences of up to 2100 tokens
+// 57.2 us at one, 55.4 at two; 32 of 40 pairs each 58.6 and 58.3).
 constexpr int kInt8PairCost = 2;
-constexpr int kInt8Whole = 512;  // tokens of a pair that may stay whole with a warp
+constexpr int kInt8Whole = 512;  // tokens of a pair that may stay whole with a warp (256, 1024: the same)
 
 // Four 8 x 8 matrices of 16-bit elements (rows of 16 bytes at the lanes' addresses), as they
 // lie or transposed.

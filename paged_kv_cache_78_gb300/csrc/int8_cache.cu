@@ -10,11 +10,12 @@
 // its scale read beside the rows, and its codes read and rounded again only where it grows.
 //
 // Measured (graph replays in a row, data larger than L2), 8 heads of 128, bf16, blocks of 16: 16384
-// tokens of a prompt 30 us (3.4 TB/s, half of the copy rate: instructions, about 900 for 2048
-// elements, and three dependent trips a run at 24 warps per SM; fp32 37 us, 4.5 TB/s), 500
-// tokens 5.5 us; 128 tokens of as many sequences 2.8 us, 1024 7.3 us.
-// Each kind by itself, the other kind's kernel taking it: single tokens by the whole warp
-// 17 us (1024), prompts by groups 26 us (500 tokens; blocks of 256 tokens 330 us).
+// tokens of a prompt 30.4 us (3.3 TB/s, half of the copy rate: three dependent trips a run -
+// slots, rows, codes - and about 1080 instructions for 2048 elements, of which 32 warps per SM
+// hide each other's waits to 2.3 a clock; fp32 37 us, 4.5 TB/s; heads of 64 26, blocks of 8
+// 27, of 256 43), 500 tokens 5.3 us; 128 tokens of as many sequences 2.8 us, 1024 5.9 us.
+// Each kind by itself, the other kind's kernel taking it: single tokens by whole warps 17 us
+// (1024), prompts by groups 26 us (500 tokens; 2000 in blocks of 256 330 us).
 //
 // Reading back takes 16 elements of a token's key and of its value per thread: 65536 tokens
 // 61.7 us, 96% of the copy rate.
