@@ -33,9 +33,9 @@ def table(positions, rotary, seed=0):
 
 
 def rope_bound(x, weight, eps, cos_sin, positions, interleaved, dtype):
-    """The norm: a sum of squares, 16 in a row and 4 over lanes (2^-24 each, halved by the root),
-    the mean and eps, the root, two products: 15 * 2^-24.  The rotation: a product and a sum
-    each of |u c| + |v s|: 3 * 2^-24.  One rounding to the type, half a step."""
+    """The norm: a sum of squares, 16 in a row and 4 over lanes at the most (2^-24 each, halved by the
+    root: 10), eps (halved), the root (2 last places: 2.2), two products: 15 * 2^-24.  The rotation: a
+    product and a sum each of |u c| + |v s|: 3 * 2^-24.  One rounding to the type, half a step."""
     if cos_sin is None:
         near = np.abs(int8.norm_rope(x, weight, eps, None, positions, interleaved))
     else:
