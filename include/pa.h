@@ -607,10 +607,13 @@ pa_status pa_gather_cache_int8(void* key, void* value, int32_t dtype, const void
  *   block_weights      likewise, the weights before the step; the same buffer (in place) or
  *                      other memory; NULL: zeros.
  *   decay              finite.
- *   workspace          as for pa_decode_fp4, of pa_decode_int8_workspace_size bytes:
- *                      num_seqs and max_blocks_per_seq are those of the largest call that
- *                      keeps weights (8 bytes for every 16 tokens, or block of 8, and query
- *                      head of such a table), 0 if none does.
+ *   workspace          device scratch of pa_decode_int8_workspace_size bytes, 256-byte
+ *                      aligned, zeroed once at allocation.  It serves pa_decode_int8 calls of any
+ *                      shape it is large enough for, one after another, and no other call; calls
+ *                      that overlap on the GPU need separate workspaces.  num_seqs and
+ *                      max_blocks_per_seq are those of the largest call that keeps weights (8
+ *                      bytes for every 16 tokens, or block of 8, and query head of such a
+ *                      table; at most 2^32 - 1 entries, else PA_ERR_UNSUPPORTED), 0 if none does.
  * out, block_weights_out and the workspace must overlap neither each other nor anything
  * that the call reads, but for weights in place (PA_ERR_INVALID_ARG).  A sequence that
  * is recorded as PA_DEVERR_SEQ_LEN keeps the weights that it has in block_weights_out. */
@@ -675,7 +678,8 @@ pa_status pa_evict_blocks(const int32_t* block_tables, const float* block_weight
  *     out_i = y_i c_i - y_j s_i,  out_j = y_j c_i + y_i s_i   for the pairs (i, j),
  * c_i = cos_sin[p][i], s_i = cos_sin[p][rotary_dim / 2 + i], i < rotary_dim / 2: with
  * j = i + rotary_dim / 2, or, interleaved, the elements 2 i and 2 i + 1.  Elements from
- * rotary_dim on are y.  Arithmetic is fp32, rounded once at the end.
+ * rotary_dim on are y.  Arithmetic is fp32, rounded once at the end; squares have to stay in
+ * its range (elements past 2^59 may not).
  *   query, key          device, [num_tokens] rows of [num_heads] (num_kv_heads) [head_size]
  *                       elements of `dtype` (PA_BF16 or PA_FP32), query_stride / key_stride
  *                       elements apart (slices of a fused projection's output, say).

@@ -42,6 +42,10 @@ bool grid_ok(const pa_cache_desc* d, int64_t num_tokens) {
   return (num_tokens + 7) / 8 * d->num_kv_heads < (1ll << 31);
 }
 
+// Tables whose blocks' weights are kept: 32 bits count their entries (and 64 the bytes of the
+// workspace: 2^32 entries of up to 16 cells, 2^20 heads, 8 bytes).
+bool tables_ok(int64_t num_seqs, int64_t max_blocks) { return num_seqs * max_blocks < (1ll << 32); }
+
 }  // namespace
 
 namespace pa {
@@ -120,7 +124,8 @@ pa_status pa_decode_int8_workspace_size(const pa_cache_desc* desc, int32_t num_h
   if (!bytes || num_heads < 1 || num_heads % desc->num_kv_heads != 0 || num_seqs < 0 ||
       num_seqs > 65535 || max_blocks_per_seq < 0)
     return PA_ERR_INVALID_ARG;
-  if (num_heads / desc->num_kv_heads > kInt8MaxGroup) return PA_ERR_UNSUPPORTED;
+  if (num_heads / desc->num_kv_heads > kInt8MaxGroup || !tables_ok(num_seqs, max_blocks_per_seq))
+    return PA_ERR_UNSUPPORTED;
   int sms = 0;
   if ((st = pa::device_state(nullptr, &sms)) != PA_OK) return st;
   if (sms > pa::kInt8MaxCtas) return PA_ERR_UNSUPPORTED;
@@ -143,7 +148,7 @@ pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t qu
     return PA_ERR_INVALID_ARG;
   if (num_heads < 1 || num_heads % desc->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
   if (num_heads / desc->num_kv_heads > kInt8MaxGroup || (int64_t)num_seqs * num_heads >= (1ll << 31) ||
-      (block_weights_out && (int64_t)num_seqs * max_blocks_per_seq >= (1ll << 32)))
+      (block_weights_out && !tables_ok(num_seqs, max_blocks_per_seq)))
     return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   const int64_t row = (int64_t)num_heads * desc->head_size;

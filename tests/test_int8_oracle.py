@@ -458,4 +458,10 @@ def test_workspace_size_refusals():
     assert call(desc(), 4, 65536) == pa.PA_ERR_INVALID_ARG
     assert call(desc(), 4, 1, -1) == pa.PA_ERR_INVALID_ARG
     assert call(desc(), 34) == pa.PA_ERR_UNSUPPORTED
+    # more entries than 32 bits count, whose bytes 64 bits might not
+    for s, b in ((65535, (1 << 31) - 1), (3, (1 << 31) - 1), (65535, 65538)):
+        assert call(desc(), 4, s, b) == pa.PA_ERR_UNSUPPORTED
+    heads = desc(num_kv_heads=65535, head_size=64, block_size=8)
+    assert call(heads, 16 * 65535, 65535, (1 << 31) - 1) == pa.PA_ERR_UNSUPPORTED
+    assert decode_call(s=65535, mb=65538, after=far(90), ws_bytes=1 << 62, out=far(70)) == pa.PA_ERR_UNSUPPORTED
     assert call(desc(head_size=32), 4) == pa.PA_ERR_UNSUPPORTED
