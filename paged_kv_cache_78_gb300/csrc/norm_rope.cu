@@ -9,9 +9,9 @@
 // go through them with the same cosines; products go two to an instruction.
 //
 // Measured (graph replays in a row, data larger than L2): 16381 tokens, 32 + 8 heads of 128, bf16
-// 62 us (5.5 TB/s, 82% of the copy rate), fp32 101 us (6.7 TB/s, 99%); 128 tokens 2.3 us, 64 of 14 + 2
-// heads of 64 1.8 us.  (With the next heads on their way to shared memory, two stages a thread:
-// 60.6 us, fp32 149.)
+// 60.5 us (5.6 TB/s, 84% of the copy rate), fp32 99 us (6.8 TB/s, 101%); 128 tokens 2.3 us, 64 of
+// 14 + 2 heads of 64 1.7 us.  (With the next heads on their way to shared memory, two stages a
+// thread: 60.6 us, fp32 149.)
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -19,7 +19,9 @@ namespace pa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+// CTAs of four warps leave the SM's last wave the least to wait for (512 tokens of 40 heads 3.7 us;
+// 4.8 with eight warps, 4.6 with two).
+constexpr int kRopeThreads = 128;
 
 struct RopeParams {
   pa_norm_rope_args a;
@@ -207,7 +209,7 @@ __device__ __forceinline__ void turn_head(const pa_norm_rope_args& a, const Lane
 // A row of lanes has N heads of a token, all of which it asks for at once and before it knows
 // the position.
 template <typename T, int D, int N>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 3 : 4)
+__global__ void __launch_bounds__(kRopeThreads, 8)
     norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;
   const pa_norm_rope_args& a = p.a;
@@ -257,11 +259,13 @@ cudaError_t launch(const pa_norm_rope_args& args, int num_sms, unsigned int* err
   RopeParams p;
   p.a = args;
   p.err = err;
-  // 128 bytes of a thread on their way at once where there are more rows than the GPU's threads hold
-  // (16381 tokens of 40 heads of 128, bf16: 62 us, 77 with a head each; fp32 101 and 107).
+  // 96 bytes of a thread (fp32 128) on their way at once where there are more rows than the GPU's
+  // threads hold: 16381 tokens of 40 heads of 128, bf16: 60.5 us with three heads a thread, 61.1 with two,
+  // 77 with one (four leave registers for fewer warps: 60.7, heads of 256 55.9 for 54.6); fp32 99 with
+  // two, 107 with one.
   const int64_t rows = (int64_t)args.num_tokens * (args.num_heads + args.num_kv_heads);
   if (rows * (D / 16) <= 2048ll * num_sms) return launch_heads<T, D, 1>(p, stream);
-  return launch_heads<T, D, sizeof(T) == 2 ? 4 : 2>(p, stream);
+  return launch_heads<T, D, sizeof(T) == 2 ? 3 : 2>(p, stream);
 }
 
 }  // namespace
