@@ -10,15 +10,17 @@
 // its scale read beside the rows, and its codes read and rounded again only where it grows.
 //
 // Measured (graph replays in a row, data larger than L2), 8 heads of 128, bf16, blocks of 16: 16384
-// tokens of a prompt 30.4 us (3.3 TB/s, half of the copy rate: three dependent trips a run -
-// slots, rows, codes - and about 1080 instructions for 2048 elements, of which 32 warps per SM
-// hide each other's waits to 2.3 a clock; fp32 37 us, 4.5 TB/s; heads of 64 26, blocks of 8
-// 27, of 256 43), 500 tokens 5.3 us; 128 tokens of as many sequences 2.8 us, 1024 5.9 us.
+// tokens of a prompt 23.2 us (4.3 TB/s, 64% of the copy rate: three dependent trips a run -
+// slots, rows, codes - and about 450 instructions for 1024 elements, of which 32 warps per SM
+// hide each other's waits to 2.4 a clock; fp32 31.5 us, 5.3 TB/s; heads of 64 21, blocks of 8
+// 22, of 256 31), 128 tokens of as many sequences 2.7 us, 1024 5.3 us.
 // Each kind by itself, the other kind's kernel taking it: single tokens by whole warps 17 us
 // (1024), prompts by groups 26 us (500 tokens; 2000 in blocks of 256 330 us).
 //
 // Reading back takes 16 elements of a token's key and of its value per thread: 65536 tokens
 // 61.7 us, 96% of the copy rate.
+#include <type_traits>
+
 #include "pa_int8.cuh"
 #include "pa_launch.h"
 
@@ -26,7 +28,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kInt8Threads = 256;
+constexpr int kInt8Threads = 256;   // of a CTA that reads back
+constexpr int kWriteThreads = 128;
 
 // ---- write --------------------------------------------------------------------
 
@@ -65,15 +68,15 @@ struct Piece {
   // The largest |x|, as bits (which order NaN above infinity above numbers).
   __device__ __forceinline__ uint32_t largest() const {
     if constexpr (sizeof(T) == 2) {
-      __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+      uint32_t top = 0;  // a pair, whose signs mean nothing
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[e])));
+          asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(v[e]));
       }
-      return __float_as_uint(__bfloat162float(__hmax_nan(top.x, top.y)));
+      return max((top << 16) & 0x7fff0000u, top & 0x7fff0000u);
     } else {
       uint32_t top = 0;
 #pragma unroll
@@ -83,6 +86,8 @@ struct Piece {
       return top;
     }
   }
+  // kOwn: the scale is these rows' own.
+  template <bool kOwn>
   __device__ __forceinline__ uint4 codes(const Scale& sc) const {
     constexpr int kPer = ElemTraits<T>::kPerChunk;
     const float s = sc.s;
@@ -92,9 +97,9 @@ struct Piece {
     uint32_t c[16];
     bool sure = s >= kInt8Small;
     if constexpr (sizeof(T) == 2) {
-      if (sc.lean != 0.f) {
+      if (kOwn || sc.lean != 0.f) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) c[e] = int8_plain(x[e], sc.lean);
+        for (int e = 0; e < 16; e += 2) int8_plain(x[e], x[e + 1], sc.lean, c + e);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) c[e] = int8_near_bf16(x[e], sc.inv, s);
@@ -153,10 +158,11 @@ __device__ __forceinline__ void grow(uint8_t* base, int codes, int l2bs, float o
   }
 }
 
-// A piece of the token at `off` in the block whose tiles begin at base; j: its place in the row.
+// Where the first 16 codes of the token at `off` in a block are, after the block's first; its others
+// follow every 128 bytes.
 template <int D>
-__device__ __forceinline__ uint8_t* piece_at(uint8_t* base, int codes, int off, int j) {
-  return base + (off >> 3) * int8_tile_bytes(D) + codes + j * 128 + (off & 7) * 16;
+__device__ __forceinline__ int place_of(int off) {
+  return (off >> 3) * int8_tile_bytes(D) + (off & 7) * 16;
 }
 
 struct WriteParams {
@@ -170,9 +176,9 @@ struct WriteParams {
   bool wide;         // rows are on 32-byte boundaries
   int single_ctas;   // the first CTAs of the grid, which take runs of one token
   int single_window; // tokens of a warp of theirs
-  int window;        // tokens of a team of the others
-  int row_warps;     // warps of a team: they share a run's rows
-  int per;           // heads and sides of a team, one after another
+  int window;        // tokens that a run of the others begins in
+  int row_warps, l2_row_warps;  // warps of a team: they share a run's rows
+  unsigned teams, per, more;  // per pairs of a window and a side each; the first `more` teams one more
   __device__ __forceinline__ int block_of(int64_t slot) const {  // -1: padding, or no slot
     return (uint64_t)slot < (uint64_t)pool.num_slots ? (int)(slot >> pool.log2_block_size) : -1;
   }
@@ -187,12 +193,17 @@ __device__ __forceinline__ const T* row_of(const WriteParams& p, int side, int64
                    : static_cast<const T*>(p.key) + t * p.key_stride) + at;
 }
 
-// Steps of rows that a warp holds: bf16's 16 registers leave room for four CTAs an SM (1024
-// single tokens 5.7 us, 7.5 with twice the rows and three CTAs; blocks of 8 26.5 and 33.3; blocks of
-// 16 30 either way), while fp32 rather has its loads on their way at once (37.0 us, 41.0 with half).
+// Steps of rows that a warp holds, and CTAs of an SM: bf16's 16 registers of rows leave room for
+// eight (16384 tokens of a prompt 23.4 us, 24.1 and 26.1 with seven and six, 34 with half the rows), while fp32
+// rather has its loads on their way at once (32.9 us; half the rows and seven CTAs 34.5, five CTAs 40).
 template <typename T>
 __host__ __device__ constexpr int write_steps() {
   return sizeof(T) == 2 ? 2 : 4;
+}
+
+template <typename T>
+__host__ __device__ constexpr int write_ctas() {
+  return sizeof(T) == 2 ? 8 : 4;
 }
 
 // Runs of one token, as a decode batch has them: a warp takes some tokens and as many heads
@@ -203,7 +214,7 @@ __device__ __forceinline__ void write_singles(const WriteParams& p) {
   const int lane = threadIdx.x & 31, j = lane % kLanes;
   const int sides = 2 * p.pool.num_kv_heads;
   const unsigned parts = (unsigned)((sides + kGroups - 1) / kGroups);
-  const unsigned unit = blockIdx.x * (kInt8Threads / 32) + threadIdx.x / 32;
+  const unsigned unit = blockIdx.x * (kWriteThreads / 32) + threadIdx.x / 32;
   const int side = (int)(unit % parts) * kGroups + lane / kLanes, h = side >> 1, kv = side & 1;
   const bool on = side < sides;
   const int64_t t0 = (int64_t)(unit / parts) * p.single_window;
@@ -251,7 +262,7 @@ __device__ __forceinline__ void write_singles(const WriteParams& p) {
       if (begins || sc.grows)
         for (int k = j; k < 1 << (l2bs - 3); k += kLanes)
           (reinterpret_cast<float*>(base) + kv)[k * (int8_tile_bytes(D) / 4)] = sc.s;
-      stg_v4(piece_at<D>(base, codes, off, j), x.codes(sc));
+      stg_v4(base + codes + place_of<D>(off) + j * 128, x.template codes<false>(sc));
     }
   }
 }
@@ -262,123 +273,156 @@ __device__ __forceinline__ void write_singles(const WriteParams& p) {
 template <typename T, int D>
 __device__ __forceinline__ void write_runs(const WriteParams& p, unsigned cta) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a step
-  constexpr int kSteps = write_steps<T>(), kWarps = kInt8Threads / 32;
+  constexpr int kSteps = write_steps<T>(), kWarps = kWriteThreads / 32;
   __shared__ uint32_t tops[2][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int team = warp / p.row_warps, rank = warp % p.row_warps;
+  const int team = warp >> p.l2_row_warps, rank = warp & (p.row_warps - 1);
   const int j = lane % kLanes;
   const int row0 = rank * kRows + lane / kLanes, step = p.row_warps * kRows;  // the lane's rows
-  const int sides = 2 * p.pool.num_kv_heads;
-  const unsigned unit = cta * (kWarps / p.row_warps) + team;
-  const unsigned parts = (unsigned)((sides + p.per - 1) / p.per);
-  const int side0 = (int)(unit % parts) * p.per, side1 = min(side0 + p.per, sides);
-  int64_t at = (int64_t)(unit / parts) * p.window;
-  const int64_t end = min(at + p.window, (int64_t)p.num_tokens);
+  const int batch = kSteps * step;  // rows that the team holds
+  const unsigned sides = 2u * p.pool.num_kv_heads;
   const int l2bs = p.pool.log2_block_size, last = (1 << l2bs) - 1;
+  // With a number that the compiler knows: one from a register takes all 16 barriers of a CTA,
+  // and four CTAs those of the SM.
   auto sync = [&]() {
     if (p.row_warps == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * p.row_warps) : "memory");
+    else if (team == 0) asm volatile("bar.sync 1, %0;" ::"r"(32 * p.row_warps) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"r"(32 * p.row_warps) : "memory");
   };
-  if (at >= end) return;  // the whole team
-  // The window's rows of the first side are on their way to L2 while its slots are read.
-  constexpr int kLines = D * sizeof(T) / 128;
-  for (int r = rank * 32 + lane; r < (int)(end - at) * kLines; r += 32 * p.row_warps)
-    prefetch_l2(reinterpret_cast<const uint8_t*>(row_of<T>(p, side0, at + r / kLines, (side0 >> 1) * D)) +
-                r % kLines * 128);
+  // The team's part of all (window, side) pairs, which are as many for each team or one more.
+  const unsigned me = cta * (kWarps >> p.l2_row_warps) + team;
+  if (me >= p.teams) return;  // the whole team
+  const unsigned first = me * p.per + min(me, p.more);
+  int left = (int)(p.per + (me < p.more ? 1 : 0));
+  unsigned window = first / sides;
+  int side0 = (int)(first - window * sides);
   int turn = 0;
-  while (at < end) {
-    // The slots from here on; the next run of two tokens or more that begins.
-    const int64_t slot = at + lane < p.num_tokens ? __ldg(p.slots + at + lane) : -1;
-    const int mine = p.block_of(slot);
-    int before = __shfl_up_sync(0xffffffffu, mine, 1), after = __shfl_down_sync(0xffffffffu, mine, 1);
-    if (lane == 0) before = p.block_at(at - 1);
-    if (lane == 31) after = p.block_at(at + 32);
-    const uint32_t starts = __ballot_sync(
-        0xffffffffu, mine >= 0 && mine != before && mine == after && at + lane < end);
-    if (!starts) {
-      at += 32;
-      continue;
-    }
-    const int skip = __ffs(starts) - 1;
-    const int block = __shfl_sync(0xffffffffu, mine, skip);
-    const uint32_t other = ~__ballot_sync(0xffffffffu, mine == block) & (0xffffffffu << skip);
-    at += skip;
-    const int seen = 32 - skip;  // slots of the run that lanes may hold
-    int n = other ? __ffs(other) - 1 - skip : seen;
-    bool begins = __any_sync(0xffffffffu, lane >= skip && lane < skip + n && ((int)slot & last) == 0);
-    if (!other)
-      for (uint32_t same = 0xffffffffu; same == 0xffffffffu;) {
-        const int64_t i = at + n + lane;
-        const int64_t s = i < p.num_tokens ? __ldg(p.slots + i) : -1;
-        same = __ballot_sync(0xffffffffu, p.block_of(s) == block);
-        const int more = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-        begins |= __any_sync(0xffffffffu, lane < more && ((int)s & last) == 0);
-        n += more;
+  for (; left > 0; ++window) {
+    const int side1 = min(side0 + left, (int)sides);
+    left -= side1 - side0;
+    unsigned at = window * p.window;
+    const unsigned num_tokens = p.num_tokens, end = min(at + p.window, num_tokens);
+    // The window's rows of the first side are on their way to L2 while its slots are read.
+    constexpr int kLines = D * sizeof(T) / 128;
+    for (unsigned t = at + (rank * 32 + lane) / kLines; t < end; t += 32 / kLines * p.row_warps)
+      prefetch_l2(row_of<T>(p, side0, t, (side0 >> 1) * D + lane % kLines * (D / kLines)));
+    while (at < end) {
+      // The slots from here on; the next run of two tokens or more that begins.
+      const int64_t slot = at + lane < num_tokens ? __ldg(p.slots + at + lane) : -1;
+      const int mine = p.block_of(slot);
+      int before = __shfl_up_sync(0xffffffffu, mine, 1), after = __shfl_down_sync(0xffffffffu, mine, 1);
+      if (lane == 0) before = p.block_at((int64_t)at - 1);
+      if (lane == 31) after = p.block_at((int64_t)at + 32);
+      const uint32_t starts = __ballot_sync(
+          0xffffffffu, mine >= 0 && mine != before && mine == after && at + lane < end);
+      if (!starts) {
+        at += 32;
+        continue;
       }
-    int offs[kSteps];  // of the lane's tokens in the block
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = row0 + i * step;
-      offs[i] = (int)__shfl_sync(0xffffffffu, (int)slot, skip + r) & last;
-      if (r >= seen && r < n) offs[i] = (int)__ldg(p.slots + at + r) & last;
-    }
-#pragma unroll 1
-    for (int side = side0; side < side1; ++side, turn ^= 1) {
-      const int kv = side & 1;
-      const int codes = kv ? int8_value_codes(D) : int8_key_codes();
-      const int64_t stride = kv ? p.value_stride : p.key_stride;
-      uint8_t* base = p.pool.cache + int8_block_offset(block, side >> 1, p.pool.num_kv_heads, l2bs, D);
-      float* head = reinterpret_cast<float*>(base) + kv;
-      const float held = *head;
-      const T* src = row_of<T>(p, side, at, (side >> 1) * D + j * 16);
-      Piece<T> x[kSteps];
-      uint32_t top = 0;
+      const int skip = __ffs(starts) - 1;
+      const int block = __shfl_sync(0xffffffffu, mine, skip);
+      const uint32_t other = ~__ballot_sync(0xffffffffu, mine == block) & (0xffffffffu << skip);
+      at += skip;
+      const int seen = 32 - skip;  // slots of the run that lanes may hold
+      int n = other ? __ffs(other) - 1 - skip : seen;
+      bool begins = __any_sync(0xffffffffu, lane >= skip && lane < skip + n && ((int)slot & last) == 0);
+      if (!other)
+        for (uint32_t same = 0xffffffffu; same == 0xffffffffu;) {
+          const unsigned i = at + n + lane;
+          const int64_t s = i < num_tokens ? __ldg(p.slots + i) : -1;
+          same = __ballot_sync(0xffffffffu, p.block_of(s) == block);
+          const int more = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+          begins |= __any_sync(0xffffffffu, lane < more && ((int)s & last) == 0);
+          n += more;
+        }
+      int places[kSteps];  // of the lane's tokens in the block
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const int r = row0 + i * step;
-        if (r < n) x[i].load(src + r * stride, p.wide);
-        else x[i].clear();
+        int off = (int)__shfl_sync(0xffffffffu, (int)slot, skip + r) & last;
+        if (r >= seen && r < n) off = (int)__ldg(p.slots + (at + r)) & last;
+        places[i] = place_of<D>(off);
       }
+      const T* rows[2];  // the lane's first, of the first head
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) top = max(top, x[i].largest());
+      for (int kv = 0; kv < 2; ++kv) rows[kv] = row_of<T>(p, kv, (int64_t)at + row0, j * 16);
+      uint8_t* const tiles = p.pool.cache + int8_block_offset(block, 0, p.pool.num_kv_heads, l2bs, D);
+      auto write = [&](auto plain) {
+        constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll 1
-      for (int r = row0 + kSteps * step; r < n; r += step) {  // rows past the team's registers
-        Piece<T> y;
-        y.load(src + r * stride, p.wide);
-        top = max(top, y.largest());
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (p.row_warps > 1) {
-        if (lane == 0) tops[turn][warp] = top;
-        sync();
-        for (int i = 0; i < p.row_warps; ++i) top = max(top, tops[turn][warp - rank + i]);
-      }
-      const Scale sc = scale_of<T>(top, held, begins);
-      if (sc.grows) {
-        // All codes of the block, those that are written below among them.
-        grow<D>(base, codes, l2bs, held, sc.s, rank * 32 + lane, p.row_warps * 32);
-        sync();  // before other lanes' codes of the new tokens
-      }
-      if (begins || sc.grows)
-        for (int i = rank * 32 + lane; i < 1 << (l2bs - 3); i += p.row_warps * 32)
-          head[i * (int8_tile_bytes(D) / 4)] = sc.s;
+        for (int side = side0; side < side1; ++side, turn ^= 1) {
+          const int kv = side & 1;
+          uint8_t* base = tiles + (size_t)(side >> 1) * (int8_tile_bytes(D) << (l2bs - 3));
+          float* head = reinterpret_cast<float*>(base) + kv;
+          const float held = kPlain ? 0.f : *head;
+          const int64_t stride = (kv ? p.value_stride : p.key_stride);
+          const T* src = (kv ? rows[1] : rows[0]) + (side >> 1) * D;
+          Piece<T> x[kSteps];
+          auto load = [&](int r0) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (row0 + i * step < n) stg_v4(piece_at<D>(base, codes, offs[i], j), x[i].codes(sc));
+            for (int i = 0; i < kSteps; ++i) {
+              const int r = r0 + i * step;
+              if (kPlain) x[i].load(src + r * stride, true);
+              else if (row0 + r < n) x[i].load(src + r * stride, p.wide);
+              else x[i].clear();
+            }
+          };
+          // Batch after batch for the maximum; the last one stays, and those before it are read
+          // again, from its end on.
+          uint32_t top = 0;
+          int r0 = 0;
 #pragma unroll 1
-      for (int r = row0 + kSteps * step; r < n; r += step) {
-        Piece<T> y;
-        y.load(src + r * stride, p.wide);
-        stg_v4(piece_at<D>(base, codes, (int)__ldg(p.slots + at + r) & last, j), y.codes(sc));
-      }
+          for (;; r0 += batch) {
+            load(r0);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) top = max(top, x[i].largest());
+            if (r0 + batch >= n) break;
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (p.row_warps > 1) {
+            if (lane == 0) tops[turn][warp] = top;
+            sync();
+            for (int i = 0; i < p.row_warps; ++i) top = max(top, tops[turn][warp - rank + i]);
+          }
+          const Scale sc = scale_of<T>(top, held, kPlain || begins);
+          uint8_t* to = base + (kv ? int8_value_codes(D) : int8_key_codes());
+          if (!kPlain && sc.grows) {
+            // All codes of the block, those that are written below among them.
+            grow<D>(base, (int)(to - base), l2bs, held, sc.s, rank * 32 + lane, p.row_warps * 32);
+            sync();  // before other lanes' codes of the new tokens
+          }
+          if (kPlain || begins || sc.grows)
+            for (int i = rank * 32 + lane; i < 1 << (l2bs - 3); i += p.row_warps * 32)
+              head[i * (int8_tile_bytes(D) / 4)] = sc.s;
+          to += j * 128;
+          const bool many = r0 > 0;
+#pragma unroll 1
+          for (;;) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              const int r = r0 + row0 + i * step;
+              if (kPlain || r < n)
+                stg_v4(to + (many ? place_of<D>((int)__ldg(p.slots + (at + r)) & last) : places[i]),
+                       x[i].template codes<kPlain>(sc));
+            }
+            if (r0 == 0) break;
+            r0 -= batch;
+            load(r0);
+          }
+        }
+      };
+      // Whole batches that begin their block, as nearly all of a prompt do, have nothing to ask.
+      if (begins && p.wide && n % batch == 0) write(std::true_type{});
+      else write(std::false_type{});
+      at += n;
     }
-    at += n;
+    side0 = 0;
   }
 }
 
 // One launch for both: CTAs that find no run of their kind are done at once.
 template <typename T, int D>
-__global__ void __launch_bounds__(kInt8Threads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kWriteThreads, write_ctas<T>())
     int8_write_kernel(const WriteParams p) {
   grid_dependents_launch();
   grid_dependency_wait();
@@ -442,31 +486,36 @@ __global__ void __launch_bounds__(kInt8Threads)
 
 template <typename T, int D>
 cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
-  constexpr int kWarps = kInt8Threads / 32, kRows = 512 / D;
+  constexpr int kWarps = kWriteThreads / 32, kRows = 512 / D;
   const int64_t n = p.num_tokens, sides = 2ll * p.pool.num_kv_heads;
   // Warps of either kind that are worth having at once (32 an SM: 64 prompts of 37 tokens 13.3 us, not
   // 11.4).
   const int64_t resident = 24ll * num_sms;
-  auto ctas = [](int64_t warps) { return (warps + kWarps - 1) / kWarps; };
   const int64_t parts = (sides + kRows - 1) / kRows;
   p.single_window = 1;
-  while (p.single_window < 32 && (n + p.single_window - 1) / p.single_window * parts > 2 * resident)
-    p.single_window *= 2;
-  p.single_ctas = (int)ctas((n + p.single_window - 1) / p.single_window * parts);
+  if (n * parts > 2 * resident)
+    while (p.single_window < 32 && (n + p.single_window - 1) / p.single_window * parts > resident)
+      p.single_window *= 2;
+  p.single_ctas = (int)(((n + p.single_window - 1) / p.single_window * parts + kWarps - 1) / kWarps);
   const int block = 1 << p.pool.log2_block_size;
   p.window = block;
-  const int64_t windows = (n + block - 1) / block;
+  const int64_t windows = (n + block - 1) / block, pairs = windows * sides;
   // Rows of a warp: as many as it holds, fewer where there are few runs.
-  p.row_warps = 1;
+  p.row_warps = 1, p.l2_row_warps = 0;
   while (p.row_warps < kWarps && (p.row_warps * write_steps<T>() * kRows < block ||
-                                  (p.row_warps * kRows < block && windows * sides * p.row_warps * 2 <= resident)))
-    p.row_warps *= 2;
-  const int64_t per = windows * sides * p.row_warps / 8192;
-  p.per = (int)(per < 1 ? 1 : per > 4 ? 4 : per);
-  const int64_t grid = p.single_ctas + ctas(windows * ((sides + p.per - 1) / p.per) * p.row_warps);
+                                  (p.row_warps * kRows < block && pairs * p.row_warps * 2 <= resident)))
+    p.row_warps *= 2, ++p.l2_row_warps;
+  // Teams share the pairs evenly, twice as many as are there at once: with as many a team that is
+  // slow ends alone (30.7 us for 25.9), with four times as many they look for runs more often.
+  const int team_ctas = kWarps / p.row_warps;  // teams of a CTA
+  const int64_t most = (int64_t)num_sms * write_ctas<T>() * team_ctas;
+  p.teams = (unsigned)(pairs < 2 * most ? pairs : 2 * most);
+  p.per = (unsigned)(pairs / p.teams);
+  p.more = (unsigned)(pairs % p.teams);
+  const int64_t grid = p.single_ctas + (p.teams + team_ctas - 1) / team_ctas;
   void* args[] = {&p};
   return launch_overlapped((const void*)int8_write_kernel<T, D>, dim3((unsigned)grid),
-                           dim3(kInt8Threads), 0, stream, args);
+                           dim3(kWriteThreads), 0, stream, args);
 }
 
 template <typename T, int D>

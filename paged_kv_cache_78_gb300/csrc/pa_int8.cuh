@@ -84,10 +84,11 @@ __device__ __forceinline__ uint32_t int8_near(float x, float inv, float* off) {
 // (relative) away from one, as both have eight bits.  One in a hundred is a tie, and x / s
 // then lies beside it, on the side that the rounding of s gives, the same for all.  So the
 // reciprocal is taken off by 2^-21 that way (int8_lean): ties fall on their side, and nothing else
-// moves past one.  0: s is m / 127 exactly, and ties are ties.
+// moves past one.  Where s is m / 127 exactly, m is 127 times a power of two, which s and its reciprocal
+// are then, and ties are ties.
 __device__ __forceinline__ float int8_lean(float m, float s, float inv) {
   const float e = fmaf(s, 127.f, -m);  // exact: the rounding of s, times 127
-  return e == 0.f ? 0.f : inv + (e > 0.f ? -inv : inv) * 0x1p-21f;
+  return e == 0.f ? inv : inv + (e > 0.f ? -inv : inv) * 0x1p-21f;
 }
 
 // Any bf16 x: the nearest whole number c, then the one nearest to c + e / s with the
@@ -101,8 +102,11 @@ __device__ __forceinline__ uint32_t int8_near_bf16(float x, float inv, float s) 
   const float r = fmaf(x, inv, kGrid);
   return __float_as_uint(fmaf(fmaf(kGrid - r, s, x), inv, r));
 }
-__device__ __forceinline__ uint32_t int8_plain(float x, float inv) {
-  return __float_as_uint(fmaf(x, inv, 12582912.f + kInt8Bias));
+// Two at a time.
+__device__ __forceinline__ void int8_plain(float x, float y, float inv, uint32_t* c) {
+  constexpr float kGrid = 12582912.f + kInt8Bias;
+  const float2 r = parts(fma2(two(x, y), two(inv, inv), two(kGrid, kGrid)));
+  c[0] = __float_as_uint(r.x), c[1] = __float_as_uint(r.y);
 }
 
 // The low bytes of four words.
