@@ -7,16 +7,16 @@
 // a second launch's work, one CTA, after all have read them.
 //
 // A sequence's weights become keys in shared memory whose unsigned order is theirs.  The
-// k-th smallest key is found by counting, three bits at a time; keys below it leave, and as many
-// of those equal to it, from the lowest index on, as are left to go.  Then the row is
-// gone through once, a chunk of a thread per entry at a time (eight chunks' entries are asked for
-// at once): what stays moves down (so that a
-// row may be its own output: nothing is written before it was read), and what leaves
+// k-th smallest key is found by counting, three bits at a time, until a value parts k keys from the
+// others or all bits are known; keys below it leave, and as many of those equal to it, from
+// the lowest index on, as are left to go.  Then the row is
+// gone through once, eight chunks of a thread per entry at a time, with one barrier: what stays moves
+// down (so that a row may be its own output: nothing is written before it was read), and what leaves
 // goes to the ring and is kept aside in shared memory for the row's end.
 // Latency is all there is to it: 256 sequences of up to 130 blocks, of which one or two leave, take
-// 6 us (launch, lengths, weights, eleven counts, entries), with lengths written in place 8; 16
-// sequences of 8192 blocks, of which three quarters leave, 21 us, half of it the counts of one
-// CTA (bit by bit 28 us, with entries asked for a chunk at a time 27).
+// 4.8 us (launch, lengths, weights, about six counts, entries; with all eleven counts and two barriers
+// a chunk 6.2), with lengths written in place 2 more; 16 sequences of 8192 blocks, of which three quarters
+// leave, 18 us, half of it the counts of one CTA (21 before, bit by bit 28).
 #include <atomic>
 #include <climits>
 
@@ -102,7 +102,8 @@ __device__ __forceinline__ void write_state(const EvictParams& p, int s, int len
 
 __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ int counts[2][32];
+  constexpr int kBatch = 8;  // chunks whose entries are on their way at once
+  __shared__ uint32_t counts[2][kBatch][32];
   __shared__ uint4 digits[2][32];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
@@ -120,17 +121,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
   }
   if (p.free_state && !totals.refused)
     ring = in_ring(p.free_state[0] + p.free_state[1] + totals.before);
-  // Exclusive count of a flag over the CTA's threads, and all of them.  One barrier a use:
-  // `which` alternates between uses, so that a use's writers have passed the barrier that the
-  // readers of the use before the last came to after they had read.
-  auto count = [&](bool flag, int which, int* all) -> int {
-    const uint32_t b = __ballot_sync(0xffffffffu, flag);
-    if (lane == 0) counts[which][warp] = __popc(b);
-    __syncthreads();
-    const int c = lane < warps ? counts[which][lane] : 0;
-    *all = __reduce_add_sync(0xffffffffu, c);
-    return __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(b & ((1u << lane) - 1));
-  };
   for (int s = s0; s < s1; ++s) {
     const int len = p.seq_lens[s];
     const int n = len < 0 ? 0 : min(blocks_of(p, len), p.max_blocks_per_seq);
@@ -187,6 +177,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
       c[2] = __reduce_add_sync(0xffffffffu, all.z);
       c[3] = __reduce_add_sync(0xffffffffu, all.w);
       uint32_t digit = 0;
+      bool all_leave = false;  // the keys of the digit
 #pragma unroll
       for (int v = 1; v < 8; ++v) {
         const int n_below = (c[v / 2] >> (16 * (v & 1))) & 0xffff;
@@ -194,13 +185,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
           digit = v;
           below = n_below;
         }
+        all_leave |= n_below == k;
       }
       kth += digit << shift;
+      // Where exactly k keys are below one of the values, the least such value parts them as well as
+      // the k-th key.  (At the top values past the third are 2^32 and more.)
+      if (all_leave && shift < 30) {
+        kth += 1u << shift;
+        below = k;
+        break;
+      }
     }
     const int equal = k - below;  // of the keys equal to it, the first so many leave
-    int gone = 0, ties = 0;       // so far
-    constexpr int kBatch = 8;     // chunks whose entries are on their way at once
-    for (int b0 = 0; b0 < n; b0 += kBatch * threads) {
+    int less = 0, ties = 0;       // so far
+    for (int b0 = 0, turn = 0; b0 < n; b0 += kBatch * threads, turn ^= 1) {
       int id[kBatch];
       float w[kBatch];
 #pragma unroll
@@ -209,23 +207,41 @@ __global__ void __launch_bounds__(kEvictThreads) evict_rows_kernel(const EvictPa
         id[c] = i < n ? ids[i] : 0;
         w[c] = i < n ? weights[i] : 0.f;
       }
+      // Keys that are less and that are equal: a bit of the thread's, and the two counts of its
+      // chunk's warps in a word (of at most 1024 a chunk).
+      uint32_t is_less = 0, is_tie = 0;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const int i = b0 + c * threads + tid;
+        bool l = false, t = false;
+        if (i >= first && i < first + m) {
+          const uint32_t key = keys[i - first];
+          l = key < kth;
+          t = key == kth;
+        }
+        is_less |= (uint32_t)l << c;
+        is_tie |= (uint32_t)t << c;
+        const uint32_t sum = __popc(__ballot_sync(0xffffffffu, l)) | __popc(__ballot_sync(0xffffffffu, t)) << 16;
+        if (lane == 0) counts[turn][c][warp] = sum;
+      }
+      // Everything of the batch is read.  One barrier a batch: the other turn's counts are
+      // written when all have passed the barrier after they read them.
+      __syncthreads();
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
         if (b0 + c * threads >= n) break;
         const int i = b0 + c * threads + tid;
-        bool less = false, tie = false;
-        if (i >= first && i < first + m) {
-          const uint32_t key = keys[i - first];
-          less = key < kth;
-          tie = key == kth;
-        }
-        int all;
-        const int tied = ties + count(tie, 1, &all);
-        ties += all;
-        const bool leaves = less || (tie && tied < equal);
-        const int before = gone + count(leaves, 0, &all);  // everything of the chunk is read
-        gone += all;
-        if (leaves) {
+        const bool l = is_less >> c & 1, t = is_tie >> c & 1;
+        const uint32_t sum = lane < warps ? counts[turn][c][lane] : 0;
+        const uint32_t of_warps = __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+        const uint32_t of_all = __reduce_add_sync(0xffffffffu, sum);
+        const uint32_t lower = (1u << lane) - 1;
+        const int tied = ties + (int)(of_warps >> 16) + __popc(__ballot_sync(0xffffffffu, t) & lower);
+        const int before = less + (int)(of_warps & 0xffff) +
+                           __popc(__ballot_sync(0xffffffffu, l) & lower) + min(tied, equal);
+        less += of_all & 0xffff;
+        ties += of_all >> 16;
+        if (l || (t && tied < equal)) {
           keys[before] = (uint32_t)id[c];  // before <= i - first: a key that was read
           if (p.free_state) p.free_blocks[in_ring(ring + before)] = id[c];
         } else if (i < n) {
