@@ -115,6 +115,29 @@ def test_equal_and_special_weights(in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("width", [40, 700, 9000])
+def test_weights_that_part_early_late_and_not_at_all(width, in_place):
+    """Rows whose k-th weight a few leading bits part from the rest (signs, exponents), only the
+    last bit does, or none; where all that may leave does."""
+    rng = np.random.default_rng(width)
+    one = np.float32(1).view(np.int32)
+    rows = [
+        np.where(np.arange(width) % 2 == 0, -1.0, 1.0),                           # signs
+        2.0 ** (np.arange(width) % 200 - 100),                                    # exponents
+        rng.permutation(one + np.arange(width, dtype=np.int32)).view(np.float32),  # last bits
+        rng.integers(0, 3, width).astype(float),                                  # ties
+        -rng.random(width) * 1e-41,                                               # numbers below the normal ones
+        np.where(rng.random(width) < 0.5, np.nan, np.inf),
+        np.where(rng.random(width) < 0.5, 0.0, -0.0),
+        rng.standard_normal(width),
+    ]
+    weights = np.stack(rows).astype(np.float32)
+    for most in (4, width // 2, width // 2 + 2, width - 1):
+        assert Evict([16 * width - r for r in range(len(rows))], most=most, first=1, last=3, weights=weights.copy(),
+                     seed=most).check(in_place, most) == (0, False)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_refused_as_a_whole(in_place):
     lens = [100, 200, 33]
     bad = [(Evict([100, 209, 33], width=13, most=3), pa.PA_DEVERR_SEQ_LEN),

@@ -145,6 +145,35 @@ def test_chunks_that_continue_blocks(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("head,hkv,block,blocks", [(64, 5, 8, 2300), (64, 3, 256, 60), (128, 2, 128, 90), (256, 1, 64, 100)])
+def test_many_runs_of_any_length(dtype, head, hkv, block, blocks):
+    """Blocks that begin with any number of tokens, many of them whole, one or none, in any order
+    with padding between them; then what is left of some, larger in every other one, so that
+    their scales grow.  More runs, heads and sides than the GPU takes at once."""
+    rng = np.random.default_rng(head + block)
+    cache = rng.integers(-128, 128, (blocks, hkv, block // 8, 16 * (head + 1)), dtype=np.int8)
+    first = np.where(rng.random(blocks) < 0.5, block, rng.integers(0, block + 1, blocks))
+    first = np.where(rng.random(blocks) < 0.1, 1, first)
+    second = np.where(first > 0, np.minimum(block, first + rng.integers(0, block + 1, blocks)), 0)
+    d, want = dev(cache), cache.copy()
+    for begin, end in ((np.zeros(blocks, int), first), (first, second)):
+        slots = []
+        for b in rng.permutation(blocks):
+            slots.append(b * block + begin[b] + rng.permutation(end[b] - begin[b]))
+            slots.append(np.full(rng.integers(0, 3) * (rng.random() < 0.3), -1))
+        slots = np.concatenate(slots).astype(np.int64)
+        n = len(slots)
+        size = np.where(slots // block % 2 == 0, 3.0, 1.0)[:, None, None] if begin.any() else 1.0
+        k = rounded(size * rng.standard_normal((n, hkv, head)), dtype)
+        v = rounded(size * rng.standard_normal((n, hkv, head)), dtype)
+        pa.pa_reshape_and_cache_int8(d, dev(k), dev(v), dev(slots))
+        int8.write(want, host(k), host(v), slots)
+    live = np.concatenate([b * block + np.arange(n) for b, n in enumerate(second)])
+    assert_pool(d.cpu().numpy(), want, live)
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_codes_round_on_the_exact_quotients(dtype):
     """Every border between two codes times scales of many mantissas, the nearest number of the type
     and its neighbours; a maximum of 127 times the scale fixes it."""
