@@ -13,7 +13,8 @@
 // tokens of a prompt 23.2 us (4.3 TB/s, 64% of the copy rate: three dependent trips a run -
 // slots, rows, codes - and about 450 instructions for 1024 elements, of which 32 warps per SM
 // hide each other's waits to 2.4 a clock; fp32 31.5 us, 5.3 TB/s; heads of 64 21, blocks of 8
-// 22, of 256 31), 128 tokens of as many sequences 2.7 us, 1024 5.3 us.
+// 22, of 256 31), 128 tokens of as many sequences 2.7 us, 1024 5.3 us, 8000 33 us (with one at a
+// time on its way to a warp 38).
 // Each kind by itself, the other kind's kernel taking it: single tokens by whole warps 17 us
 // (1024), prompts by groups 26 us (500 tokens; 2000 in blocks of 256 330 us).
 //
@@ -232,37 +233,43 @@ __device__ __forceinline__ void write_singles(const WriteParams& p) {
   // Bad slots are recorded here, by the first heads and sides.
   if (slot >= p.pool.num_slots && unit % parts == 0) record_error(p.err, PA_DEVERR_SLOT);
   const bool alone = block >= 0 && p.block_at(t - 1) != block && p.block_at(t + 1) != block;
-  for (uint32_t singles = __ballot_sync(0xffffffffu, alone); singles; singles &= singles - 1) {
-    const int i = __ffs(singles) - 1;
-    const int off = __shfl_sync(0xffffffffu, (int)slot, i) & last;
-    const bool begins = off == 0;
-    uint8_t* base = p.pool.cache;
-    float held = 0.f;
-    uint32_t top = 0;
+  uint32_t singles = __ballot_sync(0xffffffffu, alone);
+  // The next token's row and scale are on their way while a token is written.
+  uint8_t* base = p.pool.cache;
+  float held = 0.f;
+  auto fetch = [&](int i, bool row) {
     const int b = __shfl_sync(0xffffffffu, block, i);
-    if (on) {
-      base += int8_block_offset(b, h, p.pool.num_kv_heads, l2bs, D);
-      held = reinterpret_cast<const float*>(base)[kv];
-      if (!early) x.load(row_of<T>(p, side, t0 + i, h * D + j * 16), p.wide);
-      top = x.largest();
-    }
+    if (!on) return;
+    base = p.pool.cache + int8_block_offset(b, h, p.pool.num_kv_heads, l2bs, D);
+    held = reinterpret_cast<const float*>(base)[kv];
+    if (row) x.load(row_of<T>(p, side, t0 + i, h * D + j * 16), p.wide);
+  };
+  if (singles) fetch(__ffs(singles) - 1, !early);
+  for (; singles; singles &= singles - 1) {
+    const int off = __shfl_sync(0xffffffffu, (int)slot, __ffs(singles) - 1) & last;
+    const bool begins = off == 0;
+    const Piece<T> now = x;
+    uint8_t* const to = base;
+    const float old = held;
+    if (singles & (singles - 1)) fetch(__ffs(singles & (singles - 1)) - 1, true);
+    uint32_t top = on ? now.largest() : 0;
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const Scale sc = scale_of<T>(top, held, begins || !on);
+    const Scale sc = scale_of<T>(top, old, begins || !on);
     // Blocks whose scale grows, each by the whole warp.
     uint32_t growing = __ballot_sync(0xffffffffu, j == 0 && sc.grows);
     for (; growing; growing &= growing - 1) {
       const int g = __ffs(growing) - 1;
-      uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)base, g));
-      grow<D>(at, __shfl_sync(0xffffffffu, codes, g), l2bs, __shfl_sync(0xffffffffu, held, g),
+      uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)to, g));
+      grow<D>(at, __shfl_sync(0xffffffffu, codes, g), l2bs, __shfl_sync(0xffffffffu, old, g),
               __shfl_sync(0xffffffffu, sc.s, g), lane, 32);
     }
     __syncwarp();
     if (on) {
       if (begins || sc.grows)
         for (int k = j; k < 1 << (l2bs - 3); k += kLanes)
-          (reinterpret_cast<float*>(base) + kv)[k * (int8_tile_bytes(D) / 4)] = sc.s;
-      stg_v4(base + codes + place_of<D>(off) + j * 128, x.template codes<false>(sc));
+          (reinterpret_cast<float*>(to) + kv)[k * (int8_tile_bytes(D) / 4)] = sc.s;
+      stg_v4(to + codes + place_of<D>(off) + j * 128, now.template codes<false>(sc));
     }
   }
 }
