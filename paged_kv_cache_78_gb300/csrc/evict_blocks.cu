@@ -283,19 +283,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_state_kernel(const EvictP
 }  // namespace
 
 cudaError_t launch_evict_blocks(const EvictParams& params, int num_sms, cudaStream_t stream) {
+  // Raised on the first call of a device whatever its size: how much a launch may have unasked is
+  // 48 KB less the kernel's own arrays.
   static std::atomic<bool> configured[64];
   const size_t smem = (size_t)params.max_blocks_per_seq * 4;
-  if (smem > 47 * 1024) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(evict_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PA_MAX_EVICT_BLOCKS * 4);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev].load(std::memory_order_relaxed)) {
-      e = cudaFuncSetAttribute(evict_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               PA_MAX_EVICT_BLOCKS * 4);
-      if (e != cudaSuccess) return e;
-      configured[dev].store(true, std::memory_order_relaxed);
-    }
+    configured[dev].store(true, std::memory_order_relaxed);
   }
   const int threads = params.max_blocks_per_seq <= 1024 ? 256 : kEvictThreads;
   int ctas = params.num_seqs < 2 * num_sms ? params.num_seqs : 2 * num_sms;
@@ -303,8 +303,8 @@ cudaError_t launch_evict_blocks(const EvictParams& params, int num_sms, cudaStre
   EvictParams p = params;
   p.alone = p.seq_lens_out != p.seq_lens && (!p.free_state || p.free_state_out != p.free_state);
   void* args[] = {&p};
-  cudaError_t e = launch_overlapped((const void*)evict_rows_kernel, dim3((unsigned)ctas),
-                                    dim3(threads), smem, stream, args);
+  e = launch_overlapped((const void*)evict_rows_kernel, dim3((unsigned)ctas), dim3(threads), smem,
+                        stream, args);
   if (e != cudaSuccess || p.alone) return e;
   return launch_overlapped((const void*)evict_state_kernel, dim3(1),
                            dim3(p.num_seqs <= 256 ? 256 : kEvictThreads), 0, stream, args);

@@ -1,4 +1,8 @@
 """Eviction by accumulated attention weight on the GPU (exact)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -197,3 +201,27 @@ def test_rows_behind_the_batch_stay_and_calls_repeat_in_a_graph():
     assert np.array_equal(big_t[:4].cpu().numpy(), rt) and np.array_equal(big_w[:4].cpu().numpy(), rw)
     assert big_n[:4].tolist() == rn.tolist()
     assert (big_t[4:] == -3).all() and (big_w[4:] == -3).all() and (big_n[4:] == -3).all()
+
+
+FIRST_EVICTION = """
+import sys
+sys.path.insert(0, "tests")
+import test_gpu_evict as t
+
+width = int(sys.argv[1])
+for in_place in (False, True):
+    e = t.Evict([16 * width, 16 * 5000 - 3, 0], most=100, width=width, seed=width)
+    assert e.check(in_place) == (0, False)
+print("right")
+"""
+
+
+@pytest.mark.parametrize("width", [11392, 11424, 11425, 12032, 12033, 12160, 12161, 12288, 12289])
+def test_first_eviction_of_a_process_at_any_width(width):
+    """Widths about 48 KB of shared memory, which a CTA has unasked: with the kernel's own arrays
+    beside the keys (from 11425 on the limit has to be raised) and without; no call came before that
+    raised it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_EVICTION, str(width)], cwd=root, capture_output=True,
+                       text=True, timeout=280)
+    assert r.returncode == 0 and r.stdout.split()[-1] == "right", r.stderr
