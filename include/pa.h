@@ -616,7 +616,8 @@ pa_status pa_gather_cache_int8(void* key, void* value, int32_t dtype, const void
  *                      table; at most 2^32 - 1 entries, else PA_ERR_UNSUPPORTED), 0 if none does.
  * out, block_weights_out and the workspace must overlap neither each other nor anything
  * that the call reads, but for weights in place (PA_ERR_INVALID_ARG).  A sequence that
- * is recorded as PA_DEVERR_SEQ_LEN keeps the weights that it has in block_weights_out. */
+ * is recorded as PA_DEVERR_SEQ_LEN keeps the weights that it has in block_weights_out, and so do all
+ * of a call that is refused on the device or recorded as PA_DEVERR_TIMEOUT. */
 pa_status pa_decode_int8_workspace_size(const pa_cache_desc* desc, int32_t num_heads,
                                         int32_t num_seqs, int32_t max_blocks_per_seq,
                                         size_t* bytes);

@@ -47,10 +47,10 @@ __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodePara
   const unsigned blocks = (unsigned)p.num_seqs * (unsigned)p.max_blocks_per_seq;  // below 2^32
   grid_dependents_launch();
   grid_dependency_wait();
+  const uint2 state = *reinterpret_cast<const uint2*>(p.counters + kInt8GaveUp);  // gave up, refused
   for (unsigned at = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at < blocks;) {
     const unsigned s = at / (unsigned)p.max_blocks_per_seq;
     const int b = (int)(at - s * (unsigned)p.max_blocks_per_seq);
-    const bool refused = p.counters[kInt8HeaderBytes / 4 - 1];  // the call as a whole
     const int len = p.seq_lens[s];
     const float old = p.block_weights ? p.block_weights[at] : 0.f;
     const float2* row = p.rows + (size_t)s * p.num_heads;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodePara
       r = row[lane];
       v = cell[lane];
     }
-    const bool there = !refused && len > 0 && (len - 1) >> l2bs < p.max_blocks_per_seq &&
+    const bool there = !(state.x | state.y) && len > 0 && (len - 1) >> l2bs < p.max_blocks_per_seq &&
                        b <= (len - 1) >> l2bs;
     if (there) {
       const int n = min(per_block, ((len - 1) >> l2cell) + 1 - b * per_block);
@@ -83,6 +83,14 @@ __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodePara
     }
     if (blocks - at <= (unsigned)warps) break;
     at += warps;
+  }
+  if (state.x) {
+    // The next call's weights are added up again: the last CTA that has seen the word clears it.
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(p.counters + kInt8Seen, 1u) == gridDim.x - 1) {
+      p.counters[kInt8Seen] = 0u;
+      p.counters[kInt8GaveUp] = 0u;
+    }
   }
 }
 

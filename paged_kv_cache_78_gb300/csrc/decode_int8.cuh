@@ -11,8 +11,13 @@ constexpr int kInt8MostWarps = 16;      // of a CTA; one CTA per SM
 constexpr int kInt8Gather = 16;         // parts that are merged at once
 constexpr int kInt8MaxCtas = kInt8Gather * kInt8Gather;
 constexpr int kInt8Rows = 16;           // heads of a unit at most, each merged by itself
-// Counters; the header's last word says that a call was refused on the device.
+// Counters; then, in the header's last words, what keeps the blocks' weights from being added up: the
+// call was refused on the device (each call writes it), a wait of it gave up (set by the warp, cleared
+// by the sums' launch), and how many CTAs of that launch have seen the latter.
 constexpr int kInt8HeaderBytes = kInt8MaxCtas * 3 * kInt8Rows * 4 + 256;
+constexpr int kInt8Refused = kInt8HeaderBytes / 4 - 1;
+constexpr int kInt8GaveUp = kInt8HeaderBytes / 4 - 2;
+constexpr int kInt8Seen = kInt8HeaderBytes / 4 - 3;
 
 // Warps of a CTA: 16 where a thread's accumulators and query fragments leave room in 128
 // registers, which hide each other's waits (heads of 64: 64 sequences of up to 2048 tokens with
@@ -67,7 +72,7 @@ struct Int8DecodeParams {
   const float* block_weights;  // may be NULL
   float* block_weights_out;    // NULL: no weights
   unsigned int* err;
-  unsigned int* counters;  // [CTAs][3][kInt8Rows], zero between calls
+  unsigned int* counters;  // [CTAs][3][kInt8Rows], zero between calls; the header's last words
   float* warp_partials;    // [CTAs][warps][partial]
   float* cta_partials;     // [CTAs][4][partial]: of CTAs, then of groups of CTAs
   float* chains;           // [CTAs][warps][int8_chain_floats]

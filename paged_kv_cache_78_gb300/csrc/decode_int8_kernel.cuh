@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Int8Config<T, D, H, kWeights>::kThreads, 1)
     pre[tid] = (int)base + sum - mine;
     if (tid == 0 && blockIdx.x == 0) {
       if (most) record_error(p.err, PA_DEVERR_SEQ_LEN);
-      if (kWeights) p.counters[kInt8HeaderBytes / 4 - 1] = most;  // no weights to add up
+      if (kWeights) p.counters[kInt8Refused] = most;  // no weights to add up
     }
     total = most ? 0 : (int)all;
     pairs = __reduce_add_sync(0xffffffffu, lane < W ? warp_seqs[lane] : 0) * per_seq;
@@ -821,7 +821,9 @@ __global__ void __launch_bounds__(Int8Config<T, D, H, kWeights>::kThreads, 1)
       }
     }
     if (!ok) {
-      // A wait gave up: this warp's copies in flight end before it leaves.
+      // A wait gave up: cells and rows of this call are missing, and the weights stay.
+      if (kWeights && lane == 0) p.counters[kInt8GaveUp] = 1u;
+      // This warp's copies in flight end before it leaves.
       // Slot i's last copy is its (issued - 1 - i) / NS + 1-th.
       for (int i = 0; i < NS && i < issued; ++i)
         mbar_wait_bounded(bars + 8u * i, ((issued - 1 - i) / NS) & 1, p.err);

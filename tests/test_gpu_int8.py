@@ -926,3 +926,50 @@ def test_decode_waits_that_give_up_leave_the_workspace_usable():
     for _ in range(2):
         assert torch.equal(call(), first)
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("heads,in_place", [(16, True), (16, False), (8, True)])
+def test_waits_that_give_up_leave_the_weights(heads, in_place):
+    """The sums of the blocks' weights need every cell and row of the call: where a wait gave up
+    the weights stay, as they last over steps; the next call's are right again."""
+    head, hkv, block, lens = 128, 8, 16, [120_000, 5, 0, 60_001]
+    counts = [-(-n // block) for n in lens]
+    cache = torch.randint(-128, 128, (sum(counts), hkv, block // 8, 16 * (head + 1)), dtype=torch.int8,
+                          device="cuda")
+    cache.view(torch.uint8)[..., :8] = torch.tensor([0.01, 0.02], device="cuda").view(torch.uint8)
+    tables = torch.zeros((4, max(counts)), dtype=torch.int32)
+    ids, at = torch.randperm(sum(counts)).int(), 0
+    for r, c in enumerate(counts):
+        tables[r, :c] = ids[at:at + c]
+        at += c
+    tables, lens = tables.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn((4, heads, head), device="cuda").bfloat16()
+    ws = pa.alloc_workspace(pa.pa_decode_int8_workspace_size(cache, heads, tables), "cuda")
+    before = torch.rand(tables.shape, device="cuda")
+
+    def call(weights=True):
+        w, new = before.clone(), None if in_place else torch.full_like(before, 7.0)
+        kw = dict(block_weights=w, block_weights_out=new, decay=0.5) if weights else {}
+        out = torch.empty_like(q)
+        pa.pa_decode_int8(out, q, cache, tables, lens, head ** -0.5, ws, **kw)
+        assert in_place or torch.equal(w, before)
+        return out, w if in_place else new
+
+    out, first = call()
+    assert pa.pa_get_device_error() == 0 and torch.isfinite(first).all()
+    mine = torch.arange(tables.shape[1], device="cuda") < torch.tensor(counts, device="cuda")[:, None]
+    added = (first - 0.5 * before)[mine].double().sum()
+    assert abs(added - 3 * heads) < 1e-3 * heads              # each row's attention once
+    kept = before if in_place else torch.full_like(before, 7.0)
+    for calls in ((True,), (True, True), (False,), (False, True)):   # with weights or without
+        pa.pa_set_decode_wait_limit(1)
+        try:
+            for weights in calls:
+                assert torch.equal(call(weights)[1], kept)
+                assert pa.pa_get_device_error() == pa.PA_DEVERR_TIMEOUT
+        finally:
+            pa.pa_set_decode_wait_limit(0)
+        for _ in range(2):
+            got = call()
+            assert torch.equal(got[0], out) and torch.equal(got[1], first)
+    assert pa.pa_get_device_error() == 0
