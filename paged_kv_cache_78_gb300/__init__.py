@@ -632,6 +632,14 @@ def _too_large(n) -> ValueError:
     return ValueError("%d is past 2^31 - 1" % n)
 
 
+def _int32(n) -> int:
+    """n, which ctypes would cut to 32 bits (a large or a very negative one could pass for a valid one)."""
+    n = int(n)
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError("%d is outside 32 bits" % n)
+    return n
+
+
 def _on(stream, dev: int) -> int:
     return _cuda_raw_stream(dev) if stream is None else _stream(stream)
 
@@ -689,7 +697,7 @@ def pa_decode_fp4_workspace_size(cache_or_desc, num_heads: int) -> int:
     desc = (cache_or_desc if isinstance(cache_or_desc, CacheDesc)
             else fp4_cache_desc(cache_or_desc))
     out = ctypes.c_size_t()
-    _check(lib.pa_decode_fp4_workspace_size(ctypes.byref(desc), int(num_heads), ctypes.byref(out)),
+    _check(lib.pa_decode_fp4_workspace_size(ctypes.byref(desc), _int32(num_heads), ctypes.byref(out)),
            "pa_decode_fp4_workspace_size")
     return out.value
 
@@ -754,6 +762,7 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
                   0 if free_blocks is None else free_blocks.shape[0])
     if largest > 0x7FFFFFFF:
         raise _too_large(largest)
+    block_size, num_blocks = _int32(block_size), _int32(num_blocks)
     dev = _current_device(block_tables, "block_tables")
     i32 = torch.int32
     lens = lens_out = _arg(seq_lens, "seq_lens", i32, dev)
@@ -774,7 +783,7 @@ def pa_extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor,
             state_out = _arg(free_state_out, "free_state_out", i32, dev)
     _check(lib.pa_extend_tables(
         _arg(block_tables, "block_tables", i32, dev), tables[1], lens,
-        _arg(new_tokens, "new_tokens", i32, dev), n, int(block_size), int(num_blocks), ring, capacity,
+        _arg(new_tokens, "new_tokens", i32, dev), n, block_size, num_blocks, ring, capacity,
         state, lens_out, state_out, _arg(slot_mapping, "slot_mapping", torch.int64, dev),
         None if positions is None else _arg(positions, "positions", i32, dev),
         None if token_starts is None else _arg(token_starts, "token_starts", i32, dev),
@@ -841,7 +850,7 @@ def pa_decode_int8_workspace_size(cache_or_desc, num_heads: int,
     if max(seqs, blocks) > 0x7FFFFFFF:
         raise _too_large(max(seqs, blocks))
     out = ctypes.c_size_t()
-    _check(lib.pa_decode_int8_workspace_size(ctypes.byref(desc), int(num_heads), seqs, blocks,
+    _check(lib.pa_decode_int8_workspace_size(ctypes.byref(desc), _int32(num_heads), seqs, blocks,
                                              ctypes.byref(out)), "pa_decode_int8_workspace_size")
     return out.value
 
@@ -918,6 +927,8 @@ def pa_evict_blocks(block_tables: torch.Tensor, block_weights: torch.Tensor,
                   0 if free_blocks is None else free_blocks.shape[0])
     if largest > 0x7FFFFFFF:
         raise _too_large(largest)
+    block_size, max_blocks = _int32(block_size), _int32(max_blocks)
+    keep_first, keep_last = _int32(keep_first), _int32(keep_last)
     dev = _current_device(block_tables, "block_tables")
     i32 = torch.int32
 
@@ -939,10 +950,9 @@ def pa_evict_blocks(block_tables: torch.Tensor, block_weights: torch.Tensor,
         if free_blocks.dim() != 1:
             raise ValueError("free_blocks must be [capacity]")
         ring, capacity = _arg(free_blocks, "free_blocks", i32, dev), free_blocks.shape[0]
-    _check(lib.pa_evict_blocks(t, w, tables[1], lens, n, int(block_size), int(max_blocks),
-                               int(keep_first), int(keep_last), ring, capacity, state, gone, t_out,
-                               w_out, lens_out, state_out, gone_out, _on(stream, dev)),
-           "pa_evict_blocks")
+    _check(lib.pa_evict_blocks(t, w, tables[1], lens, n, block_size, max_blocks, keep_first,
+                               keep_last, ring, capacity, state, gone, t_out, w_out, lens_out,
+                               state_out, gone_out, _on(stream, dev)), "pa_evict_blocks")
 
 
 def pa_norm_rope(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Tensor,

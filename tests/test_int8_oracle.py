@@ -448,6 +448,27 @@ def test_sizes_past_32_bits_are_refused():
         pa.pa_norm_rope(rows, rows, rows, rows, None, None, None, meta(big))
 
 
+def test_numbers_outside_32_bits_are_refused():
+    """Negative ones that would be cut to a small positive number, and counts of heads."""
+    meta = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="meta")
+    t, w, lens = meta(1, 4), meta(1, 4, dtype=torch.float32), meta(1)
+    small = -(1 << 32)
+    for kw in (dict(size=small + 16), dict(most=small + 3), dict(first=small + 1), dict(last=small + 1),
+               dict(first=-(1 << 31) - 1)):
+        with pytest.raises(ValueError, match="outside 32 bits"):
+            pa.pa_evict_blocks(t, w, lens, kw.get("size", 16), kw.get("most", 3), kw.get("first", 1),
+                               kw.get("last", 1))
+    for kw in (dict(size=small + 16), dict(blocks=small + 8)):
+        with pytest.raises(ValueError, match="outside 32 bits"):
+            pa.pa_extend_tables(t, lens, lens, kw.get("size", 16), kw.get("blocks", 8), meta(1, dtype=torch.int64))
+    int8_desc, fp4_desc = desc(), pa.CacheDesc(8, 16, 2, 64, pa.PA_FP4)
+    for heads in ((1 << 32) + 4, small + 4):
+        with pytest.raises(ValueError, match="past 2|outside 32 bits"):
+            pa.pa_decode_int8_workspace_size(int8_desc, heads)
+        with pytest.raises(ValueError, match="past 2|outside 32 bits"):
+            pa.pa_decode_fp4_workspace_size(fp4_desc, heads)
+
+
 def test_workspace_size_refusals():
     out = ctypes.c_size_t()
     call = lambda d, h, s=0, b=0: pa.lib.pa_decode_int8_workspace_size(ctypes.byref(d), h, s, b, ctypes.byref(out))
