@@ -601,7 +601,10 @@ pa_status pa_gather_cache_int8(void* key, void* value, int32_t dtype, const void
  *     block_weights_out[s][b] = decay * block_weights[s][b]
  *                               + sum over query heads and tokens j of block b of softmax_j
  * for the blocks b of sequence s (b < ceil(seq_lens[s] / block_size)); what lies behind
- * stays as it was.  Sums are fp32, in a fixed order.
+ * stays as it was.  Sums are fp32, in a fixed order.  The call cannot tell a new sequence
+ * from one that goes on: whoever gives a row of the tables to a new sequence sets the row's
+ * weights to zero (and its evicted_tokens, see pa_evict_blocks), or its blocks inherit the attention that
+ * the sequence before got, and eviction takes the wrong ones.
  *   block_weights_out  device fp32 [num_seqs][max_blocks_per_seq], laid out as the tables;
  *                      NULL: no weights are kept.
  *   block_weights      likewise, the weights before the step; the same buffer (in place) or
@@ -641,7 +644,7 @@ pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t qu
  *     seq_lens[s]              less block_size for each block that left
  *     evicted_tokens[s]        more by as much, so that a token's position is its place
  *                              in the sequence plus evicted_tokens[s] (pa_norm_rope's
- *                              position_offsets)
+ *                              position_offsets; a new sequence in row s begins with zero)
  *     the ring of free blocks  (pa_extend_tables) at its end: the blocks that left,
  *                              sequence after sequence
  * The blocks must not be shared with other sequences.

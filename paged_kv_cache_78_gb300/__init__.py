@@ -863,7 +863,8 @@ def pa_decode_int8(out: torch.Tensor, query: torch.Tensor, cache: torch.Tensor,
     """pa_decode over an 8-bit pool; query (rows may lie apart) and out are bf16
     or fp32.  With block_weights (fp32, the tables' shape) the attention that
     each block gets is added to decay times what it holds (in place unless
-    block_weights_out is given; that alone starts from zeros).  The launches depend on the shapes
+    block_weights_out is given; that alone starts from zeros); whoever gives a row to
+    a new sequence sets its weights to zero.  The launches depend on the shapes
     alone, so that a captured call serves sequences as they grow."""
     _, desc, _, size = _int8_pool(cache)
     s, hq, d = query.shape

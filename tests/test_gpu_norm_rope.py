@@ -245,6 +245,70 @@ def test_captured_step_serves_sequences_that_lose_blocks(dtype, heads, hkv, head
     assert (total > most * block).all() and pa.pa_get_device_error() == 0
 
 
+def test_a_row_that_a_new_sequence_takes_begins_at_zero():
+    """A captured step; both rows' sequences end, and others take the rows with weights and
+    evicted tokens set to zero: every later step is what it is for the same sequences in rows that
+    no other had before, bit for bit, evictions among it."""
+    block, most, heads, hkv, head, width, blocks, s = 8, 4, 4, 2, 64, 6, 24, 2
+    rng = np.random.default_rng(31)
+    i32 = lambda a: dev(np.asarray(a), torch.int32)
+    cs, one = dev(table(200, head)), i32([1] * s)
+    qkv = torch.zeros((s, heads + 2 * hkv, head), dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv.split([heads, hkv, hkv], dim=1)
+
+    class Server:
+        def __init__(self):
+            self.cache = pa.alloc_int8_cache(blocks, block, hkv, head)
+            self.tables = torch.zeros((s, width), dtype=torch.int32, device="cuda")
+            self.lens, self.gone, self.pos = i32([0] * s), i32([0] * s), i32([0] * s)
+            self.ring, self.state = i32(np.arange(blocks)), i32([0, blocks])
+            self.weights = torch.zeros((s, width), device="cuda")
+            self.slots = torch.empty(s, dtype=torch.int64, device="cuda")
+            self.q, self.k = torch.empty_like(q.contiguous()), torch.empty_like(k.contiguous())
+            self.out = torch.empty_like(self.q)
+            self.ws = pa.alloc_workspace(pa.pa_decode_int8_workspace_size(self.cache, heads, self.tables), "cuda")
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                self.step()
+
+        def step(self):
+            pa.pa_evict_blocks(self.tables, self.weights, self.lens, block, most, 1, 1, self.ring, self.state,
+                               self.gone)
+            pa.pa_extend_tables(self.tables, self.lens, one, block, blocks, self.slots, positions=self.pos,
+                                free_blocks=self.ring, free_state=self.state)
+            pa.pa_norm_rope(self.q, self.k, q, k, None, None, cs, self.pos, position_offsets=self.gone)
+            pa.pa_reshape_and_cache_int8(self.cache, self.k, v, self.slots)
+            pa.pa_decode_int8(self.out, self.q, self.cache, self.tables, self.lens, head ** -0.5, self.ws,
+                              block_weights=self.weights, decay=0.9)
+
+        def begin(self, row):
+            """The row's blocks go back to the ring; a new sequence has none."""
+            n = -(-int(self.lens[row]) // block)
+            front, count = self.state.tolist()
+            for i in range(n):
+                self.ring[(front + count + i) % blocks] = self.tables[row, i]
+            self.state[1] += n
+            self.lens[row], self.gone[row], self.weights[row] = 0, 0, 0.0
+
+        def seen(self):
+            lens = self.lens.tolist()
+            return lens, self.gone.tolist(), [self.weights[r, :-(-n // block)].tolist() for r, n in enumerate(lens)]
+
+    rows = lambda: rounded(rng.standard_normal(tuple(qkv.shape)), "bf16")
+    old, fresh = Server(), Server()
+    for _ in range(block * most + 2 * block + 3):
+        qkv.copy_(rows())
+        old.graph.replay()
+    assert min(old.gone.tolist()) > 0 and (old.weights[:, :most] > 0).all()
+    old.begin(0), old.begin(1)
+    assert old.state.tolist()[1] == blocks
+    for i in range(block * most + 3 * block + 1):             # long enough to lose blocks again
+        qkv.copy_(rows())
+        old.graph.replay(), fresh.graph.replay()
+        assert torch.equal(old.out, fresh.out) and old.seen() == fresh.seen(), i
+    assert min(old.gone.tolist()) > 0 and pa.pa_get_device_error() == 0
+
+
 FIRST_CALLS = """
 import torch
 import paged_kv_cache_78_gb300 as pa
