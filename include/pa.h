@@ -699,7 +699,9 @@ pa_status pa_evict_blocks(const int32_t* block_tables, const float* block_weight
  *   position_offsets    device int32 [num_tokens] or NULL: added to the positions (for one
  *                       token a sequence, pa_evict_blocks' evicted_tokens).
  * A position outside [0, max_position) after that records PA_DEVERR_POSITION and leaves its
- * token's rows as they were (with rotary_dim 0 none is).  What is written must not overlap what is
+ * token's rows as they were (with rotary_dim 0 none is): evicted tokens count, so that a sequence
+ * that loses blocks reaches the table's end all the same, and what reads its rows behind the call
+ * reads an earlier token's.  What is written must not overlap what is
  * read, or each other, but for rows in place (PA_ERR_INVALID_ARG).  head_size is 64, 128 or 256
  * (else PA_ERR_UNSUPPORTED).  num_tokens == 0 is a no-op. */
 typedef struct pa_norm_rope_args {
