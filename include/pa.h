@@ -652,7 +652,10 @@ pa_status pa_decode_int8(void* out, const void* query, int32_t dtype, int64_t qu
  *   max_blocks   >= keep_first + keep_last; keep_first >= 0; keep_last >= 1 (the last
  *                block, which may be partly filled, always stays).
  *   free_blocks, free_capacity, free_state   the ring; free_blocks is written.  All NULL / 0: the
- *                host finds the blocks that left in the tables.
+ *                host finds the blocks that left in the tables, and gives them to whatever it takes
+ *                blocks from.  That is not a pa_pool_*: no call of it takes a block out of the middle of
+ *                a sequence, so sequences that lose blocks live in tables and ring, without the
+ *                pool's forks, prefix cache and swaps.
  *   evicted_tokens   device int32 [num_seqs], or NULL with evicted_tokens_out.
  *   ..._out      the state after the call; each may be its input (in place), or other
  *                memory (of which the same entries are written).
@@ -689,7 +692,8 @@ pa_status pa_evict_blocks(const int32_t* block_tables, const float* block_weight
  *                       elements apart (slices of a fused projection's output, say).
  *   query_out, key_out  likewise; each may be its input (in place, the same stride).
  *                       Pointers and strides are multiples of 16 bytes.
- *   query_weight, key_weight  device [head_size] of `dtype`, 16-byte aligned; NULL: ones.
+ *   query_weight, key_weight  device [head_size] of `dtype`, 16-byte aligned; NULL: ones (rows are
+ *                       normed all the same).
  *   eps                 finite, >= 0.
  *   cos_sin             device fp32 [max_position][rotary_dim], 16-byte aligned: the cosines, then
  *                       the sines, of a position's angles (of whatever scaling the model has).
