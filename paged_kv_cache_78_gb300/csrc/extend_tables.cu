@@ -181,19 +181,19 @@ __global__ void __launch_bounds__(kTablesThreads) extend_tables_kernel(const Tab
 }  // namespace
 
 cudaError_t launch_extend_tables(const TablesParams& params, int num_sms, cudaStream_t stream) {
+  // Raised on the first call of a device whatever its size: how much a launch may have unasked is
+  // 48 KB less the kernel's own arrays.
   static std::atomic<bool> configured[64];
   const size_t smem = (size_t)(2 * params.num_seqs + 1) * 4;
-  if (smem > 47 * 1024) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (2 * PA_MAX_TABLE_REQUESTS + 1) * 4);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev].load(std::memory_order_relaxed)) {
-      e = cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (2 * PA_MAX_TABLE_REQUESTS + 1) * 4);
-      if (e != cudaSuccess) return e;
-      configured[dev].store(true, std::memory_order_relaxed);
-    }
+    configured[dev].store(true, std::memory_order_relaxed);
   }
   // A CTA takes 4096 tokens in one pass.  In place, where a cluster's barrier is
   // needed, eight CTAs are the most that every GPU allows; otherwise all SMs (500
