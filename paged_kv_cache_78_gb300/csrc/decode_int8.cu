@@ -36,53 +36,54 @@ Layout layout(int head_size, int num_heads, int group, int log2_block_size, size
 
 // A block's weight: the sum over heads and cells of weights / the row's sum, at the row's
 // maximum.  A warp takes a block, lanes the heads, so that a cell's are read in one piece;
-// 8 bytes per cell and head, written by the decode's kernel just before.  Everything is asked
-// for at once, whether the block is there or not: the addresses are in the workspace anyway.
+// 8 bytes per cell and head, written by the decode's kernel just before.  Which of the tables' entries
+// are blocks is known from the lengths: a warp looks at 32 of its entries at once, a lane each, and
+// goes on with those that are there, so that the width of a table costs a length per entry, 32 at a
+// time, and no cell is read but the sequences' own.
 __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodeParams p) {
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (blockDim.x / 32);
+  const unsigned warps = gridDim.x * (blockDim.x / 32), width = (unsigned)p.max_blocks_per_seq;
   const int l2bs = p.log2_block_size, l2cell = int8_log2_cell(l2bs);
   const int per_block = 1 << (l2bs - l2cell);
   const int64_t cells = (int64_t)p.max_blocks_per_seq * per_block;
-  const unsigned blocks = (unsigned)p.num_seqs * (unsigned)p.max_blocks_per_seq;  // below 2^32
+  const unsigned blocks = (unsigned)p.num_seqs * width;  // below 2^32
   grid_dependents_launch();
   grid_dependency_wait();
   const uint2 state = *reinterpret_cast<const uint2*>(p.counters + kInt8GaveUp);  // gave up, refused
-  for (unsigned at = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at < blocks;) {
-    const unsigned s = at / (unsigned)p.max_blocks_per_seq;
-    const int b = (int)(at - s * (unsigned)p.max_blocks_per_seq);
-    const int len = p.seq_lens[s];
-    const float old = p.block_weights ? p.block_weights[at] : 0.f;
-    const float2* row = p.rows + (size_t)s * p.num_heads;
-    const float2* cell = p.cells + (s * cells + (int64_t)b * per_block) * p.num_heads;
-    float2 r = make_float2(0.f, 1.f), v = make_float2(0.f, 0.f);
-    if (lane < p.num_heads) {
-      r = row[lane];
-      v = cell[lane];
+  for (uint64_t at0 = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at0 < blocks; at0 += 32ull * warps) {
+    const uint64_t mine = at0 + (uint64_t)lane * warps;
+    unsigned my_s = 0;
+    int my_b = 0, my_len = 0;
+    bool there = false;
+    if (mine < blocks) {
+      my_s = (unsigned)mine / width;
+      my_b = (int)((unsigned)mine - my_s * width);
+      my_len = p.seq_lens[my_s];
+      const int last = (my_len - 1) >> l2bs;
+      there = !(state.x | state.y) && my_len > 0 && last < p.max_blocks_per_seq && my_b <= last;
     }
-    const bool there = !(state.x | state.y) && len > 0 && (len - 1) >> l2bs < p.max_blocks_per_seq &&
-                       b <= (len - 1) >> l2bs;
-    if (there) {
+    for (uint32_t left = __ballot_sync(0xffffffffu, there); left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const unsigned s = __shfl_sync(0xffffffffu, my_s, i), at = (unsigned)at0 + i * warps;
+      const int b = __shfl_sync(0xffffffffu, my_b, i), len = __shfl_sync(0xffffffffu, my_len, i);
+      const float old = p.block_weights ? p.block_weights[at] : 0.f;
+      const float2* row = p.rows + (size_t)s * p.num_heads;
+      const float2* cell = p.cells + (s * cells + (int64_t)b * per_block) * p.num_heads;
       const int n = min(per_block, ((len - 1) >> l2cell) + 1 - b * per_block);
       float sum = 0.f;
       for (int h = lane; h < p.num_heads; h += 32) {
-        if (h != lane) {
-          r = row[h];
-          v = cell[h];
-        }
-        float mine = v.x * fast_exp2(v.y - r.x);
+        const float2 r = row[h], v = cell[h];
+        float weight = v.x * fast_exp2(v.y - r.x);
         for (int c = 1; c < n; ++c) {
           const float2 u = cell[(size_t)c * p.num_heads + h];
-          mine = fmaf(u.x, fast_exp2(u.y - r.x), mine);
+          weight = fmaf(u.x, fast_exp2(u.y - r.x), weight);
         }
-        sum += __fdiv_rn(mine, r.y);
+        sum += __fdiv_rn(weight, r.y);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) p.block_weights_out[at] = fmaf(p.decay, old, sum);
     }
-    if (blocks - at <= (unsigned)warps) break;
-    at += warps;
   }
   if (state.x) {
     // The next call's weights are added up again: the last CTA that has seen the word clears it.

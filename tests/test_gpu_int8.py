@@ -973,3 +973,53 @@ def test_waits_that_give_up_leave_the_weights(heads, in_place):
             got = call()
             assert torch.equal(got[0], out) and torch.equal(got[1], first)
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("width,seqs", [(40, 3), (5000, 70), (8192, 300)])
+def test_weights_over_tables_wider_than_the_sequences(width, seqs):
+    lens = np.random.default_rng(width).integers(0, 300, seqs)
+    lens[:3] = [0, 16 * min(width, 40), 1]
+    r = Run(Batch(lens, 4, 2, 64, 16, seed=width, width=width), decay=0.5)
+    r.check()
+    r.lens[2] = 16 * width + 1                                # past its row: its weights stay
+    r.batch.lens[2] = 0
+    r.new.fill_(5.0)
+    ref = r.batch.reference()
+    r()
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_SEQ_LEN
+    assert_weights(r.new, r.batch, r.batch.old, 0.5, np.full(r.batch.old.shape, 5.0), reference=ref)
+
+
+def test_weights_cost_what_the_sequences_have_not_what_the_tables_could():
+    """256 sequences of seven blocks in tables of 8192 columns: at most three times as long as in tables
+    that just hold them (a length per entry is looked at; reading every entry's cells takes 14 times as
+    long)."""
+    seqs, tokens, heads, hkv, head = 256, 100, 32, 8, 128
+    n = -(-tokens // 16)
+    cache = pa.alloc_int8_cache(seqs * n, 16, hkv, head)
+    q = torch.randn((seqs, heads, head), device="cuda").bfloat16()
+    out, lens = torch.empty_like(q), torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")
+
+    def us(width):
+        t = torch.zeros((seqs, width), dtype=torch.int32, device="cuda")
+        t[:, :n] = torch.arange(seqs * n, device="cuda").int().view(seqs, n)
+        w = torch.zeros(t.shape, device="cuda")
+        ws = pa.alloc_workspace(pa.pa_decode_int8_workspace_size(cache, heads, t), "cuda")
+        call = lambda: pa.pa_decode_int8(out, q, cache, t, lens, head ** -0.5, ws, block_weights=w)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                call()
+        best = float("inf")
+        for _ in range(8):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            g.replay()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert us(8192) < 3 * us(n)
