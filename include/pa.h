@@ -592,9 +592,13 @@ pa_status pa_gather_cache_int8(void* key, void* value, int32_t dtype, const void
 /* Decode attention over an 8-bit pool: pa_decode's operation on the numbers that the
  * pool holds.  out, query, tables, lengths, scale, groups (<= 16), the limit on the work
  * and the errors are pa_decode_fp4's, and so is what a captured call may rely on: the
- * launches depend on the shapes alone.  Queries and weights of the values enter their
- * products as in pa_decode_fp4, codes exactly; a weight is off by up to 2^-32 (fp32
- * outputs: 2^-36) of the largest, in units of the sequence's largest value scale.
+ * launches depend on the shapes alone.  Codes enter their products exactly, and so do
+ * bf16 queries; fp32 queries are two fp16 parts.  A weight of a value, times the value's scale, is
+ * rounded to one fp16 number for bf16 outputs (by up to 2^-11 of it; a bf16 output has 2^-8, and one in
+ * eleven comes out as the other bf16 number beside the exact result), to two fp16 parts for fp32
+ * outputs, and is off by up to 2^-32 (fp32 outputs: 2^-36) of the largest besides, in units of the
+ * sequence's largest value scale.  Maxima, sums of weights and sums over tokens are fp32: the matrix unit's after
+ * each 16 or 32 tokens, added with rounding, in chains of at most 4096 tokens.
  *
  * The attention that each block of a sequence gets can be added up over the steps, for
  * pa_evict_blocks:

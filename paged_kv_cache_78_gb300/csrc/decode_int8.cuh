@@ -20,11 +20,11 @@ constexpr int kInt8GaveUp = kInt8HeaderBytes / 4 - 2;
 constexpr int kInt8Seen = kInt8HeaderBytes / 4 - 3;
 
 // Warps of a CTA: 16 where a thread's accumulators and query fragments leave room in 128
-// registers, which hide each other's waits (heads of 64: 64 sequences of up to 2048 tokens with
-// weights 16.2 us, 17.9 with 8; fp32 50.6 and 57.5; 8 x 32768 tokens of 128 with weights 91.0 and
-// 93.4), else 8.  But 8 for heads of 128 where no weights are kept: they copy 8 KB at a time,
-// not 4, which the memory gives faster (84.4 and 86.0 us, 384 x 1500 tokens 186 and 194), and for
-// fp32 of 128 (85 and 92), whose registers would spill.
+// registers, which hide each other's waits (with 8, 64 sequences of up to 2048 tokens with weights and
+// heads of 64 take 10% longer, fp32 14%, 8 x 32768 tokens of 128 with weights 3%), else 8.
+// But 8 for heads of 128 where no weights are kept: they copy 8 KB at a time, not 4, which the
+// memory gives faster (with 16, 8 x 32768 tokens take 2% longer, 384 x 1500 4%), and for
+// fp32 of 128 (8%), whose registers would spill.
 __host__ __device__ constexpr int int8_warps(int head_size, int heads, bool fp32, bool weights) {
   return head_size == 64 ? (heads == 16 && fp32 ? 8 : 16)
                          : head_size == 128 && heads == 8 && !fp32 && weights ? 16 : 8;
@@ -39,7 +39,7 @@ __host__ __device__ constexpr int int8_step(int head_size, int warps) {
 }
 
 // Query heads of a unit of work (columns of the matrix instructions): 8, or 16 where the
-// registers hold them (16 heads of 128: 97 us where eight take 86, so twice eight would take 172);
+// registers hold them (16 heads of 128 take 13% longer than eight, not twice as long);
 // groups past eight heads of 256 elements read the keys and values once per eight heads.
 __host__ __device__ constexpr int int8_heads(int head_size, int group) {
   return group <= 8 || head_size == 256 ? 8 : 16;

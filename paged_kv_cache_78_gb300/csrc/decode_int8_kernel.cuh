@@ -22,8 +22,14 @@
 // same order.
 //
 // Two stages a warp, 132 KB on their way per SM: with three (198 KB) the memory gives less (8 x
-// 32768 tokens 84.4 us, 91 with three; 384 x 1500 186 and 204), and so it does without the
-// hint that L2 may drop the lines first (85.4; 128 sequences of up to 2100 tokens 50.2 and 53.3).
+// 32768 tokens take 8% longer, 384 x 1500 10%), and so it does without the hint that L2 may drop
+// the lines first (1%; 128 sequences of up to 2100 tokens 6%).
+//
+// Weights times value scales enter their product as one fp16 number in bf16 calls, half a step 2^-11 of
+// it, and as two in fp32 calls.  Of the bf16 outputs one in eleven is thereby the other neighbour of the exact
+// result than the one that exact weights give (1% more error against 64 bits than the output's own rounding
+// makes).  Two for bf16 as well take 0.5% longer for 8 x 32768 tokens, 1 to 5% for smaller
+// batches, 6% where the blocks' weights are kept, 16% for 16 heads a group: not taken.
 //
 // Value scales: O is kept in units of the pair's largest value scale so far (rounded up
 // to a power of two, so that nothing but the ratios' own rounding is lost), which moves with the
@@ -34,17 +40,18 @@
 // the rows' maxima and sums are known.
 //
 // Measured (graph replays in a row, data larger than L2, 6776 GB/s = 100%):
-//   8 x 32768 tokens, 32 heads on 8 of 128, bf16     84.4 us  538 MB  94%  (with weights 91 us)
-//   the same with blocks of 256                      82.3 us          96%
+//   8 x 32768 tokens, 32 heads on 8 of 128, bf16     84 us    538 MB  94%  (with weights 91 us)
+//   the same with blocks of 256                      82 us            97%
 //   the same with 64 heads, with 128 heads on 8      86, 97 us        92%, 82%
 //   the same in fp32                                 85 us            93%
-//   16 x 32768 tokens, 32 heads on 8 of 64           87 us    539 MB  92%
+//   16 x 32768 tokens, 32 heads on 8 of 64           86 us    539 MB  93%
 //   8 x 32768 tokens, 32 heads on 4 of 256           88 us    538 MB  90%
-//   384 x 1500 tokens, 32 heads on 8 of 128         186 us   1.19 GB  94%
+//   384 x 1500 tokens, 32 heads on 8 of 128         185 us   1.19 GB  95%
 //   128 sequences of 0 .. 2100 tokens                50 us    273 MB  80%  (56 us)
 //   32 sequences of 1 .. 2048 tokens, 40 heads       53 us    311 MB  86%
-//   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  13.0 us               (16.2 us)
+//   64 sequences of 0 .. 2048 tokens, 14 on 2 of 64  13.0 us               (16.8 us)
 //   four sequences of up to 100 tokens                6.1 us
+// One box differs from another by 1%.
 // What is left of the short ones is the launch (2.5 us), lengths, tables and first copies one
 // after another (4 us), steps of a lone warp (1.5 us each) and merges over CTAs (3 to 4 us);
 // 16 heads of 128 are bound by instructions (8 warps, two column tiles).
@@ -70,8 +77,8 @@ constexpr int kInt8MaxWork = (1 << 30) - 1;
 // Tokens of a chain of sums: rounded additions drop whatever is below half a step of a sum, so
 // a chain's sums are added to the piece's in global memory.
 constexpr int kInt8Chain = 4096;
-// A pair's queries and its end count as this many stages (128 sequences of up to 2100 tokens
-// 57.2 us at one, 55.4 at two; 32 of 40 pairs each 58.6 and 58.3).
+// A pair's queries and its end count as this many stages (at one, 128 sequences of up to 2100 tokens
+// take 3% longer, 32 of 40 pairs each 0.5%).
 constexpr int kInt8PairCost = 2;
 constexpr int kInt8Whole = 512;  // tokens of a pair that may stay whole with a warp (256, 1024: the same)
 

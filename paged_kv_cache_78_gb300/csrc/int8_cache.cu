@@ -10,13 +10,21 @@
 // its scale read beside the rows, and its codes read and rounded again only where it grows.
 //
 // Measured (graph replays in a row, data larger than L2), 8 heads of 128, bf16, blocks of 16: 16384
-// tokens of a prompt 23.2 us (4.3 TB/s, 64% of the copy rate: three dependent trips a run -
-// slots, rows, codes - and about 450 instructions for 1024 elements, of which 32 warps per SM
-// hide each other's waits to 2.4 a clock; fp32 31.5 us, 5.3 TB/s; heads of 64 21, blocks of 8
-// 22, of 256 31), 128 tokens of as many sequences 2.7 us, 1024 5.3 us, 8000 33 us (with one at a
-// time on its way to a warp 38).
+// tokens of a prompt 23.3 us (4.3 TB/s, 64% of the copy rate: three dependent trips a run -
+// slots, rows, codes - and about 450 instructions for 1024 elements, most of which a warp needs
+// once for a run and side, however many rows: maxima, barrier, quotients, headers; 32 warps per SM
+// hide each other's waits to 2.4 a clock; fp32 31.7 us, 5.3 TB/s; heads of 64 21.5, blocks of 8
+// 21.7, of 256 31), 128 tokens of as many sequences 2.7 us, 1024 5.3 us, 8000 29 to 33 us (with one at a
+// time on its way to a warp a sixth longer).
 // Each kind by itself, the other kind's kernel taking it: single tokens by whole warps 17 us
 // (1024), prompts by groups 26 us (500 tokens; 2000 in blocks of 256 330 us).
+//
+// These are writes whose scales stay, as those of a pass that is repeated do.  A decode batch's do not: of like
+// rows token i of a block raises each of its scales with probability 1 / (i + 1), and the codes that
+// the block holds are rounded again, a warp's growing scales one after another and each piece stored before
+// the next is asked for.  Steps as they come, 8 heads of 128 (in brackets: repeated; where
+// every scale grows): 64 sequences 11 us (3.3; 15), 256 13 us (3.8; 19), 1024 17 us (4.4; 25), 64 of 2 heads of
+// 64 6.1 us (2.6; 8.8); in blocks of 256, 64 sequences 94 us (3.4; 168), 256 132 us (5.8; 267).
 //
 // Reading back takes 16 elements of a token's key and of its value per thread: 65536 tokens
 // 61.7 us, 96% of the copy rate.
@@ -195,8 +203,8 @@ __device__ __forceinline__ const T* row_of(const WriteParams& p, int side, int64
 }
 
 // Steps of rows that a warp holds, and CTAs of an SM: bf16's 16 registers of rows leave room for
-// eight (16384 tokens of a prompt 23.4 us, 24.1 and 26.1 with seven and six, 34 with half the rows), while fp32
-// rather has its loads on their way at once (32.9 us; half the rows and seven CTAs 34.5, five CTAs 40).
+// eight (16384 tokens of a prompt take 3% and 12% longer with seven and six, 45% with half the rows), while
+// fp32 rather has its loads on their way at once (half the rows and seven CTAs 5% longer, five CTAs 22%).
 template <typename T>
 __host__ __device__ constexpr int write_steps() {
   return sizeof(T) == 2 ? 2 : 4;
@@ -495,8 +503,8 @@ template <typename T, int D>
 cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kWriteThreads / 32, kRows = 512 / D;
   const int64_t n = p.num_tokens, sides = 2ll * p.pool.num_kv_heads;
-  // Warps of either kind that are worth having at once (32 an SM: 64 prompts of 37 tokens 13.3 us, not
-  // 11.4).
+  // Warps of either kind that are worth having at once (32 an SM: 64 prompts of 37 tokens take 17%
+  // longer).
   const int64_t resident = 24ll * num_sms;
   const int64_t parts = (sides + kRows - 1) / kRows;
   p.single_window = 1;
@@ -513,7 +521,7 @@ cudaError_t launch_write(WriteParams p, int num_sms, cudaStream_t stream) {
                                   (p.row_warps * kRows < block && pairs * p.row_warps * 2 <= resident)))
     p.row_warps *= 2, ++p.l2_row_warps;
   // Teams share the pairs evenly, twice as many as are there at once: with as many a team that is
-  // slow ends alone (30.7 us for 25.9), with four times as many they look for runs more often.
+  // slow ends alone (a fifth longer), with four times as many they look for runs more often.
   const int team_ctas = kWarps / p.row_warps;  // teams of a CTA
   const int64_t most = (int64_t)num_sms * write_ctas<T>() * team_ctas;
   p.teams = (unsigned)(pairs < 2 * most ? pairs : 2 * most);

@@ -9,9 +9,9 @@
 // go through them with the same cosines; products go two to an instruction.
 //
 // Measured (graph replays in a row, data larger than L2): 16381 tokens, 32 + 8 heads of 128, bf16
-// 60.5 us (5.6 TB/s, 84% of the copy rate), fp32 99 us (6.8 TB/s, 101%); 128 tokens 2.3 us, 64 of
-// 14 + 2 heads of 64 1.7 us.  (With the next heads on their way to shared memory, two stages a
-// thread: 60.6 us, fp32 149.)
+// 60.4 us (5.7 TB/s, 84% of the copy rate), fp32 100 us (6.8 TB/s, 100%); heads of 256 55 us (8192 tokens),
+// 128 tokens 2.3 us, 64 of 14 + 2 heads of 64 1.7 us.  (With the next heads on their way to shared memory,
+// two stages a thread: the same, fp32 half as long again.)
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -19,8 +19,8 @@ namespace pa {
 
 namespace {
 
-// CTAs of four warps leave the SM's last wave the least to wait for (512 tokens of 40 heads 3.7 us;
-// 4.8 with eight warps, 4.6 with two).
+// CTAs of four warps leave the SM's last wave the least to wait for (512 tokens of 40 heads 3.7 us; 30%
+// longer with eight warps, 24% with two).
 constexpr int kRopeThreads = 128;
 
 struct RopeParams {
@@ -236,9 +236,9 @@ cudaError_t launch(const pa_norm_rope_args& args, int num_sms, unsigned int* err
   p.a = args;
   p.err = err;
   // 96 bytes of a thread (fp32 128) on their way at once where there are more rows than the GPU's
-  // threads hold: 16381 tokens of 40 heads of 128, bf16: 60.5 us with three heads a thread, 61.1 with two,
-  // 77 with one (four leave registers for fewer warps: 60.7, heads of 256 55.9 for 54.6); fp32 99 with
-  // two, 107 with one.
+  // threads hold: 16381 tokens of 40 heads of 128, bf16, take 1% longer with two heads a thread than with
+  // three, 27% with one (four leave registers for fewer warps: 0.3%, heads of 256 2%); fp32 8% longer
+  // with one than with two.
   const int64_t rows = (int64_t)args.num_tokens * (args.num_heads + args.num_kv_heads);
   if (rows * (D / 16) <= 2048ll * num_sms) return launch_heads<T, D, 1>(p, stream);
   return launch_heads<T, D, sizeof(T) == 2 ? 3 : 2>(p, stream);
