@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(256) block_weights_kernel(const Int8DecodePara
       my_s = (unsigned)mine / width;
       my_b = (int)((unsigned)mine - my_s * width);
       my_len = p.seq_lens[my_s];
-      const int last = (my_len - 1) >> l2bs;
-      there = !(state.x | state.y) && my_len > 0 && last < p.max_blocks_per_seq && my_b <= last;
+      there = !(state.x | state.y) && my_len > 0 && (my_len - 1) >> l2bs < p.max_blocks_per_seq &&
+              my_b <= (my_len - 1) >> l2bs;
     }
     for (uint32_t left = __ballot_sync(0xffffffffu, there); left; left &= left - 1) {
       const int i = __ffs(left) - 1;
